@@ -34,3 +34,13 @@ from .binding import (  # noqa: F401
     w48_group_acc,
     w48_packed_bytes,
 )
+from .paged import (  # noqa: F401
+    PagedCache,
+    cache_evict,
+    cache_evict_workspace,
+    paged_attention,
+    paged_attention_workspace,
+    rope,
+    rope_append,
+    rope_table,
+)

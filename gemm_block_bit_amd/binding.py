@@ -31,6 +31,18 @@ _lib = None
 _lock = threading.Lock()
 
 _vp, _sz, _i, _u = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint
+_l, _f, _d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+
+
+class _RopeScaling(ctypes.Structure):   # gbb_rope_scaling
+    _fields_ = [("kind", _i), ("factor", _d), ("original_len", _d), ("low", _d), ("high", _d), ("attention", _d)]
+
+
+class _PagedCache(ctypes.Structure):    # gbb_paged_cache
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("weights", _vp), ("positions", _vp),
+                ("dtype", _i), ("num_pages", _i), ("page", _i), ("kv_heads", _i), ("head_dim", _i)]
+
+
 _SIGS = {
     "gbb_last_error": (ctypes.c_char_p, []),
     "gbb_version": (_i, []),
@@ -66,6 +78,13 @@ _SIGS = {
     "gbb_gemm_w48a8_workspace": (_sz, [_i, _i, _i, _i, _i]),
     "gbb_gemm_w48a8_split": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp, _sz, _vp]),
     "gbb_w48_group_acc": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _i, _vp]),
+    "gbb_rope_table": (_i, [_i, _i, _d, _vp, _vp]),
+    "gbb_rope": (_i, [_vp, _l, _l, _vp, _l, _l, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "gbb_rope_append": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+    "gbb_paged_attention_workspace": (_sz, [_vp, _i, _i, _i, _i]),
+    "gbb_paged_attention": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _i, _vp, _i, _f, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "gbb_cache_evict_workspace": (_sz, [_vp, _i, _i, _i]),
+    "gbb_cache_evict": (_i, [_vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 EXPORTS = tuple(_SIGS)
 

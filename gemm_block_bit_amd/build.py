@@ -28,7 +28,8 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-Wall",
 CXX_FLAGS = ["-O2", "-Wall", "-Wextra", "-fno-fast-math"] + COMMON
 
 # graph.cpp is host code on the HIP runtime (stream capture), so hipcc builds it too
-HIP_SOURCES = ["decode.hip", "decode64.hip", "prefill.hip", "w48.hip", "debug.hip", "noalloc.hip", "graph.cpp"]
+HIP_SOURCES = ["decode.hip", "decode64.hip", "prefill.hip", "w48.hip", "debug.hip", "noalloc.hip", "graph.cpp",
+               "rope.hip", "attention.hip", "evict.hip"]
 # per-source extra flags: the decode kernel reads its MFMA results with VALU
 # code right away, so it keeps them in VGPRs rather than accumulation
 # registers; its single-token kernel takes its arguments preloaded into
@@ -38,7 +39,7 @@ HIP_EXTRA = {"decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form", "-mllvm", "-amdg
              # the W4.4A8 kernels scale their int32 MFMA results with VALU code
              # right away too, so they also keep them in VGPRs
              "w48.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
-CXX_SOURCES = ["pack.cpp", "api.cpp"]
+CXX_SOURCES = ["pack.cpp", "api.cpp", "rope_table.cpp", "cache.cpp"]
 
 
 def _run(cmd):

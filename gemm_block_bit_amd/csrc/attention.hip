@@ -1,0 +1,530 @@
+// Attention of one new token per sequence over a paged cache
+// (gbb_paged_attention), split over the cache's length and joined.
+//
+// For a kv head with G query heads the work is two thin products and a
+// softmax, o = softmax(scale q K^T) V with q [G][D]: 4 G D operations a slot
+// against 2 D elements read, so with G <= 16 the cache's bytes bound it and
+// the matrix cores, at 16 query rows a tile, have room to spare.
+//
+// Layout of the work.  A workgroup (4 waves) takes one run of `chunk` slots
+// of one (sequence, kv head); its waves take tiles of 32 slots in turn.  No
+// operand goes through LDS and no lane needs another lane's data:
+//  - S^T = K q^T: the A operand of a 16x16x32 MFMA is 16 slots x 32 elements
+//    of K, for which a lane loads 16 bytes of "its" slot's row; the result
+//    has lane c + 16 g holding query head c, slots 4 g ... 4 g + 3.
+//  - O^T = V^T P: the contraction runs over slots, and which slot a k index
+//    stands for is free as long as both operands agree.  So P's registers
+//    are the B operand as they are, and a lane of the A operand needs
+//    elements of V at the slots 4 g ... 4 g + 3: it loads 16 bytes of those
+//    four rows (16 lanes side by side take a whole row) and byte permutes
+//    within the lane pair them up.  Output row c of tile j is element
+//    EV c + j of the head.
+//  - the running maximum is per query head, hence the same in the 4 lanes
+//    that share c (two lane exchanges a tile); sums stay per lane to the end.
+// P is rounded to 16 bits for the matrix cores; what the rounding drops is
+// multiplied too, as a second operand, so a product carries about 22 (fp16)
+// or 16 (bf16) bits of P and the output's own rounding is what is left.
+// exp2 is taken 14 powers above the running maximum's 0, so that fp16 keeps
+// small probabilities out of its subnormals; the sums carry the same factor.
+//
+// The partial results of a sequence with several runs (maximum, sum and
+// unnormalised output, fp32) go to the workspace and a second launch joins
+// them.  With weights, the first launch also stores the scores, and the
+// second adds exp(s - max) / sum over the kv head's query heads, one thread
+// a slot, without atomics.
+#include <algorithm>
+
+#include "device.h"
+#include "internal.h"
+
+namespace gbb {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kShift = 14.f;   // see above: 2^14 < 65504
+constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles x 4 waves x 32 slots
+
+
+// 16-bit element types of q, P and out.
+template <int DT> struct Half;
+template <> struct Half<GBB_F16> {
+  typedef _Float16 T;
+  typedef half8 V8;
+  static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  // two e4m3 bytes (the low or the high pair of w) as two elements, exactly
+  template <bool HI> static __device__ __forceinline__ uint32_t widen(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, HI));
+  }
+};
+template <> struct Half<GBB_BF16> {
+  typedef __bf16 T;
+  typedef bf16x8 V8;
+  static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI> static __device__ __forceinline__ uint32_t widen(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, HI));
+  }
+};
+
+struct SplitArgs {
+  const void* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* lengths;
+  const float* weights;
+  float* weights_out;
+  void* out;
+  float* lse;
+  float2* ml;       // [B][Hkv][nsplit][G] maximum (log2 domain) and sum
+  float* o;         // [B][Hkv][nsplit][G][D]
+  float* scores;    // [B][Hkv][G][score_stride], log2 domain
+  size_t score_stride;
+  int64_t q_token;
+  int B, Hq, Hkv, G, qtiles, num_pages, pshift, max_pages, max_len, chunk, nsplit;
+  float scale;      // scale * log2(e)
+};
+
+__device__ __forceinline__ int length_of(const SplitArgs& a, int b) {
+  return max(0, min(a.lengths[b], a.max_len));
+}
+// 2^(x - m) with 2^(-inf - -inf) = 0, for joining partial results
+__device__ __forceinline__ float rescale(float x, float m) {
+  return x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - m);
+}
+
+template <int DT, int CT, int D, bool WT>
+__global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void split_kernel(SplitArgs a) {
+  typedef Half<DT> H;
+  typedef typename H::V8 V8;
+  constexpr bool F8 = CT == GBB_E4M3;
+  constexpr int ES = F8 ? 1 : 2, ROW = D * ES;
+  constexpr int KP = ROW / 64;                       // 16-byte loads a lane and 16 slots of K
+  constexpr int VB = ROW / 16 < 16 ? ROW / 16 : 16;  // bytes a lane loads at once of a row of V
+  constexpr int VW = VB / 4, NV = ROW / 16 / VB, EV = VB / ES;
+  constexpr int NT = D / 16;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int c = lane & 15, g4 = lane >> 4;
+  int id = blockIdx.x;
+  const int sp = id % a.nsplit;
+  id /= a.nsplit;
+  const int qt = id % a.qtiles;
+  id /= a.qtiles;
+  const int hk = id % a.Hkv, b = id / a.Hkv;
+  const int len = length_of(a, b);
+  const int rows = min(16, a.G - 16 * qt);           // query heads of this tile
+  const int hq0 = hk * a.G + 16 * qt;
+  const int k0 = sp * a.chunk;
+  if (k0 >= len) {
+    if (sp == 0) {                                   // an empty sequence
+      for (int i = threadIdx.x; i < rows * D; i += 256)
+        static_cast<typename H::T*>(a.out)[(size_t(b) * a.Hq + hq0) * D + i] = typename H::T(0.f);
+      if (a.lse && threadIdx.x < rows) a.lse[size_t(b) * a.Hq + hq0 + threadIdx.x] = -INFINITY;
+    }
+    return;
+  }
+  const int k1 = min(len, k0 + a.chunk);
+  const int ntile = (k1 - k0 + 31) >> 5;
+  const int n = (ntile - wave + 3) >> 2;             // tiles of this wave: wave, wave + 4, ...
+  // lane 2 i + s holds the page of 16-slot half s of this wave's tile i
+  int page = -1;
+  {
+    const int key = k0 + 32 * (wave + 4 * (lane >> 1)) + 16 * (lane & 1);
+    if (key < k1) page = a.block_table[size_t(b) * a.max_pages + (key >> a.pshift)];
+    if (unsigned(page) >= unsigned(a.num_pages)) page = -1;
+  }
+  V8 qf[D / 32];
+#pragma unroll
+  for (int kc = 0; kc < D / 32; ++kc) {
+    const int d = F8 ? 64 * (kc >> 1) + 16 * g4 + 8 * (kc & 1) : 32 * kc + 8 * g4;
+    u32x4 z = {0, 0, 0, 0};
+    if (c < rows) z = ld16(static_cast<const uint16_t*>(a.q) + b * a.q_token + size_t(hq0 + c) * D + d);
+    qf[kc] = __builtin_bit_cast(V8, z);
+  }
+  const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
+
+  f32x4 o[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) o[i] = f32x4{0, 0, 0, 0};
+  float m = -INFINITY, l = 0.f;
+  const int pmask = (1 << a.pshift) - 1;
+  const size_t page_bytes = (size_t(1) << a.pshift) * ROW;
+
+  struct Tile {
+    u32x4 k[2][KP];
+    uint32_t v[2][4][NV][VW];
+  };
+  // Pages hold whole 16-slot halves, so a half's rows are always memory of
+  // the cache; a page that is not there is read as page 0 and masked.
+  auto load = [&](Tile& t, int i) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int p = max(0, __builtin_amdgcn_readlane(page, 2 * i + s));
+      const int key = k0 + 32 * (wave + 4 * i) + 16 * s;
+      const size_t off = (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * ROW;
+      const uint8_t* kb = a.k + off + c * ROW + g4 * 16;
+      const uint8_t* vb = a.v + off + 4 * g4 * ROW + c * VB;
+#pragma unroll
+      for (int j = 0; j < KP; ++j) t.k[s][j] = ld16(kb + 64 * j);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          const uint8_t* p2 = vb + r * ROW + u * 256;
+          if constexpr (VW == 4) {
+            const u32x4 x = ld16(p2);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) t.v[s][r][u][w] = x[w];
+          } else if constexpr (VW == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p2);
+            t.v[s][r][u][0] = x.x;
+            t.v[s][r][u][1] = x.y;
+          } else {
+            t.v[s][r][u][0] = *reinterpret_cast<const uint32_t*>(p2);
+          }
+        }
+    }
+  };
+  auto compute = [&](Tile& t, int i) {
+    const int key0 = k0 + 32 * (wave + 4 * i);
+    f32x4 s[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s[e] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        if constexpr (F8) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w0 = t.k[e][j][2 * h], w1 = t.k[e][j][2 * h + 1];
+            const u32x4 x = {H::template widen<false>(w0), H::template widen<true>(w0),
+                             H::template widen<false>(w1), H::template widen<true>(w1)};
+            s[e] = H::mfma(__builtin_bit_cast(V8, x), qf[2 * j + h], s[e]);
+          }
+        } else {
+          s[e] = H::mfma(__builtin_bit_cast(V8, t.k[e][j]), qf[j], s[e]);
+        }
+      }
+      s[e] *= scale;
+    }
+    // a tile that the length or a missing page cuts: those slots take no
+    // part, and whatever their memory holds must not reach the product
+    const int p0 = __builtin_amdgcn_readlane(page, 2 * i), p1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
+    if (key0 + 32 > k1 || (p0 | p1) < 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (key0 + 16 * e + 4 * g4 + r >= k1 || (e ? p1 : p0) < 0) {
+            s[e][r] = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) t.v[e][r][u][w] = 0;
+          }
+    }
+    if constexpr (WT) {
+      if (c < rows) {
+        float* sc = a.scores + (size_t(b) * a.Hq + hq0 + c) * a.score_stride + key0 + 4 * g4;
+        *reinterpret_cast<f32x4*>(sc) = s[0];
+        *reinterpret_cast<f32x4*>(sc + 16) = s[1];
+      }
+    }
+    float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx), f = rescale(m, mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) o[j] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.f : m - kShift;
+    V8 ph, pl;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = __builtin_amdgcn_exp2f(s[e][r] - ref);
+        l += p;
+        const typename H::T h = typename H::T(p);
+        ph[4 * e + r] = h;
+        pl[4 * e + r] = typename H::T(p - float(h));
+      }
+    auto product = [&](int tile, const u32x4& x) {
+      o[tile] = H::mfma(__builtin_bit_cast(V8, x), ph, o[tile]);
+      o[tile] = H::mfma(__builtin_bit_cast(V8, x), pl, o[tile]);
+    };
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        // word w of the four rows of both halves: elements EV c + (w's) of them
+        if constexpr (F8) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x07030602u : 0x05010400u;   // (a, b) -> a0 b0 a1 b1 of two rows' words
+            uint32_t x[2][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                x[e][r] = __builtin_amdgcn_perm(t.v[e][2 * r + 1][u][w], t.v[e][2 * r][u][w], sel);
+            product(u * EV + 4 * w + 2 * h,
+                    u32x4{H::template widen<false>(x[0][0]), H::template widen<false>(x[0][1]),
+                          H::template widen<false>(x[1][0]), H::template widen<false>(x[1][1])});
+            product(u * EV + 4 * w + 2 * h + 1,
+                    u32x4{H::template widen<true>(x[0][0]), H::template widen<true>(x[0][1]),
+                          H::template widen<true>(x[1][0]), H::template widen<true>(x[1][1])});
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x07060302u : 0x05040100u;
+            product(u * EV + 2 * w + h,
+                    u32x4{__builtin_amdgcn_perm(t.v[0][1][u][w], t.v[0][0][u][w], sel),
+                          __builtin_amdgcn_perm(t.v[0][3][u][w], t.v[0][2][u][w], sel),
+                          __builtin_amdgcn_perm(t.v[1][1][u][w], t.v[1][0][u][w], sel),
+                          __builtin_amdgcn_perm(t.v[1][3][u][w], t.v[1][2][u][w], sel)});
+          }
+        }
+      }
+  };
+  Tile t0, t1;
+  if (n > 0) {
+    load(t0, 0);
+    int i = 0;
+    for (; i + 2 <= n; i += 2) {
+      load(t1, i + 1);
+      compute(t0, i);
+      if (i + 2 < n) load(t0, i + 2);
+      compute(t1, i + 1);
+    }
+    if (i < n) compute(t0, i);
+  }
+
+  // join the four waves
+  __shared__ float sm[4][16], sl[4][16];
+  __shared__ float so[4][16][D + 4];
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g4 == 0) {
+    sm[wave][c] = m;
+    sl[wave][c] = l;
+  }
+  if (c < rows) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) so[wave][c][(t / EV) * 16 * EV + EV * (4 * g4 + r) + t % EV] = o[t][r];
+  }
+  __syncthreads();
+  const bool whole = len <= a.chunk;
+  const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+  for (int i = threadIdx.x; i < rows * D; i += 256) {
+    const int q = i / D, d = i % D;
+    const float mm = fmaxf(fmaxf(sm[0][q], sm[1][q]), fmaxf(sm[2][q], sm[3][q]));
+    float ll = 0.f, oo = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = rescale(sm[w][q], mm);
+      ll += f * sl[w][q];
+      oo += f * so[w][q][d];
+    }
+    const size_t row = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt + q;
+    if (whole) {
+      const size_t head = size_t(b) * a.Hq + hq0 + q;
+      static_cast<typename H::T*>(a.out)[head * D + d] = typename H::T(ll == 0.f ? 0.f : oo / ll * vs);
+      if (d == 0 && a.lse) a.lse[head] = ll == 0.f ? -INFINITY : (mm - kShift + __builtin_amdgcn_logf(ll)) * kLn2;
+      if (WT && d == 0) a.ml[row] = make_float2(mm, ll);
+    } else {
+      a.o[row * D + d] = oo;
+      if (d == 0) a.ml[row] = make_float2(mm, ll);
+    }
+  }
+}
+
+// Maximum and sum of a query head over its runs, the same in all 64 lanes.
+__device__ __forceinline__ float2 join_sums(const float2* ml, int ns, int G, int lane) {
+  float mm = -INFINITY, ll = 0.f;
+  for (int i = lane; i < ns; i += 64) mm = fmaxf(mm, ml[size_t(i) * G].x);
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) mm = fmaxf(mm, __shfl_xor(mm, x));
+  for (int i = lane; i < ns; i += 64) {
+    const float2 e = ml[size_t(i) * G];
+    ll += rescale(e.x, mm) * e.y;
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) ll += __shfl_xor(ll, x);
+  return make_float2(mm, ll);
+}
+
+// Joins the runs of every (sequence, query head) in the first `heads`
+// workgroups; the others (with weights) take 256 slots of a (sequence, kv
+// head) each.
+template <int DT, bool F8, int D, bool WT>
+__global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
+  typedef Half<DT> H;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  if (int(blockIdx.x) < heads) {
+    const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
+    const int hk = hq / a.G, q = hq % a.G;
+    const int len = length_of(a, b);
+    if (len <= a.chunk) return;
+    const int ns = (len + a.chunk - 1) / a.chunk;
+    const size_t row = size_t(b * a.Hkv + hk) * a.nsplit * a.G + q;
+    const float2* ml = a.ml + row;
+    const float2 e = join_sums(ml, ns, a.G, lane);
+    constexpr int TR = D / 4, NR = 256 / TR;   // threads a row, rows at once
+    const int r0 = threadIdx.x / TR, d = 4 * (threadIdx.x % TR);
+    f32x4 acc = {0, 0, 0, 0};
+    for (int i = r0; i < ns; i += NR) {
+      const float f = rescale(ml[size_t(i) * a.G].x, e.x);
+      acc += f * *reinterpret_cast<const f32x4*>(a.o + (row + size_t(i) * a.G) * D + d);
+    }
+    __shared__ f32x4 part[NR][TR];
+    part[r0][threadIdx.x % TR] = acc;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float oo = 0.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) oo += part[r][threadIdx.x / 4][threadIdx.x % 4];
+      const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+      const size_t head = size_t(b) * a.Hq + hq;
+      static_cast<typename H::T*>(a.out)[head * D + threadIdx.x] = typename H::T(e.y == 0.f ? 0.f : oo / e.y * vs);
+      if (threadIdx.x == 0 && a.lse)
+        a.lse[head] = e.y == 0.f ? -INFINITY : (e.x - kShift + __builtin_amdgcn_logf(e.y)) * kLn2;
+    }
+    return;
+  }
+  if constexpr (WT) {
+    const int nb = (a.max_len + 255) / 256;
+    int id = blockIdx.x - heads;
+    const int j0 = (id % nb) * 256;
+    id /= nb;
+    const int hk = id % a.Hkv, b = id / a.Hkv;
+    const int len = length_of(a, b);
+    if (j0 >= len) return;
+    const int ns = (len + a.chunk - 1) / a.chunk;
+    // per query head: what is taken off a score, and one over the sum
+    __shared__ float ref[kMaxGroup], inv[kMaxGroup];
+    for (int q = wave; q < a.G; q += 4) {
+      const float2 e = join_sums(a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G + q, ns, a.G, lane);
+      if (lane == 0) {
+        ref[q] = e.x == -INFINITY ? 0.f : e.x - kShift;
+        inv[q] = e.y == 0.f ? 0.f : 1.f / e.y;
+      }
+    }
+    __syncthreads();
+    const int j = j0 + threadIdx.x;
+    if (j >= len) return;
+    const int p = a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)];
+    if (unsigned(p) >= unsigned(a.num_pages)) return;
+    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + j;
+    float w = 0.f;
+    for (int q = 0; q < a.G; ++q) w += __builtin_amdgcn_exp2f(s[q * a.score_stride] - ref[q]) * inv[q];
+    const size_t at = ((size_t(p) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
+    a.weights_out[at] = a.weights[at] + w;
+  }
+}
+
+template <int DT, int CT, int D>
+void run(const SplitArgs& a, bool wt, hipStream_t s) {
+  const unsigned grid = unsigned(a.B) * a.Hkv * a.qtiles * a.nsplit;
+  if (wt) hipLaunchKernelGGL((split_kernel<DT, CT, D, true>), dim3(grid), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((split_kernel<DT, CT, D, false>), dim3(grid), dim3(256), 0, s, a);
+  const int heads = a.nsplit > 1 ? a.B * a.Hq : 0;
+  constexpr bool F8 = CT == GBB_E4M3;
+  if (wt) {
+    const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + 255) / 256);
+    hipLaunchKernelGGL((join_kernel<DT, F8, D, true>), dim3(unsigned(heads) + more), dim3(256), 0, s, a, heads);
+  } else if (heads) {
+    hipLaunchKernelGGL((join_kernel<DT, F8, D, false>), dim3(unsigned(heads)), dim3(256), 0, s, a, heads);
+  }
+}
+template <int DT, int CT>
+void run_dim(const SplitArgs& a, int D, bool wt, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, wt, s);
+  else if (D == 128) run<DT, CT, 128>(a, wt, s);
+  else run<DT, CT, 256>(a, wt, s);
+}
+
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace
+
+AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights) {
+  AttendPlan p;
+  const int G = Hq / c.kv_heads;
+  p.qtiles = (G + 15) / 16;
+  const int64_t pairs = int64_t(B) * c.kv_heads * p.qtiles;
+  // the longest run that still gives two workgroups a CU (the register
+  // budget's residency); short contexts end at runs of one tile a wave
+  int chunk = kMaxChunk;
+  while (chunk > 128 && pairs * ((max_len + chunk - 1) / chunk) < 2 * int64_t(device_compute_units())) chunk /= 2;
+  p.chunk = chunk;
+  p.nsplit = std::max(1, (max_len + chunk - 1) / chunk);
+  const size_t rows = size_t(B) * Hq * p.nsplit;
+  p.score_stride = (size_t(max_len) + 31) & ~size_t(31);
+  const bool parts = p.nsplit > 1;
+  p.ml_off = 0;
+  p.o_off = parts || with_weights ? up(rows * sizeof(float2)) : 0;
+  p.s_off = p.o_off + (parts ? up(rows * c.head_dim * sizeof(float)) : 0);
+  p.ws_bytes = p.s_off + (with_weights ? up(size_t(B) * Hq * p.score_stride * sizeof(float)) : 0);
+  return p;
+}
+
+int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPlan& p, void* stream) {
+  SplitArgs a;
+  a.q = x.q;
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.block_table = x.block_table;
+  a.lengths = x.lengths;
+  a.weights = c.weights;
+  a.weights_out = x.weights_out;
+  a.out = x.out;
+  a.lse = x.lse;
+  a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
+  a.o = reinterpret_cast<float*>(x.ws + p.o_off);
+  a.scores = reinterpret_cast<float*>(x.ws + p.s_off);
+  a.score_stride = p.score_stride;
+  a.q_token = x.q_token;
+  a.B = x.B;
+  a.Hq = x.Hq;
+  a.Hkv = c.kv_heads;
+  a.G = x.Hq / c.kv_heads;
+  a.qtiles = p.qtiles;
+  a.num_pages = c.num_pages;
+  a.pshift = __builtin_ctz(unsigned(c.page));
+  a.max_pages = x.max_pages;
+  a.max_len = x.max_len;
+  a.chunk = p.chunk;
+  a.nsplit = p.nsplit;
+  a.scale = x.scale * kLog2e;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool wt = x.weights_out != nullptr;
+  if (x.dtype == GBB_F16) {
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, wt, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, wt, s);
+  } else {
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, wt, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, wt, s);
+  }
+  return int(hipGetLastError());
+}
+
+}  // namespace gbb

@@ -106,6 +106,69 @@ int launch_w48(const W48ImageView& im, const int8_t* xq, const uint16_t* xs, int
                int M, void* workspace, size_t ws_bytes, void* stream);
 int launch_w48_acc(const W48ImageView& im, const int8_t* xq, int ga, int32_t* acc, int M, void* stream);
 
+// ---- the decoding step's attention (rope.hip, attention.hip, evict.hip) ------
+// Arguments are checked by cache.cpp; the launchers only plan and launch.
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int64_t x_token, x_head, y_token, y_head;
+  const int32_t* positions;
+  const float* table;
+  int T, H, D, n_pos, rot, layout, transpose, dtype;
+};
+int launch_rope(const RopeArgs& a, void* stream);
+
+struct AppendArgs {
+  const void* qkv;
+  void* q;
+  int64_t token_stride;
+  const int32_t* positions;
+  const int32_t* slots;
+  const float* table;
+  int T, Hq, n_pos, rot, layout, dtype;
+};
+int launch_append(const gbb_paged_cache& c, const AppendArgs& a, void* stream);
+
+// The split of gbb_paged_attention: every sequence's slots in runs of `chunk`
+// (nsplit of them up to max_len), one workgroup each.
+constexpr int kMaxGroup = 128;   // query heads per kv head
+struct AttendPlan {
+  int chunk, nsplit, qtiles;
+  size_t ml_off, o_off, s_off, ws_bytes;   // workspace sections
+  size_t score_stride;                     // scores per query head (with weights)
+};
+AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights);
+struct AttendArgs {
+  const void* q;
+  int64_t q_token;
+  const int32_t* block_table;
+  const int32_t* lengths;
+  void* out;
+  float* lse;
+  float* weights_out;
+  char* ws;
+  int B, Hq, max_pages, max_len, dtype;
+  float scale;
+};
+int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPlan& p, void* stream);
+
+struct EvictPlan {
+  size_t key_stride;    // ranking keys per (sequence, kv head)
+  size_t most;          // rows that can move per (sequence, kv head)
+  size_t count_off, dst_off, src_off, key_off, ws_bytes;
+};
+EvictPlan evict_plan(const gbb_paged_cache& c, int B, int max_len, int budget);
+struct EvictArgs {
+  const int32_t* block_table;
+  const int32_t* lengths;
+  int32_t* lengths_out;
+  float* weights_out;
+  int32_t* positions_out;
+  char* ws;
+  int B, max_pages, max_len, budget, recent;
+};
+int launch_evict(const gbb_paged_cache& c, const EvictArgs& a, const EvictPlan& p, void* stream);
+
 // Returns a message for a HIP error code, or nullptr for success.
 const char* device_error_text(int err);
 

@@ -397,6 +397,184 @@ gbb_status gbb_gemm_w48a8_split(const void* image, int N, int K, int n8, const i
 gbb_status gbb_w48_group_acc(const void* image, int N, int K, int n8, const int8_t* xq, int ga,
                              int32_t* acc, int M, void* stream);
 
+/* ======================================================================== */
+/* The rest of a decoding step's attention: rotary positions, a paged       */
+/* key-value cache, attention of one new token over it, and eviction        */
+/* ======================================================================== */
+
+/* Element types (the values of every `dtype` argument below). */
+enum {
+  GBB_F16 = 0,    /* IEEE binary16 */
+  GBB_BF16 = 1,   /* bfloat16 */
+  GBB_F32 = 2,    /* IEEE binary32 (gbb_rope only) */
+  GBB_E4M3 = 3    /* OCP 8-bit e4m3 without infinities, largest 448 (caches only) */
+};
+
+/* How a rotated head pairs its first `rot` elements. */
+enum {
+  GBB_ROPE_HALF = 0,          /* (i, i + rot/2) */
+  GBB_ROPE_INTERLEAVED = 1    /* (2i, 2i + 1) */
+};
+
+/* Scalings of the rotary frequencies f_i = base^(-2i/rot) for contexts
+ * longer than the model's own (F = factor, L = original_len). */
+enum {
+  GBB_ROPE_PLAIN = 0,    /* f_i */
+  GBB_ROPE_LINEAR = 1,   /* f_i / F */
+  GBB_ROPE_BANDS = 2,    /* by the wave length w = 2 pi / f_i: f_i where w < L / high, f_i / F where
+                            w > L / low, else (1 - t) f_i / F + t f_i with t = (L / w - low) / (high - low) */
+  GBB_ROPE_YARN = 3      /* by the pair's index ("YaRN: Efficient Context Window Extension of Large Language
+                            Models"): with d(r) = rot ln(L / (2 pi r)) / (2 ln base), a = max(floor(d(high)), 0),
+                            b = min(ceil(d(low)), rot - 1) and t = clamp((i - a) / max(b - a, 0.001), 0, 1):
+                            (1 - t) f_i + t f_i / F */
+};
+
+typedef struct {
+  int kind;              /* GBB_ROPE_PLAIN ... GBB_ROPE_YARN */
+  double factor;         /* F >= 1; ignored by PLAIN */
+  double original_len;   /* L > 0; BANDS and YARN */
+  double low, high;      /* BANDS: 0 < low < high (wave lengths per L); YARN: turns per L, 0 < low < high */
+  double attention;      /* multiplies every cos and sin (1: none); finite and not 0 */
+} gbb_rope_scaling;
+
+/* Table of rotations (host, synchronous, may use several CPU threads):
+ * table[p][i] = (cos(p f_i), sin(p f_i)) * attention for p < n_pos and
+ * i < rot/2, each computed in double and rounded once; float
+ * [n_pos][rot/2][2].  scaling NULL is PLAIN with attention 1.
+ * Errors: GBB_E_ARG (NULL, rot odd or not positive, n_pos <= 0, base not
+ * above 1, a scaling outside the ranges above). */
+gbb_status gbb_rope_table(int rot, int n_pos, double base, const gbb_rope_scaling* scaling, float* table);
+
+/* Rotary positions: for every token t < T and head h < H, pair i of the
+ * head's first `rot` elements (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s)
+ * with (c, s) = table[positions[t]][i], in fp32 and rounded once; elements
+ * rot ... D - 1 are copied.  transpose != 0 takes -s for s: the transposed
+ * map, which is the gradient with respect to x of a call without it (and,
+ * for a table with attention 1, its inverse).
+ *   x, y       device, `dtype` GBB_F16, GBB_BF16 or GBB_F32: element d of
+ *              head h of token t is at t * token stride + h * head stride
+ *              + d (strides in elements, 16-byte alignment not required).
+ *              y == x with equal strides works in place; otherwise x and y
+ *              must not overlap.
+ *   positions  device int32 [T]; table device float [n_pos][rot/2][2].  A
+ *              token whose position is outside [0, n_pos) is padding: its
+ *              y is zero.
+ * T = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE (D odd or above 1024,
+ * rot odd, below 2 or above D, heads of a token that overlap), GBB_E_ALIGN
+ * (a pointer that is not aligned to its element), GBB_E_DEVICE. */
+gbb_status gbb_rope(const void* x, int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head,
+                    int dtype, int T, int H, int D, const int32_t* positions, const float* table, int n_pos,
+                    int rot, int layout, int transpose, void* stream);
+
+/* A paged cache of keys and values.  Slot s is token s % page of page
+ * s / page.  All pointers are device memory that the caller owns. */
+typedef struct {
+  void* k;                /* [num_pages][kv_heads][page][head_dim], dtype */
+  void* v;                /* the same shape and dtype */
+  const float* k_scale;   /* [kv_heads], GBB_E4M3 only: an element stands for its value times this */
+  const float* v_scale;   /* (NULL: 1; finite and above 0, which is not checked) */
+  float* weights;         /* [num_pages][kv_heads][page] attention weight that a slot gathered, or NULL */
+  int32_t* positions;     /* [num_pages][kv_heads][page] position of a slot's token, or NULL */
+  int dtype;              /* GBB_F16, GBB_BF16 or GBB_E4M3 */
+  int num_pages;          /* num_pages * page < 2^31 */
+  int page;               /* 16, 32, 64, 128 or 256 tokens */
+  int kv_heads;
+  int head_dim;           /* 64, 128 or 256 */
+} gbb_paged_cache;
+
+/* Rotary positions of a fused q|k|v product's output, with k and v written
+ * to the cache in the same pass.
+ *   qkv        device [T][token_stride], dtype GBB_F16 or GBB_BF16: q_heads
+ *              query heads, then the cache's kv_heads key heads, then as
+ *              many value heads, head_dim elements each.
+ *   positions, table, n_pos, rot, layout  as gbb_rope.
+ *   slots      device int32 [T]: the cache slot of each token.  Two tokens
+ *              of a call must not name the same slot.
+ *   q          device [T][q_heads][head_dim]: the rotated query heads.
+ *   cache      k (rotated) and v; its dtype is that of qkv, or GBB_E4M3:
+ *              then an element is value / scale (fp32), clamped to +-448
+ *              and rounded to nearest even.  A NaN stays one.
+ *              Where the cache has them, positions[slot] = the token's
+ *              position and weights[slot] = 0 for every kv head.
+ * A token whose position is outside [0, n_pos) or whose slot is outside the
+ * cache is padding: its q is zero and it is not written to the cache.
+ * T = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN (qkv, q,
+ * k, v and table 16-byte aligned, token_stride a multiple of 8),
+ * GBB_E_DEVICE. */
+gbb_status gbb_rope_append(const gbb_paged_cache* cache, const void* qkv, int64_t token_stride, int dtype, int T,
+                           int q_heads, const int32_t* positions, const int32_t* slots, const float* table,
+                           int n_pos, int rot, int layout, void* q, void* stream);
+
+/* Bytes of workspace of gbb_paged_attention (0 on a bad argument or where
+ * none is needed).  It must be zero before its first use; every call leaves
+ * it ready for the next one of any size, but not zero: it must not be shared
+ * with calls that want a zero workspace (gbb_gemm_*). */
+size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_heads, int max_len, int with_weights);
+
+/* Attention of one new token per sequence over the cache:
+ * for query head h of sequence b, with kv head h / (q_heads / kv_heads) and
+ * s_j = scale * (q . k_j) over the slots j < lengths[b] of the sequence,
+ * out = sum_j p_j v_j, p_j = exp(s_j) / sum_j exp(s_j); fp32 sums, one
+ * rounding of out.  A sequence of length 0 gives zeros (so does a head
+ * whose scores are all -inf).  Memory past the length is never used, so it
+ * may hold anything, NaN included.
+ *   q, out     device [B][q_heads][head_dim] of `dtype` (GBB_F16 or
+ *              GBB_BF16; the cache's dtype or a GBB_E4M3 cache); sequence b
+ *              of q is at b * q_token elements.
+ *   block_table device int32 [B][max_pages]: slot j of sequence b is token
+ *              j % page of page block_table[b][j / page].  An entry outside
+ *              [0, num_pages) is a page that is not there: its slots take no
+ *              part.
+ *   lengths    device int32 [B], at most max_len (larger ones are taken as
+ *              max_len, negative ones as 0).
+ *   max_len    an upper bound on the lengths, at most max_pages * page.  The
+ *              split over the length is planned for it.
+ *   lse        NULL, or device float [B][q_heads]: log(sum_j exp(s_j)), -inf
+ *              for an empty sequence: what joining the outputs over parts of
+ *              a context takes.
+ *   weights_out NULL, or like the cache's weights (which must be there, and
+ *              may be the same memory): for every slot j < lengths[b] the
+ *              cache's weight plus the sum of p_j over the kv head's query
+ *              heads.  Other slots are not written.  No atomics: results do
+ *              not depend on the order of execution.  Two sequences of a
+ *              call must not share a page then.
+ *   workspace  16-byte aligned, of gbb_paged_attention_workspace bytes.
+ * B = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN,
+ * GBB_E_SPACE, GBB_E_DEVICE. */
+gbb_status gbb_paged_attention(const gbb_paged_cache* cache, const void* q, int64_t q_token, int dtype, int B,
+                               int q_heads, const int32_t* block_table, int max_pages, const int32_t* lengths,
+                               int max_len, float scale, void* out, float* lse, float* weights_out,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of gbb_cache_evict (0 on a bad argument).  Its contents
+ * need no initialisation. */
+size_t gbb_cache_evict_workspace(const gbb_paged_cache* cache, int B, int max_len, int budget);
+
+/* Eviction by accumulated attention weight.  For every sequence b and kv
+ * head with lengths[b] > budget, `budget` of the first lengths[b] slots are
+ * kept: first those whose position is above (the largest position among
+ * them) - recent, then those of the largest weight (a NaN ranks below
+ * everything, -0 as 0); ties go to the lower slot.  Kept slots below budget
+ * stay where they are; the i-th dropped slot below budget takes k, v, weight
+ * and position of the i-th kept slot from budget on.  So slots are in no
+ * order afterwards, which attention over rotated keys does not need, and no
+ * more rows move than have to.
+ *   lengths_out device int32 [B], not overlapping lengths: min(lengths[b],
+ *              budget).
+ *   weights_out, positions_out  like the cache's weights and positions
+ *              (both must be there), and may be the same memory; in other
+ *              memory, all slots below lengths[b] are written.  Slots from
+ *              the new length up to lengths[b] get weight 0 and position -1.
+ *   0 <= recent <= budget, 1 <= budget, 1 <= max_len <= max_pages * page.
+ * k and v change in place.  Two sequences must not share a page.  A sequence
+ * with an entry outside [0, num_pages) among its pages is left as it is.
+ * B = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN,
+ * GBB_E_SPACE, GBB_E_DEVICE. */
+gbb_status gbb_cache_evict(const gbb_paged_cache* cache, int B, const int32_t* block_table, int max_pages,
+                           const int32_t* lengths, int max_len, int budget, int recent, int32_t* lengths_out,
+                           float* weights_out, int32_t* positions_out, void* workspace, size_t ws_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

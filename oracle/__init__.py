@@ -16,6 +16,8 @@ image       an independent reader for the packed block image, written from the
 w48         output-feature mixed W8(sym)/W4(asym) x A8(sym) reference: row
             split, weight and activation quantizers, two-step group GEMM.
 model       the arithmetic-intensity formula of the MixLLM page.
+decode_step rotary positions, paged cache writes, attention of one new token
+            and eviction by accumulated attention weight, in 64 bits.
 alloc       offline bitwidth allocation (batched greedy) and bidirectional
             channel reordering, with a weight-magnitude sensitivity proxy.
 
@@ -25,4 +27,4 @@ that produces the int8 activations); reference products are fp64.
 Every function names the passage it follows.  Functions without an
 independent pin say "parity unpinned" -- none currently.
 """
-from . import alloc, blockquant, image, model, w48  # noqa: F401
+from . import alloc, blockquant, decode_step, image, model, w48  # noqa: F401
