@@ -53,8 +53,9 @@ gbb_status check_cache(const gbb_paged_cache* c) {
   if (int64_t(c->num_pages) * c->page > INT_MAX)
     return fail(GBB_E_SHAPE, "num_pages * page must be below 2^31 (%d * %d)", c->num_pages, c->page);
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(GBB_E_ALIGN, "the cache's k and v must be 16-byte aligned");
-  if (!aligned(c->weights, 4) || !aligned(c->positions, 4) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
-    return fail(GBB_E_ALIGN, "weights, positions or scales are misaligned");
+  if (!aligned(c->weights, 16) || !aligned(c->positions, 16))
+    return fail(GBB_E_ALIGN, "the cache's weights and positions must be 16-byte aligned");
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return fail(GBB_E_ALIGN, "k_scale or v_scale is misaligned");
   return GBB_OK;
 }
 

@@ -9,12 +9,16 @@
 // below it and nothing else moves: 4 bytes of weight and position in and out
 // a slot, and 2 rows read and written a moved slot, are what it takes.
 //
-// The first launch selects, one workgroup a (sequence, kv head): the key of
-// the budget-th slot is found 8 bits at a time from histograms in LDS, then
-// one pass in slot order lists holes and the slots that fill them, and
-// weights and positions follow.  The second launch moves the rows of k and
-// v, over as many workgroups as the rows give.
+// One workgroup of 16 waves selects for a (sequence, kv head): the threads
+// hold the keys in registers, 4 slots to a load (rows above 32768 slots go
+// through the workspace), the budget-th largest is found 11 bits at a time
+// from histograms in LDS, and ranks in slot order are prefix sums of each
+// thread's counts.  Where few rows
+// can move, as in a cache that is one token over its budget, the same
+// workgroup moves them; else a second launch moves rows and writes weights
+// and positions over as many workgroups as the slots give.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "internal.h"
@@ -23,9 +27,10 @@ namespace gbb {
 
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kMaxHeld = 32 * 1024;   // slots a row whose keys a workgroup's registers hold
+constexpr int kFew = 64;              // rows that the selecting workgroup moves itself
 
-struct SelectArgs {
+struct EvictKernelArgs {
   const int32_t* block_table;
   const int32_t* lengths;
   int32_t* lengths_out;
@@ -33,12 +38,17 @@ struct SelectArgs {
   const int32_t* positions;
   float* weights_out;
   int32_t* positions_out;
-  int32_t* count;    // [B Hkv] rows to move
-  int32_t* dst;      // [B Hkv][most] slots, ascending
-  int32_t* src;
-  uint32_t* keys;    // [B Hkv][key_stride]
+  uint8_t* k;
+  uint8_t* v;
+  int32_t* count;    // [B Hkv] rows to move, -1: the sequence is left as it is
+  uint64_t* dst;     // [B Hkv][most] places (Slots), in the order of slots
+  uint64_t* src;
+  uint32_t* keys;    // [B Hkv][key_stride], for rows that registers do not hold
+  uint64_t* words;   // [B Hkv][3][key_stride / 64], with the keys
+  uint8_t* flags;    // [B Hkv][key_stride / 4]: which of 4 slots are kept, a bit each
   size_t key_stride, most;
-  int Hkv, num_pages, pshift, max_pages, max_len, budget, recent;
+  int Hkv, num_pages, pshift, max_pages, max_len, budget, recent, lshift;
+  bool other;        // weights_out and positions_out are not the cache's own
 };
 
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -48,21 +58,22 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 }
 
 // Sum over the workgroup's threads before this one; total: over all.
-__device__ __forceinline__ int scan(int x, int* lds, int& total) {
+template <int WAVES>
+__device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* lds, uint32_t& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int s = x;
+  uint32_t s = x;
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) {
-    const int o = __shfl_up(s, k);
+    const uint32_t o = __shfl_up(s, k);
     if (lane >= k) s += o;
   }
   if (lane == 63) lds[wave] = s;
   __syncthreads();
-  int before = 0;
+  uint32_t before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int t = lds[w];
+  for (int w = 0; w < WAVES; ++w) {
+    const uint32_t t = lds[w];
     before += w < wave ? t : 0;
     total += t;
   }
@@ -70,163 +81,505 @@ __device__ __forceinline__ int scan(int x, int* lds, int& total) {
   return before + s - x;
 }
 
-__global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a) {
-  __shared__ int lds[kWaves];
-  __shared__ unsigned hist[256];
-  __shared__ unsigned chosen[2];
-  const int tid = threadIdx.x, pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
-  const int len = max(0, min(a.lengths[b], a.max_len));
-  const int32_t* table = a.block_table + size_t(b) * a.max_pages;
+// Where slot j of a (sequence, kv head) is, in slots of the weights and
+// positions and in rows of k and v.
+struct Slots {
+  const int32_t* table;
+  int hk, Hkv, pshift;
+  __device__ __forceinline__ size_t operator()(int j) const {
+    return ((size_t(table[j >> pshift]) * Hkv + hk) << pshift) + (j & ((1 << pshift) - 1));
+  }
+};
+
+// One move between two places: 16 bytes of k and of v a thread (`piece` of
+// the row), and with the first piece its weight and position.  No place is
+// both a source and a target, so the order of the moves is free.
+__device__ __forceinline__ void move_row(const EvictKernelArgs& a, uint64_t to, uint64_t from, int piece) {
+  const size_t x = ((from << a.lshift) + piece) * 16, y = ((to << a.lshift) + piece) * 16;
+  const u32x4 kk = ld16(a.k + x), vv = ld16(a.v + x);
+  st16(a.k + y, kk);
+  st16(a.v + y, vv);
+  if (piece == 0) {
+    a.weights_out[to] = a.weights[from];
+    a.positions_out[to] = a.positions[from];
+    a.weights_out[from] = 0.f;
+    a.positions_out[from] = -1;
+  }
+}
+
+// Slot j that does not move: copied to other memory where it stays, cleared
+// where it lies above the new length.
+__device__ __forceinline__ void settle(const EvictKernelArgs& a, const Slots& at, int j, int stay, bool kept) {
+  if (j < stay ? !(a.other && kept) : kept) return;
+  const size_t x = at(j);
+  a.weights_out[x] = j < stay ? a.weights[x] : 0.f;
+  a.positions_out[x] = j < stay ? a.positions[x] : -1;
+}
+
+constexpr int kThreads = 1024, kWaves = 16;
+constexpr int kBins[3] = {2048, 2048, 1024};   // digits of 11, 11 and 10 bits
+constexpr int kShift[3] = {21, 10, 0};
+
+// Inclusive sum over the wave's lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8: within 16 lanes
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t x, int lane) {
+  return uint32_t(__builtin_amdgcn_readlane(int(x), lane));
+}
+
+// The digit that holds the need-th largest entry of a histogram, in every
+// wave: sums of 16 groups of bins first, then the bins of one group.  After:
+// need is the rank within the digit.
+template <int BINS>
+__device__ __forceinline__ uint32_t find_digit(const uint32_t* hist, uint32_t* sums, uint32_t& need, int lane, int wave) {
+  constexpr int G = BINS / kWaves, N = G / 64;   // bins a group, bins a lane
+  uint32_t s = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += hist[wave * G + lane * N + i];
+  s = wave_scan(s);
+  if (lane == 63) sums[wave] = s;
+  __syncthreads();
+  const uint32_t g = lane < kWaves ? sums[kWaves - 1 - lane] : 0;
+  const uint32_t ig = wave_scan(g);
+  const int l = __builtin_ctzll(__ballot(ig >= need));
+  const int group = kWaves - 1 - l;
+  need -= lane_of(ig, l) - lane_of(g, l);
+  // lane i: bins from the group's top down
+  uint32_t h[N], sum = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum += h[i] = hist[group * G + G - 1 - lane * N - i];
+  const uint32_t is = wave_scan(sum);
+  const int at = __builtin_ctzll(__ballot(is >= need));
+  need -= lane_of(is, at) - lane_of(sum, at);
+  int i = 0;
+#pragma unroll
+  for (int k = 0; k + 1 < N; ++k) {
+    const uint32_t n = lane_of(h[k], at);
+    if (i == k && n < need) {
+      need -= n;
+      i = k + 1;
+    }
+  }
+  return uint32_t(group * G + G - 1 - at * N - i);
+}
+
+// A sequence that is not over its budget, or lacks a page, stays as it is: in
+// other memory its weights and positions are copied (if its pages are there).
+__device__ __forceinline__ bool missing(const EvictKernelArgs& a, const Slots& at, int len) {
   const int pages = (len + (1 << a.pshift) - 1) >> a.pshift;
-  int bad = 0;
-  for (int i = tid; i < pages; i += kThreads) bad |= unsigned(table[i]) >= unsigned(a.num_pages);
-  bad = __syncthreads_or(bad);
-  const int stay = bad ? len : min(len, a.budget);
-  if (tid == 0 && hk == 0) a.lengths_out[b] = stay;
-  if (tid == 0) a.count[pair] = 0;
-  if (bad) return;
-  // weights and positions of slot j of this head
-  const auto at = [&](int j) {
-    return ((size_t(table[j >> a.pshift]) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
-  };
-  const bool other = a.weights_out != a.weights || a.positions_out != a.positions;
-  if (stay == len) {
-    if (other)
-      for (int j = tid; j < len; j += kThreads) {
-        const size_t x = at(j);
-        a.weights_out[x] = a.weights[x];
-        a.positions_out[x] = a.positions[x];
-      }
+  bool bad = false;
+  for (int i = threadIdx.x; i < pages; i += kThreads) bad |= unsigned(at.table[i]) >= unsigned(a.num_pages);
+  return __syncthreads_or(bad);
+}
+__device__ __forceinline__ void leave(const EvictKernelArgs& a, const Slots& at, int pair, int hk, int b, int len, bool finish) {
+  if (threadIdx.x == 0 && hk == 0) a.lengths_out[b] = len;
+  if (threadIdx.x == 0 && !finish) a.count[pair] = -1;
+  if (a.other && !missing(a, at, len))
+    for (int j = threadIdx.x; j < len; j += kThreads) settle(a, at, j, len, true);
+}
+
+// NB: runs of 4 slots a thread, up to 4096 NB slots a row: slot
+// 4096 i + 4 tid + e is element e of thread tid's run i (pages hold whole
+// runs).  FINISH: this launch moves the rows too (at most kFew).
+template <int NB, bool FINISH>
+__global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
+  __shared__ uint32_t hist[kBins[0] + kBins[1] + kBins[2]];
+  __shared__ uint32_t sums[3][kWaves], counts[2][NB * kWaves];
+  __shared__ int tops[kWaves];
+  __shared__ uint64_t few[2][kFew];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
+  const int len = max(0, min(a.lengths[b], a.max_len));
+  const int stay = a.budget;
+  const Slots at = {a.block_table + size_t(b) * a.max_pages, hk, a.Hkv, a.pshift};
+  if (len <= stay) {
+    leave(a, at, pair, hk, b, len, FINISH);
     return;
   }
+  for (int i = tid; i < kBins[0] + kBins[1] + kBins[2]; i += kThreads) hist[i] = 0;
 
+  constexpr bool HOLD = NB <= 4;   // registers enough to hold weights and positions to the end
+  int page[NB];
+  f32x4 w[NB];
+  i32x4 p[NB];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    page[i] = at.table[min(4096 * i + 4 * tid, len - 1) >> a.pshift];
+    const bool out = unsigned(page[i]) >= unsigned(a.num_pages);
+    bad |= out;
+    page[i] = out ? 0 : page[i];
+  }
+  const auto place = [&](int i) {   // of run i's first slot
+    return ((size_t(page[i]) * a.Hkv + hk) << a.pshift) + (min(4096 * i + 4 * tid, (len - 1) & ~3) & ((1 << a.pshift) - 1));
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    w[i] = *reinterpret_cast<const f32x4*>(a.weights + place(i));
+    p[i] = *reinterpret_cast<const i32x4*>(a.positions + place(i));
+  }
+  const auto slot = [&](int i, int e) { return 4096 * i + 4 * tid + e; };
   int newest = INT32_MIN;
-  for (int j = tid; j < len; j += kThreads) newest = max(newest, a.positions[at(j)]);
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (slot(i, e) < len) newest = max(newest, p[i][e]);
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
-  if ((tid & 63) == 0) lds[tid >> 6] = newest;
-  __syncthreads();
-  for (int w = 0; w < kWaves; ++w) newest = max(newest, lds[w]);
-  const int64_t old = int64_t(newest) - a.recent;   // positions above it are kept first
-
-  uint32_t* keys = a.keys + size_t(pair) * a.key_stride;
-  for (int j = tid; j < len; j += kThreads) {
-    const size_t x = at(j);
-    keys[j] = int64_t(a.positions[x]) > old ? 0xffffffffu : rank_of(a.weights[x]);
+  if (lane == 0) tops[wave] = newest;
+  bad = __syncthreads_or(bad);
+  if (tid == 0 && hk == 0) a.lengths_out[b] = bad ? len : stay;
+  if (bad) {
+    if (tid == 0 && !FINISH) a.count[pair] = -1;
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) newest = max(newest, tops[i]);
+  // the distance to the newest position is exact in 32 unsigned bits
+  uint32_t key[NB][4];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      key[i][e] = uint32_t(newest) - uint32_t(p[i][e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(w[i][e]);
 
-  // the budget-th largest key, and how many equal to it stay
-  uint32_t prefix = 0, mask = 0;
-  unsigned need = unsigned(a.budget);
-  for (int shift = 24; shift >= 0; shift -= 8) {
+  // the budget-th largest key, digit by digit, until all that share the
+  // digits so far stay
+  uint32_t prefix = 0, mask = 0, need = uint32_t(stay);
+  const auto round = [&](auto bins, uint32_t* h, uint32_t* s, int shift) {
+    constexpr int BINS = decltype(bins)::value;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = slot(i, e) < len && (key[i][e] & mask) == prefix;
+        const uint64_t who = __ballot(in);
+        if (!who) continue;
+        const uint32_t digit = (key[i][e] >> shift) & (BINS - 1);
+        if (in) {
+          // one addition for a wave whose keys agree (equal weights, new tokens)
+          const uint32_t first = uint32_t(uniform(int(digit)));
+          if (__ballot(digit == first) == who) {
+            if (lane == __builtin_ctzll(who)) atomicAdd(&h[digit], uint32_t(__popcll(who)));
+          } else {
+            atomicAdd(&h[digit], 1u);
+          }
+        }
+      }
     __syncthreads();
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < len; j += kThreads) {
-      const uint32_t k = keys[j];
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    const uint32_t d = find_digit<BINS>(h, s, need, lane, wave);
+    prefix |= d << shift;
+    mask |= uint32_t(BINS - 1) << shift;
+    return h[d] == need;
+  };
+  bool all = round(std::integral_constant<int, kBins[0]>(), hist, sums[0], kShift[0]);
+  if (!all) all = round(std::integral_constant<int, kBins[1]>(), hist + kBins[0], sums[1], kShift[1]);
+  if (!all) all = round(std::integral_constant<int, kBins[2]>(), hist + kBins[0] + kBins[1], sums[2], kShift[2]);
+
+  // Sums of mine[] over the runs before this thread's run i, in slot order.
+  const auto before = [&](uint32_t (&mine)[NB], uint32_t* lds, uint32_t (&out)[NB]) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint32_t s = wave_scan(mine[i]);
+      out[i] = s - mine[i];
+      if (lane == 63) lds[i * kWaves + wave] = s;
     }
     __syncthreads();
-    if (tid < 64) {   // lane i: digits 255 - 4 i ... 252 - 4 i
-      unsigned n[4], s = 0;
+    uint32_t carry = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s += n[k] = hist[255 - 4 * tid - k];
-      unsigned upto = s;
+    for (int c = 0; c < NB * kWaves; c += 64) {   // 4 runs of 16 waves at a time
+      const uint32_t v = c + lane < NB * kWaves ? lds[c + lane] : 0, s = wave_scan(v);
 #pragma unroll
-      for (int k = 1; k < 64; k *= 2) {
-        const unsigned o = __shfl_up(upto, k);
-        if (tid >= k) upto += o;
+      for (int i = c / kWaves; i < c / kWaves + 4 && i < NB; ++i) {
+        const int l = i * kWaves - c + wave;
+        out[i] += carry + lane_of(s, l) - lane_of(v, l);
       }
-      unsigned above = upto - s;
-      if (above < need && upto >= need) {
+      carry += lane_of(s, 63);
+    }
+    return carry;
+  };
+  uint32_t kept[NB];   // a bit a slot
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (above < need && above + n[k] >= need) {
-            chosen[0] = 255 - 4 * tid - k;
-            chosen[1] = need - above;
-          }
-          above += n[k];
+  for (int i = 0; i < NB; ++i) {
+    kept[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kept[i] |= uint32_t(slot(i, e) < len && (key[i][e] & mask) >= prefix) << e;
+  }
+  if (!all) {   // of the keys equal to the last the first `need` stay
+    uint32_t n[NB], rank[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      n[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) n[i] += slot(i, e) < len && key[i][e] == prefix;
+    }
+    before(n, counts[0], rank);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (slot(i, e) < len && key[i][e] == prefix && rank[i]++ >= need) kept[i] &= ~(1u << e);
+  }
+  // holes below the new length (low half) and what fills them (high half)
+  uint32_t n[NB], rank[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const uint32_t low = (1u << min(max(stay - slot(i, 0), 0), 4)) - 1;
+    n[i] = __popc(~kept[i] & low) | __popc(kept[i] & ~low) << 16;
+  }
+  const uint32_t total = before(n, counts[1], rank) & 0xffff;
+  uint64_t* dst = FINISH ? few[0] : a.dst + size_t(pair) * a.most;
+  uint64_t* src = FINISH ? few[1] : a.src + size_t(pair) * a.most;
+  uint8_t* flags = a.flags + size_t(pair) * (a.key_stride / 4);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int j = slot(i, 0);
+    if (j >= len) continue;
+    uint32_t hole = rank[i] & 0xffff, fill = rank[i] >> 16;
+    const uint64_t x = place(i);
+    if (n[i]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool k = kept[i] >> e & 1, low = j + e < stay;
+        if (low && !k) dst[hole++] = x + e;
+        if (!low && k) src[fill++] = x + e;
+      }
+    }
+    if constexpr (FINISH) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool k = kept[i] >> e & 1, low = j + e < stay;
+        if (low ? a.other && k : j + e < len && !k) {
+          a.weights_out[x + e] = !low ? 0.f : HOLD ? w[i][e] : a.weights[x + e];
+          a.positions_out[x + e] = !low ? -1 : HOLD ? p[i][e] : a.positions[x + e];
         }
+      }
+    } else {
+      flags[j / 4] = uint8_t(kept[i]);
+    }
+  }
+  if constexpr (FINISH) {
+    __syncthreads();
+    const int piece = tid & ((1 << a.lshift) - 1), rows = kThreads >> a.lshift;
+    for (uint32_t i = tid >> a.lshift; i < total; i += rows) move_row(a, dst[i], src[i], piece);
+  } else if (tid == 0) {
+    a.count[pair] = int(total);
+  }
+}
+
+// Rows of any length, with keys and words in the workspace: several times
+// slower a slot, for rows that registers do not hold.
+template <bool FINISH>
+__global__ __launch_bounds__(kThreads) void select_long_kernel(EvictKernelArgs a) {
+  constexpr int THREADS = kThreads, WAVES = kWaves, BINS = 2048;
+  __shared__ uint32_t lds[WAVES];
+  __shared__ uint32_t hist[BINS];
+  __shared__ uint32_t chosen[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
+  const int len = max(0, min(a.lengths[b], a.max_len));
+  const Slots at = {a.block_table + size_t(b) * a.max_pages, hk, a.Hkv, a.pshift};
+  if (len <= a.budget) {
+    leave(a, at, pair, hk, b, len, FINISH);
+    return;
+  }
+  const int stay = a.budget;
+  const bool bad = missing(a, at, len);
+  if (tid == 0 && hk == 0) a.lengths_out[b] = bad ? len : stay;
+  if (bad) {
+    if (tid == 0 && !FINISH) a.count[pair] = -1;
+    return;
+  }
+  uint32_t* keys = a.keys + size_t(pair) * a.key_stride;
+  const size_t third = a.key_stride / 64;
+  uint64_t* kept = a.words + size_t(pair) * 3 * third;
+  uint64_t* above = kept + third;   // keys above the budget-th, and equal to it
+  uint64_t* equal = above + third;
+  const int nwords = (len + 63) / 64;
+
+  // keys, and the newest position
+  int newest = INT32_MIN;
+  for (int j0 = tid; j0 < len; j0 += 4 * THREADS) {
+    float w[4];
+    int p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const size_t x = at(min(j0 + u * THREADS, len - 1));
+      w[u] = a.weights[x];
+      p[u] = a.positions[x];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      newest = max(newest, p[u]);
+      if (j0 + u * THREADS < len) keys[j0 + u * THREADS] = rank_of(w[u]);
+    }
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
+  if (lane == 0) lds[wave] = uint32_t(newest);
+  __syncthreads();
+  for (int w = 0; w < WAVES; ++w) newest = max(newest, int(lds[w]));
+  if (a.recent) {   // positions above `old` are kept first
+    const int64_t old = int64_t(newest) - a.recent;
+    for (int j0 = tid; j0 < len; j0 += 4 * THREADS) {
+      int p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = a.positions[at(min(j0 + u * THREADS, len - 1))];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j0 + u * THREADS < len && int64_t(p[u]) > old) keys[j0 + u * THREADS] = 0xffffffffu;
+    }
+  }
+
+  // the budget-th largest key, and how many equal to it stay: digits of 11,
+  // 11 and 10 bits
+  uint32_t prefix = 0, mask = 0, need = uint32_t(a.budget);
+#pragma unroll 1
+  for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+    const uint32_t bins = shift ? BINS : 1024;
+    for (uint32_t i = tid; i < bins; i += THREADS) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < len; j += THREADS) {
+      const uint32_t k = keys[j];
+      const bool in = (k & mask) == prefix;
+      const uint32_t digit = (k >> shift) & (bins - 1);
+      const uint64_t who = __ballot(in);
+      if (in) {
+        // one addition for a wave whose keys agree (equal weights)
+        const uint32_t first = uint32_t(uniform(int(digit)));
+        if (__ballot(digit == first) == who) {
+          if (lane == __builtin_ctzll(who)) atomicAdd(&hist[digit], uint32_t(__popcll(who)));
+        } else {
+          atomicAdd(&hist[digit], 1u);
+        }
+      }
+    }
+    __syncthreads();
+    // thread t: the digits from bins - 1 - t n down
+    const int n = int(bins) / THREADS > 0 ? int(bins) / THREADS : 1;
+    const int top = int(bins) - 1 - tid * n;
+    uint32_t sum = 0, total;
+    for (int i = 0; i < n; ++i) sum += top - i >= 0 ? hist[top - i] : 0;
+    uint32_t over = scan<WAVES>(sum, lds, total);
+    if (over < need && over + sum >= need) {
+      for (int i = 0; i < n; ++i) {
+        const uint32_t h = hist[top - i];
+        if (over < need && over + h >= need) {
+          chosen[0] = uint32_t(top - i);
+          chosen[1] = need - over;
+        }
+        over += h;
       }
     }
     __syncthreads();
     prefix |= chosen[0] << shift;
     need = chosen[1];
-    mask |= 255u << shift;
+    mask |= (bins - 1) << shift;
   }
 
-  // in slot order: what stays, the holes below the new length, and the kept
-  // slots from it on
-  int32_t* dst = a.dst + size_t(pair) * a.most;
-  int32_t* src = a.src + size_t(pair) * a.most;
-  int equal = 0, holes = 0, fills = 0;
-  for (int j0 = 0; j0 < len; j0 += kThreads) {
-    const int j = j0 + tid;
+  // a word a wave: which keys are above and which equal
+  for (int w = wave; w < nwords; w += WAVES) {
+    const int j = 64 * w + lane;
     const uint32_t k = j < len ? keys[j] : 0;
-    const bool eq = j < len && k == prefix;
-    int total;
-    const int rank = equal + scan(eq, lds, total);
-    equal += total;
-    const bool kept = j < len && (k > prefix || (eq && unsigned(rank) < need));
-    const bool hole = j < stay && !kept, fill = j >= stay && kept;
-    int both;
-    const int before = scan(int(hole) | int(fill) << 16, lds, both);
-    if (hole) dst[holes + (before & 0xffff)] = j;
-    if (fill) src[fills + (before >> 16)] = j;
-    holes += both & 0xffff;
-    fills += both >> 16;
-    if (other && j < stay) {
-      const size_t x = at(j);
-      a.weights_out[x] = a.weights[x];
-      a.positions_out[x] = a.positions[x];
+    const uint64_t gt = __ballot(j < len && k > prefix), eq = __ballot(j < len && k == prefix);
+    if (lane == 0) {
+      above[w] = gt;
+      equal[w] = eq;
     }
   }
-  if (tid == 0) a.count[pair] = holes;
   __syncthreads();
-  for (int i = tid; i < holes; i += kThreads) {
-    const size_t to = at(dst[i]), from = at(src[i]);
-    a.weights_out[to] = a.weights[from];
-    a.positions_out[to] = a.positions[from];
+  // of the equal ones the first `need` stay
+  uint32_t before = 0;
+  for (int w0 = 0; w0 < nwords; w0 += THREADS) {
+    const int w = w0 + tid;
+    const uint64_t eq = w < nwords ? equal[w] : 0;
+    uint32_t total;
+    const uint32_t rank = before + scan<WAVES>(uint32_t(__popcll(eq)), lds, total);
+    before += total;
+    if (w < nwords) {
+      uint64_t take = rank < need ? eq : 0;
+      while (take && rank + uint32_t(__popcll(take)) > need) take &= ~(uint64_t(1) << (63 - __builtin_clzll(take)));
+      kept[w] = above[w] | take;
+    }
   }
   __syncthreads();
-  for (int j = stay + tid; j < len; j += kThreads) {
-    const size_t x = at(j);
-    a.weights_out[x] = 0.f;
-    a.positions_out[x] = -1;
+  // ranks of the holes below the new length and of what fills them: prefix
+  // sums over words, in the place of `above` (holes) and `equal` (fills)
+  uint32_t holes = 0, fills = 0;
+  for (int w0 = 0; w0 < nwords; w0 += THREADS) {
+    const int w = w0 + tid;
+    uint32_t h = 0, f = 0;
+    if (w < nwords) {
+      const int below = min(max(stay - 64 * w, 0), 64);
+      const uint64_t low = below == 64 ? ~uint64_t(0) : (uint64_t(1) << below) - 1;
+      h = uint32_t(__popcll(~kept[w] & low));
+      f = uint32_t(__popcll(kept[w] & ~low));
+    }
+    uint32_t th, tf;
+    const uint32_t rh = holes + scan<WAVES>(h, lds, th), rf = fills + scan<WAVES>(f, lds, tf);
+    if (w < nwords) {
+      above[w] = rh;
+      equal[w] = rf;
+    }
+    holes += th;
+    fills += tf;
+  }
+  __syncthreads();
+  uint64_t* dst = a.dst + size_t(pair) * a.most;
+  uint64_t* src = a.src + size_t(pair) * a.most;
+  for (int w = wave; w < nwords; w += WAVES) {
+    const uint64_t stays = kept[w];
+    const int j = 64 * w + lane, below = min(max(stay - 64 * w, 0), 64);
+    const uint64_t low = below == 64 ? ~uint64_t(0) : (uint64_t(1) << below) - 1;
+    const uint64_t bit = uint64_t(1) << lane, under = bit - 1;
+    if (~stays & low & bit) dst[above[w] + __popcll(~stays & low & under)] = at(j);
+    if (stays & ~low & bit) src[equal[w] + __popcll(stays & ~low & under)] = at(j);
+    if constexpr (FINISH) {
+      if (j < len) settle(a, at, j, stay, stays & bit);
+    } else if (lane < 16) {
+      a.flags[size_t(pair) * (a.key_stride / 4) + 16 * w + lane] = uint8_t(stays >> (4 * lane) & 15);
+    }
+  }
+  if constexpr (FINISH) {
+    __syncthreads();
+    const int piece = tid & ((1 << a.lshift) - 1), per = THREADS >> a.lshift;
+    for (int i = tid >> a.lshift; i < int(holes); i += per) move_row(a, dst[i], src[i], piece);
+  } else if (tid == 0) {
+    a.count[pair] = int(holes);
   }
 }
 
-struct MoveArgs {
-  uint8_t* k;
-  uint8_t* v;
-  const int32_t* block_table;
-  const int32_t* count;
-  const int32_t* dst;
-  const int32_t* src;
-  size_t most;
-  int Hkv, pshift, max_pages, lshift;   // lshift: log2 of 16-byte pieces a row
-};
-
-// 16 bytes of k and of v a thread.  No row is both a source and a target, so
-// the order of the moves is free.
-__global__ __launch_bounds__(256) void move_kernel(MoveArgs a) {
+__global__ __launch_bounds__(256) void move_kernel(EvictKernelArgs a) {
   const int pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
   const int n = a.count[pair];
-  const int32_t* table = a.block_table + size_t(b) * a.max_pages;
+  if (n < 0) return;
+  const Slots at = {a.block_table + size_t(b) * a.max_pages, hk, a.Hkv, a.pshift};
   const int piece = threadIdx.x & ((1 << a.lshift) - 1), per = 256 >> a.lshift;
-  const auto at = [&](int j) {
-    const size_t row = ((size_t(table[j >> a.pshift]) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
-    return ((row << a.lshift) + piece) * 16;
-  };
-  for (int i = blockIdx.y * per + (threadIdx.x >> a.lshift); i < n; i += gridDim.y * per) {
-    const size_t to = at(a.dst[pair * a.most + i]), from = at(a.src[pair * a.most + i]);
-    const u32x4 x = ld16(a.k + from), y = ld16(a.v + from);
-    st16(a.k + to, x);
-    st16(a.v + to, y);
-  }
+  const uint64_t* dst = a.dst + size_t(pair) * a.most;
+  const uint64_t* src = a.src + size_t(pair) * a.most;
+  for (int i = blockIdx.y * per + (threadIdx.x >> a.lshift); i < n; i += gridDim.y * per)
+    move_row(a, dst[i], src[i], piece);
+  const int len = min(a.lengths[b], a.max_len);
+  const uint8_t* flags = a.flags + size_t(pair) * (a.key_stride / 4);
+  for (int j = (a.other ? 0 : a.budget & ~255) + blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256)
+    settle(a, at, j, a.budget, flags[j >> 2] >> (j & 3) & 1);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int NB>
+void run_select(const EvictKernelArgs& a, unsigned pairs, bool finish, hipStream_t s) {
+  if (finish) hipLaunchKernelGGL((select_kernel<NB, true>), dim3(pairs), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((select_kernel<NB, false>), dim3(pairs), dim3(kThreads), 0, s, a);
+}
 
 }  // namespace
 
@@ -237,15 +590,17 @@ EvictPlan evict_plan(const gbb_paged_cache& c, int B, int max_len, int budget) {
   p.most = size_t(std::max(0, std::min(budget, max_len - budget)));
   p.count_off = 0;
   p.dst_off = up(pairs * 4);
-  p.src_off = p.dst_off + up(pairs * p.most * 4);
-  p.key_off = p.src_off + up(pairs * p.most * 4);
-  p.ws_bytes = p.key_off + up(pairs * p.key_stride * 4);
+  p.src_off = p.dst_off + up(pairs * p.most * 8);
+  p.word_off = p.src_off + up(pairs * p.most * 8);
+  p.flag_off = p.word_off + (max_len > kMaxHeld ? up(pairs * 3 * (p.key_stride / 64) * 8) : 0);
+  p.key_off = p.flag_off + up(pairs * (p.key_stride / 4));
+  p.ws_bytes = p.key_off + (max_len > kMaxHeld ? up(pairs * p.key_stride * 4) : 0);
   return p;
 }
 
 int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& p, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  SelectArgs a;
+  EvictKernelArgs a;
   a.block_table = x.block_table;
   a.lengths = x.lengths;
   a.lengths_out = x.lengths_out;
@@ -253,10 +608,14 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
   a.positions = c.positions;
   a.weights_out = x.weights_out;
   a.positions_out = x.positions_out;
+  a.k = static_cast<uint8_t*>(c.k);
+  a.v = static_cast<uint8_t*>(c.v);
   a.count = reinterpret_cast<int32_t*>(x.ws + p.count_off);
-  a.dst = reinterpret_cast<int32_t*>(x.ws + p.dst_off);
-  a.src = reinterpret_cast<int32_t*>(x.ws + p.src_off);
+  a.dst = reinterpret_cast<uint64_t*>(x.ws + p.dst_off);
+  a.src = reinterpret_cast<uint64_t*>(x.ws + p.src_off);
   a.keys = reinterpret_cast<uint32_t*>(x.ws + p.key_off);
+  a.words = reinterpret_cast<uint64_t*>(x.ws + p.word_off);
+  a.flags = reinterpret_cast<uint8_t*>(x.ws + p.flag_off);
   a.key_stride = p.key_stride;
   a.most = p.most;
   a.Hkv = c.kv_heads;
@@ -266,24 +625,21 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
   a.max_len = x.max_len;
   a.budget = x.budget;
   a.recent = x.recent;
+  a.lshift = __builtin_ctz(unsigned(c.head_dim * (c.dtype == GBB_E4M3 ? 1 : 2) / 16));
+  a.other = x.weights_out != c.weights || x.positions_out != c.positions;
   const unsigned pairs = unsigned(x.B) * c.kv_heads;
-  hipLaunchKernelGGL(select_kernel, dim3(pairs), dim3(kThreads), 0, s, a);
-  if (p.most) {
-    MoveArgs m;
-    m.k = static_cast<uint8_t*>(c.k);
-    m.v = static_cast<uint8_t*>(c.v);
-    m.block_table = x.block_table;
-    m.count = a.count;
-    m.dst = a.dst;
-    m.src = a.src;
-    m.most = p.most;
-    m.Hkv = c.kv_heads;
-    m.pshift = a.pshift;
-    m.max_pages = x.max_pages;
-    m.lshift = __builtin_ctz(unsigned(c.head_dim * (c.dtype == GBB_E4M3 ? 1 : 2) / 16));
-    const size_t per = 256 >> m.lshift;
-    const unsigned gy = unsigned(std::min<size_t>((p.most + per - 1) / per, std::max(1u, 4096u / pairs)));
-    hipLaunchKernelGGL(move_kernel, dim3(pairs, gy), dim3(256), 0, s, m);
+  const bool finish = p.most <= size_t(kFew);
+  if (x.max_len <= 4096) run_select<1>(a, pairs, finish, s);
+  else if (x.max_len <= 8192) run_select<2>(a, pairs, finish, s);
+  else if (x.max_len <= 16384) run_select<4>(a, pairs, finish, s);
+  else if (x.max_len <= kMaxHeld) run_select<8>(a, pairs, finish, s);
+  else if (finish) hipLaunchKernelGGL((select_long_kernel<true>), dim3(pairs), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((select_long_kernel<false>), dim3(pairs), dim3(kThreads), 0, s, a);
+  if (!finish) {
+    const size_t per = 256 >> a.lshift;
+    const size_t most = std::max((p.most + per - 1) / per, (size_t(x.max_len) + 255) / 256);
+    const unsigned gy = unsigned(std::min<size_t>(most, std::max(1u, 4096u / pairs)));
+    hipLaunchKernelGGL(move_kernel, dim3(pairs, gy), dim3(256), 0, s, a);
   }
   return int(hipGetLastError());
 }

@@ -153,9 +153,9 @@ struct AttendArgs {
 int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPlan& p, void* stream);
 
 struct EvictPlan {
-  size_t key_stride;    // ranking keys per (sequence, kv head)
+  size_t key_stride;    // ranking keys per (sequence, kv head), a multiple of 64
   size_t most;          // rows that can move per (sequence, kv head)
-  size_t count_off, dst_off, src_off, key_off, ws_bytes;
+  size_t count_off, dst_off, src_off, word_off, flag_off, key_off, ws_bytes;
 };
 EvictPlan evict_plan(const gbb_paged_cache& c, int B, int max_len, int budget);
 struct EvictArgs {

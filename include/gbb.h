@@ -467,7 +467,8 @@ gbb_status gbb_rope(const void* x, int64_t x_token, int64_t x_head, void* y, int
                     int rot, int layout, int transpose, void* stream);
 
 /* A paged cache of keys and values.  Slot s is token s % page of page
- * s / page.  All pointers are device memory that the caller owns. */
+ * s / page.  All pointers are device memory that the caller owns; k, v,
+ * weights and positions are 16-byte aligned. */
 typedef struct {
   void* k;                /* [num_pages][kv_heads][page][head_dim], dtype */
   void* v;                /* the same shape and dtype */
