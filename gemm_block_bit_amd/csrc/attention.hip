@@ -73,6 +73,25 @@ template <> struct Half<GBB_BF16> {
   }
 };
 
+// 16 bytes a lane from memory to LDS at `to` (the same in all lanes) plus 16
+// bytes times the lane.  The compiler does not wait for such a load before
+// LDS reads: loads_left<N>() waits until at most the N vector memory
+// operations issued last are under way (they complete in order), in_order()
+// keeps the compiler from moving memory operations across it, and
+// reads_done() awaits LDS reads, before a load overwrites what they read.
+__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
+                                       reinterpret_cast<uintptr_t>(from)),
+                                   (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void loads_left() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 struct SplitArgs {
   const void* q;
   const uint8_t* k;
@@ -102,9 +121,14 @@ __device__ __forceinline__ float rescale(float x, float m) {
   return x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - m);
 }
 
-template <int DT, int CT, int D, bool WT>
-__global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void split_kernel(SplitArgs a) {
+// Waves of a workgroup: 4, or 8 (WIDE) for calls with so few runs that a
+// workgroup should have a CU to itself.
+constexpr int waves(bool wide) { return wide ? 8 : 4; }
+
+template <int DT, int CT, int D, bool WT, bool WIDE>
+__global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ? 3 : 4) void split_kernel(SplitArgs a) {
   typedef Half<DT> H;
+  constexpr int NW = waves(WIDE), THREADS = 64 * NW;
   typedef typename H::V8 V8;
   constexpr bool F8 = CT == GBB_E4M3;
   constexpr int ES = F8 ? 1 : 2, ROW = D * ES;
@@ -115,18 +139,30 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g4 = lane >> 4;
   int id = blockIdx.x;
-  const int sp = id % a.nsplit;
-  id /= a.nsplit;
   const int qt = id % a.qtiles;
   id /= a.qtiles;
-  const int hk = id % a.Hkv, b = id / a.Hkv;
-  const int len = length_of(a, b);
+  const int hk = id % a.Hkv;
+  id /= a.Hkv;
+  const int b = id % a.B, sp = id / a.B;
   const int rows = min(16, a.G - 16 * qt);           // query heads of this tile
   const int hq0 = hk * a.G + 16 * qt;
   const int k0 = sp * a.chunk;
+  // lane 2 i + s: the page of 16-slot half s of this wave's tile i.  It is
+  // looked up before the length is known (the table has max_len's entries).
+  const int key = k0 + 32 * (wave + NW * (lane >> 1)) + 16 * (lane & 1);
+  int page = a.block_table[size_t(b) * a.max_pages + (min(key, a.max_len - 1) >> a.pshift)];
+  // rows past the last query head repeat it: their results are not used
+  u32x4 qw[D / 32];
+#pragma unroll
+  for (int kc = 0; kc < D / 32; ++kc) {
+    const int d = F8 ? 64 * (kc >> 1) + 16 * g4 + 8 * (kc & 1) : 32 * kc + 8 * g4;
+    qw[kc] = ld16(static_cast<const uint16_t*>(a.q) + b * a.q_token + size_t(hq0 + min(c, rows - 1)) * D + d);
+  }
+  in_order();
+  const int len = uniform(length_of(a, b));
   if (k0 >= len) {
     if (sp == 0) {                                   // an empty sequence
-      for (int i = threadIdx.x; i < rows * D; i += 256)
+      for (int i = threadIdx.x; i < rows * D; i += THREADS)
         static_cast<typename H::T*>(a.out)[(size_t(b) * a.Hq + hq0) * D + i] = typename H::T(0.f);
       if (a.lse && threadIdx.x < rows) a.lse[size_t(b) * a.Hq + hq0 + threadIdx.x] = -INFINITY;
     }
@@ -134,24 +170,21 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
   }
   const int k1 = min(len, k0 + a.chunk);
   const int ntile = (k1 - k0 + 31) >> 5;
-  const int n = (ntile - wave + 3) >> 2;             // tiles of this wave: wave, wave + 4, ...
-  // lane 2 i + s holds the page of 16-slot half s of this wave's tile i
-  int page = -1;
-  {
-    const int key = k0 + 32 * (wave + 4 * (lane >> 1)) + 16 * (lane & 1);
-    if (key < k1) page = a.block_table[size_t(b) * a.max_pages + (key >> a.pshift)];
-    if (unsigned(page) >= unsigned(a.num_pages)) page = -1;
-  }
+  const int n = (ntile - wave + NW - 1) / NW;        // tiles of this wave: wave, wave + NW, ...
+  if (key >= k1 || unsigned(page) >= unsigned(a.num_pages)) page = -1;
   V8 qf[D / 32];
 #pragma unroll
   for (int kc = 0; kc < D / 32; ++kc) {
-    const int d = F8 ? 64 * (kc >> 1) + 16 * g4 + 8 * (kc & 1) : 32 * kc + 8 * g4;
-    u32x4 z = {0, 0, 0, 0};
-    if (c < rows) z = ld16(static_cast<const uint16_t*>(a.q) + b * a.q_token + size_t(hq0 + c) * D + d);
-    qf[kc] = __builtin_bit_cast(V8, z);
+    asm volatile("" : "+v"(qw[kc]));   // awaited here, with the page, and not in the loop with its loads
+    qf[kc] = __builtin_bit_cast(V8, qw[kc]);
   }
   const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
 
+  // 32 rows of K a wave, and in the end the waves' outputs
+  constexpr int OROW = D + 4, OWN = 16 * OROW * 4 > 32 * ROW ? 16 * OROW * 4 : 32 * ROW;
+  __shared__ __align__(16) uint8_t lds[NW * OWN];
+  uint8_t* mine = lds + wave * OWN;
+  const auto so = [&](int w, int q, int d) -> float& { return reinterpret_cast<float*>(lds + w * OWN)[q * OROW + d]; };
   f32x4 o[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x4{0, 0, 0, 0};
@@ -159,22 +192,37 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
   const int pmask = (1 << a.pshift) - 1;
   const size_t page_bytes = (size_t(1) << a.pshift) * ROW;
 
-  struct Tile {
-    u32x4 k[2][KP];
-    uint32_t v[2][4][NV][VW];
-  };
+  // K goes through LDS, in memory of the wave's own: it is loaded there
+  // directly with neighbouring lanes on a row (a load with a row a lane asks
+  // for 64 separate lines and takes four times as long to issue) and read
+  // back a row a lane.  The load writes lane by lane, so lane l is given the
+  // piece (16 bytes) that makes piece p of row r land at p ^ swizzle(r),
+  // which spreads the 16 rows that lanes read at once over all banks.
+  constexpr int LPR = ROW / 16, RPI = 64 / LPR;      // lanes a row, rows an instruction
+  constexpr auto swizzle = [](int r) { return (ROW >= 256 ? r : r / (256 / ROW)) & (LPR < 16 ? LPR - 1 : 15); };
   // Pages hold whole 16-slot halves, so a half's rows are always memory of
   // the cache; a page that is not there is read as page 0 and masked.
-  auto load = [&](Tile& t, int i) {
+  const auto half_at = [&](int i, int s) {
+    const int p = max(0, __builtin_amdgcn_readlane(page, 2 * i + s));
+    const int key = k0 + 32 * (wave + NW * i) + 16 * s;
+    return (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * ROW;
+  };
+  uint32_t vr[2][4][NV][VW];
+  const auto load_k = [&](int i) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int p = max(0, __builtin_amdgcn_readlane(page, 2 * i + s));
-      const int key = k0 + 32 * (wave + 4 * i) + 16 * s;
-      const size_t off = (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * ROW;
-      const uint8_t* kb = a.k + off + c * ROW + g4 * 16;
-      const uint8_t* vb = a.v + off + 4 * g4 * ROW + c * VB;
+      const uint8_t* kb = a.k + half_at(i, s);
 #pragma unroll
-      for (int j = 0; j < KP; ++j) t.k[s][j] = ld16(kb + 64 * j);
+      for (int j = 0; j < KP; ++j) {
+        const int r = j * RPI + lane / LPR;
+        to_lds(kb + r * ROW + ((lane % LPR) ^ swizzle(r)) * 16, mine + s * 16 * ROW + j * 1024);
+      }
+    }
+  };
+  const auto load_v = [&](int i) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint8_t* vb = a.v + half_at(i, s) + 4 * g4 * ROW + c * VB;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -183,38 +231,44 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
           if constexpr (VW == 4) {
             const u32x4 x = ld16(p2);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) t.v[s][r][u][w] = x[w];
+            for (int w = 0; w < 4; ++w) vr[s][r][u][w] = x[w];
           } else if constexpr (VW == 2) {
             const uint2 x = *reinterpret_cast<const uint2*>(p2);
-            t.v[s][r][u][0] = x.x;
-            t.v[s][r][u][1] = x.y;
+            vr[s][r][u][0] = x.x;
+            vr[s][r][u][1] = x.y;
           } else {
-            t.v[s][r][u][0] = *reinterpret_cast<const uint32_t*>(p2);
+            vr[s][r][u][0] = *reinterpret_cast<const uint32_t*>(p2);
           }
         }
     }
   };
-  auto compute = [&](Tile& t, int i) {
-    const int key0 = k0 + 32 * (wave + 4 * i);
+  const auto compute = [&](int i) {
+    const int key0 = k0 + 32 * (wave + NW * i);
     f32x4 s[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       s[e] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < KP; ++j) {
+        const u32x4 kk = *reinterpret_cast<const u32x4*>(mine + (16 * e + c) * ROW + ((4 * j + g4) ^ swizzle(c)) * 16);
         if constexpr (F8) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = t.k[e][j][2 * h], w1 = t.k[e][j][2 * h + 1];
+            const uint32_t w0 = kk[2 * h], w1 = kk[2 * h + 1];
             const u32x4 x = {H::template widen<false>(w0), H::template widen<true>(w0),
                              H::template widen<false>(w1), H::template widen<true>(w1)};
             s[e] = H::mfma(__builtin_bit_cast(V8, x), qf[2 * j + h], s[e]);
           }
         } else {
-          s[e] = H::mfma(__builtin_bit_cast(V8, t.k[e][j]), qf[j], s[e]);
+          s[e] = H::mfma(__builtin_bit_cast(V8, kk), qf[j], s[e]);
         }
       }
       s[e] *= scale;
+    }
+    if (i + 1 < n) {
+      reads_done();
+      load_k(i + 1);
+      in_order();
     }
     // a tile that the length or a missing page cuts: those slots take no
     // part, and whatever their memory holds must not reach the product
@@ -229,7 +283,7 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
 #pragma unroll
             for (int u = 0; u < NV; ++u)
 #pragma unroll
-              for (int w = 0; w < VW; ++w) t.v[e][r][u][w] = 0;
+              for (int w = 0; w < VW; ++w) vr[e][r][u][w] = 0;
           }
     }
     if constexpr (WT) {
@@ -280,7 +334,7 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                x[e][r] = __builtin_amdgcn_perm(t.v[e][2 * r + 1][u][w], t.v[e][2 * r][u][w], sel);
+                x[e][r] = __builtin_amdgcn_perm(vr[e][2 * r + 1][u][w], vr[e][2 * r][u][w], sel);
             product(u * EV + 4 * w + 2 * h,
                     u32x4{H::template widen<false>(x[0][0]), H::template widen<false>(x[0][1]),
                           H::template widen<false>(x[1][0]), H::template widen<false>(x[1][1])});
@@ -293,30 +347,30 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
           for (int h = 0; h < 2; ++h) {
             const uint32_t sel = h ? 0x07060302u : 0x05040100u;
             product(u * EV + 2 * w + h,
-                    u32x4{__builtin_amdgcn_perm(t.v[0][1][u][w], t.v[0][0][u][w], sel),
-                          __builtin_amdgcn_perm(t.v[0][3][u][w], t.v[0][2][u][w], sel),
-                          __builtin_amdgcn_perm(t.v[1][1][u][w], t.v[1][0][u][w], sel),
-                          __builtin_amdgcn_perm(t.v[1][3][u][w], t.v[1][2][u][w], sel)});
+                    u32x4{__builtin_amdgcn_perm(vr[0][1][u][w], vr[0][0][u][w], sel),
+                          __builtin_amdgcn_perm(vr[0][3][u][w], vr[0][2][u][w], sel),
+                          __builtin_amdgcn_perm(vr[1][1][u][w], vr[1][0][u][w], sel),
+                          __builtin_amdgcn_perm(vr[1][3][u][w], vr[1][2][u][w], sel)});
           }
         }
       }
   };
-  Tile t0, t1;
+  // the next tile's K is loaded once this one's scores are there, its V once
+  // this one's product is
   if (n > 0) {
-    load(t0, 0);
-    int i = 0;
-    for (; i + 2 <= n; i += 2) {
-      load(t1, i + 1);
-      compute(t0, i);
-      if (i + 2 < n) load(t0, i + 2);
-      compute(t1, i + 1);
-    }
-    if (i < n) compute(t0, i);
+    load_k(0);
+    in_order();
+    load_v(0);
+  }
+  for (int i = 0; i < n; ++i) {
+    loads_left<8 * NV>();   // K's loads are older than V's 8 NV
+    compute(i);
+    in_order();
+    if (i + 1 < n) load_v(i + 1);
   }
 
-  // join the four waves
-  __shared__ float sm[4][16], sl[4][16];
-  __shared__ float so[4][16][D + 4];
+  // join the waves
+  __shared__ float sm[NW][16], sl[NW][16];
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (g4 == 0) {
@@ -327,20 +381,22 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) so[wave][c][(t / EV) * 16 * EV + EV * (4 * g4 + r) + t % EV] = o[t][r];
+      for (int r = 0; r < 4; ++r) so(wave, c, (t / EV) * 16 * EV + EV * (4 * g4 + r) + t % EV) = o[t][r];
   }
   __syncthreads();
   const bool whole = len <= a.chunk;
   const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
-  for (int i = threadIdx.x; i < rows * D; i += 256) {
+  for (int i = threadIdx.x; i < rows * D; i += THREADS) {
     const int q = i / D, d = i % D;
-    const float mm = fmaxf(fmaxf(sm[0][q], sm[1][q]), fmaxf(sm[2][q], sm[3][q]));
+    float mm = sm[0][q];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) mm = fmaxf(mm, sm[w][q]);
     float ll = 0.f, oo = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float f = rescale(sm[w][q], mm);
       ll += f * sl[w][q];
-      oo += f * so[w][q][d];
+      oo += f * so(w, q, d);
     }
     const size_t row = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt + q;
     if (whole) {
@@ -355,15 +411,17 @@ __global__ __launch_bounds__(256, (D == 256 && CT != GBB_E4M3) ? 1 : 2) void spl
   }
 }
 
-// Maximum and sum of a query head over its runs, the same in all 64 lanes.
+// Maximum and sum of a query head over its ns runs, the same in all 64 lanes.
 __device__ __forceinline__ float2 join_sums(const float2* ml, int ns, int G, int lane) {
-  float mm = -INFINITY, ll = 0.f;
-  for (int i = lane; i < ns; i += 64) mm = fmaxf(mm, ml[size_t(i) * G].x);
+  const float2 e = lane < ns ? ml[size_t(lane) * G] : make_float2(-INFINITY, 0.f);
+  float mm = e.x, ll = 0.f;
+  for (int i = lane + 64; i < ns; i += 64) mm = fmaxf(mm, ml[size_t(i) * G].x);
 #pragma unroll
   for (int x = 1; x < 64; x *= 2) mm = fmaxf(mm, __shfl_xor(mm, x));
-  for (int i = lane; i < ns; i += 64) {
-    const float2 e = ml[size_t(i) * G];
-    ll += rescale(e.x, mm) * e.y;
+  ll = rescale(e.x, mm) * e.y;
+  for (int i = lane + 64; i < ns; i += 64) {
+    const float2 f = ml[size_t(i) * G];
+    ll += rescale(f.x, mm) * f.y;
   }
 #pragma unroll
   for (int x = 1; x < 64; x *= 2) ll += __shfl_xor(ll, x);
@@ -371,8 +429,11 @@ __device__ __forceinline__ float2 join_sums(const float2* ml, int ns, int G, int
 }
 
 // Joins the runs of every (sequence, query head) in the first `heads`
-// workgroups; the others (with weights) take 256 slots of a (sequence, kv
-// head) each.
+// workgroups; the others (with weights) take 1024 slots of a (sequence, kv
+// head) each.  A launch of few short loads: what counts is that the loads do
+// not wait for each other, so those of the first runs are issued before the
+// length is known (the workspace has them for all nsplit runs).
+constexpr int kJoinSlots = 1024;
 template <int DT, bool F8, int D, bool WT>
 __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
   typedef Half<DT> H;
@@ -380,18 +441,33 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
   if (int(blockIdx.x) < heads) {
     const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
     const int hk = hq / a.G, q = hq % a.G;
+    const size_t row = size_t(b * a.Hkv + hk) * a.nsplit * a.G + q;
+    const float2* ml = a.ml + row;
+    constexpr int TR = D / 4, NR = 256 / TR, AHEAD = 4;   // threads a row, rows at once, loads ahead
+    const int r0 = threadIdx.x / TR, d = 4 * (threadIdx.x % TR);
+    const float* o = a.o + row * D + d;
+    const size_t step = size_t(a.G) * D;
+    f32x4 x[AHEAD];
+    float m[AHEAD];
+    const auto fetch = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = min(i0 + u * NR, a.nsplit - 1);
+        x[u] = *reinterpret_cast<const f32x4*>(o + i * step);
+        m[u] = ml[size_t(i) * a.G].x;
+      }
+    };
+    fetch(r0);
     const int len = length_of(a, b);
     if (len <= a.chunk) return;
     const int ns = (len + a.chunk - 1) / a.chunk;
-    const size_t row = size_t(b * a.Hkv + hk) * a.nsplit * a.G + q;
-    const float2* ml = a.ml + row;
     const float2 e = join_sums(ml, ns, a.G, lane);
-    constexpr int TR = D / 4, NR = 256 / TR;   // threads a row, rows at once
-    const int r0 = threadIdx.x / TR, d = 4 * (threadIdx.x % TR);
     f32x4 acc = {0, 0, 0, 0};
-    for (int i = r0; i < ns; i += NR) {
-      const float f = rescale(ml[size_t(i) * a.G].x, e.x);
-      acc += f * *reinterpret_cast<const f32x4*>(a.o + (row + size_t(i) * a.G) * D + d);
+    for (int i0 = r0; i0 < ns; i0 += AHEAD * NR) {
+      if (i0 != r0) fetch(i0);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (i0 + u * NR < ns) acc += rescale(m[u], e.x) * x[u];
     }
     __shared__ f32x4 part[NR][TR];
     part[r0][threadIdx.x % TR] = acc;
@@ -409,14 +485,24 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
     return;
   }
   if constexpr (WT) {
-    const int nb = (a.max_len + 255) / 256;
+    const int nb = (a.max_len + kJoinSlots - 1) / kJoinSlots;
     int id = blockIdx.x - heads;
-    const int j0 = (id % nb) * 256;
+    const int j0 = (id % nb) * kJoinSlots;
     id /= nb;
     const int hk = id % a.Hkv, b = id / a.Hkv;
     const int len = length_of(a, b);
     if (j0 >= len) return;
     const int ns = (len + a.chunk - 1) / a.chunk;
+    // 4 slots a thread (a page holds whole groups of 4); its page and the
+    // first scores do not wait for the sums
+    const int j = j0 + 4 * threadIdx.x;
+    const bool in = j < len;
+    const int p = in ? a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)] : -1;
+    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + (in ? j : 0);
+    constexpr int AHEAD = 8;
+    f32x4 x[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) x[u] = *reinterpret_cast<const f32x4*>(s + min(u, a.G - 1) * a.score_stride);
     // per query head: what is taken off a score, and one over the sum
     __shared__ float ref[kMaxGroup], inv[kMaxGroup];
     for (int q = wave; q < a.G; q += 4) {
@@ -427,37 +513,52 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
       }
     }
     __syncthreads();
-    const int j = j0 + threadIdx.x;
-    if (j >= len) return;
-    const int p = a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)];
     if (unsigned(p) >= unsigned(a.num_pages)) return;
-    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + j;
-    float w = 0.f;
-    for (int q = 0; q < a.G; ++q) w += __builtin_amdgcn_exp2f(s[q * a.score_stride] - ref[q]) * inv[q];
+    f32x4 w = {0, 0, 0, 0};
+    for (int q0 = 0; q0 < a.G; q0 += AHEAD) {
+      if (q0) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+          x[u] = *reinterpret_cast<const f32x4*>(s + min(q0 + u, a.G - 1) * a.score_stride);
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (q0 + u < a.G)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] += __builtin_amdgcn_exp2f(x[u][k] - ref[q0 + u]) * inv[q0 + u];
+    }
     const size_t at = ((size_t(p) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
-    a.weights_out[at] = a.weights[at] + w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j + k < len) a.weights_out[at + k] = a.weights[at + k] + w[k];
   }
 }
 
-template <int DT, int CT, int D>
-void run(const SplitArgs& a, bool wt, hipStream_t s) {
+template <int DT, int CT, int D, bool WT>
+void run_split(const SplitArgs& a, bool wide, hipStream_t s) {
   const unsigned grid = unsigned(a.B) * a.Hkv * a.qtiles * a.nsplit;
-  if (wt) hipLaunchKernelGGL((split_kernel<DT, CT, D, true>), dim3(grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((split_kernel<DT, CT, D, false>), dim3(grid), dim3(256), 0, s, a);
+  if (wide) hipLaunchKernelGGL((split_kernel<DT, CT, D, WT, true>), dim3(grid), dim3(64 * waves(true)), 0, s, a);
+  else hipLaunchKernelGGL((split_kernel<DT, CT, D, WT, false>), dim3(grid), dim3(256), 0, s, a);
+}
+
+template <int DT, int CT, int D>
+void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
+  if (wt) run_split<DT, CT, D, true>(a, wide, s);
+  else run_split<DT, CT, D, false>(a, wide, s);
   const int heads = a.nsplit > 1 ? a.B * a.Hq : 0;
   constexpr bool F8 = CT == GBB_E4M3;
   if (wt) {
-    const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + 255) / 256);
+    const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + kJoinSlots - 1) / kJoinSlots);
     hipLaunchKernelGGL((join_kernel<DT, F8, D, true>), dim3(unsigned(heads) + more), dim3(256), 0, s, a, heads);
   } else if (heads) {
     hipLaunchKernelGGL((join_kernel<DT, F8, D, false>), dim3(unsigned(heads)), dim3(256), 0, s, a, heads);
   }
 }
 template <int DT, int CT>
-void run_dim(const SplitArgs& a, int D, bool wt, hipStream_t s) {
-  if (D == 64) run<DT, CT, 64>(a, wt, s);
-  else if (D == 128) run<DT, CT, 128>(a, wt, s);
-  else run<DT, CT, 256>(a, wt, s);
+void run_dim(const SplitArgs& a, int D, bool wide, bool wt, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, wide, wt, s);
+  else if (D == 128) run<DT, CT, 128>(a, wide, wt, s);
+  else run<DT, CT, 256>(a, wide, wt, s);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
@@ -471,8 +572,10 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   const int64_t pairs = int64_t(B) * c.kv_heads * p.qtiles;
   // the longest run that still gives two workgroups a CU (the register
   // budget's residency); short contexts end at runs of one tile a wave
+  const int64_t cus = device_compute_units();
   int chunk = kMaxChunk;
-  while (chunk > 128 && pairs * ((max_len + chunk - 1) / chunk) < 2 * int64_t(device_compute_units())) chunk /= 2;
+  while (chunk > 128 && pairs * ((max_len + chunk - 1) / chunk) < 2 * cus) chunk /= 2;
+  p.wide = false;
   p.chunk = chunk;
   p.nsplit = std::max(1, (max_len + chunk - 1) / chunk);
   const size_t rows = size_t(B) * Hq * p.nsplit;
@@ -518,11 +621,11 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool wt = x.weights_out != nullptr;
   if (x.dtype == GBB_F16) {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, wt, s);
-    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.wide, wt, s);
   } else {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, wt, s);
-    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.wide, wt, s);
   }
   return int(hipGetLastError());
 }

@@ -134,6 +134,7 @@ int launch_append(const gbb_paged_cache& c, const AppendArgs& a, void* stream);
 constexpr int kMaxGroup = 128;   // query heads per kv head
 struct AttendPlan {
   int chunk, nsplit, qtiles;
+  bool wide;   // workgroups that fill a CU
   size_t ml_off, o_off, s_off, ws_bytes;   // workspace sections
   size_t score_stride;                     // scores per query head (with weights)
 };
