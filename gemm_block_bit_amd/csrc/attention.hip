@@ -46,6 +46,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;   // see above: 2^14 < 65504
+constexpr int kMaxJoin = 64;     // runs that the last workgroup of a sequence joins itself
+constexpr int kMaxArrived = 4096;   // counters of such sequences, at the workspace's start
 constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles x 4 waves x 32 slots
 
 
@@ -104,6 +106,8 @@ struct SplitArgs {
   float* weights_out;
   void* out;
   float* lse;
+  unsigned* arrived;  // [B][Hkv][qtiles] runs of a sequence that are done, 0 between calls; NULL: join_kernel joins
+  float2* heads;    // [B][Hq] with weights: what is taken off a score, one over the sum of exponentials
   float2* ml;       // [B][Hkv][nsplit][G] maximum (log2 domain) and sum
   float* o;         // [B][Hkv][nsplit][G][D]
   float* scores;    // [B][Hkv][G][score_stride], log2 domain
@@ -124,6 +128,16 @@ __device__ __forceinline__ float rescale(float x, float m) {
 // Waves of a workgroup: 4, or 8 (WIDE) for calls with so few runs that a
 // workgroup should have a CU to itself.
 constexpr int waves(bool wide) { return wide ? 8 : 4; }
+
+// Two floats at device scope.
+__device__ __forceinline__ void put(float* p, float x, float y) {
+  const uint64_t v = uint64_t(__builtin_bit_cast(uint32_t, y)) << 32 | __builtin_bit_cast(uint32_t, x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get(const float* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__builtin_bit_cast(float, uint32_t(v)), __builtin_bit_cast(float, uint32_t(v >> 32)));
+}
 
 template <int DT, int CT, int D, bool WT, bool WIDE>
 __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ? 3 : 4) void split_kernel(SplitArgs a) {
@@ -386,28 +400,92 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   __syncthreads();
   const bool whole = len <= a.chunk;
   const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
-  for (int i = threadIdx.x; i < rows * D; i += THREADS) {
-    const int q = i / D, d = i % D;
+  typedef typename H::T V2 __attribute__((ext_vector_type(2)));
+  // out, lse and what the weights take, from the joined sums of a head
+  const auto finish = [&](int q, int d, float m, float l, float o0, float o1) {
+    const size_t head = size_t(b) * a.Hq + hq0 + q;
+    const float f0 = l == 0.f ? 0.f : o0 / l * vs, f1 = l == 0.f ? 0.f : o1 / l * vs;
+    *reinterpret_cast<V2*>(static_cast<typename H::T*>(a.out) + head * D + d) = V2{typename H::T(f0), typename H::T(f1)};
+    if (d == 0) {
+      if (a.lse) a.lse[head] = l == 0.f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
+      if (WT) a.heads[head] = make_float2(m == -INFINITY ? 0.f : m - kShift, l == 0.f ? 0.f : 1.f / l);
+    }
+  };
+  const size_t row0 = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt;
+  for (int i = threadIdx.x; i < rows * (D / 2); i += THREADS) {
+    const int q = i / (D / 2), d = 2 * (i % (D / 2));
     float mm = sm[0][q];
 #pragma unroll
     for (int w = 1; w < NW; ++w) mm = fmaxf(mm, sm[w][q]);
-    float ll = 0.f, oo = 0.f;
+    float ll = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float f = rescale(sm[w][q], mm);
       ll += f * sl[w][q];
-      oo += f * so(w, q, d);
+      o0 += f * so(w, q, d);
+      o1 += f * so(w, q, d + 1);
     }
-    const size_t row = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt + q;
     if (whole) {
-      const size_t head = size_t(b) * a.Hq + hq0 + q;
-      static_cast<typename H::T*>(a.out)[head * D + d] = typename H::T(ll == 0.f ? 0.f : oo / ll * vs);
-      if (d == 0 && a.lse) a.lse[head] = ll == 0.f ? -INFINITY : (mm - kShift + __builtin_amdgcn_logf(ll)) * kLn2;
-      if (WT && d == 0) a.ml[row] = make_float2(mm, ll);
+      finish(q, d, mm, ll, o0, o1);
     } else {
-      a.o[row * D + d] = oo;
-      if (d == 0) a.ml[row] = make_float2(mm, ll);
+      put(a.o + (row0 + q) * D + d, o0, o1);
+      if (d == 0) put(reinterpret_cast<float*>(a.ml + row0 + q), mm, ll);
     }
+  }
+  if (whole || !a.arrived) return;
+
+  // The workgroup that is the last of its sequence to get here joins all
+  // runs, in their order whichever it is.  Partial results are written and
+  // read at device scope (past the caches of the XCDs, which do not see each
+  // other's), every wave awaits its writes before the count, and no
+  // workgroup waits for another.
+  __shared__ unsigned count;
+  loads_left<0>();
+  __syncthreads();
+  unsigned* arrived = a.arrived + (b * a.Hkv + hk) * a.qtiles + qt;
+  if (threadIdx.x == 0) count = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const int ns = (len + a.chunk - 1) / a.chunk;
+  if (count != unsigned(ns - 1)) return;
+  if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const size_t first = size_t(b * a.Hkv + hk) * a.nsplit * a.G + 16 * qt;   // row of run 0
+  float* factor = reinterpret_cast<float*>(lds);   // [kMaxJoin][16], then the joined maxima and sums
+  float* joined = factor + kMaxJoin * 16;
+  for (int q = wave; q < rows; q += NW) {
+    static_assert(kMaxJoin <= 64, "a run a lane");
+    float2 e = make_float2(-INFINITY, 0.f);
+    if (lane < ns) e = get(reinterpret_cast<const float*>(a.ml + first + size_t(lane) * a.G + q));
+    float mm = e.x;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) mm = fmaxf(mm, __shfl_xor(mm, x));
+    const float f = rescale(e.x, mm);
+    float ll = f * e.y;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) ll += __shfl_xor(ll, x);
+    if (lane < kMaxJoin) factor[lane * 16 + q] = f;
+    if (lane == 0) {
+      joined[2 * q] = mm;
+      joined[2 * q + 1] = ll;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 2); i += THREADS) {
+    const int q = i / (D / 2), d = 2 * (i % (D / 2));
+    const float* o = a.o + (first + q) * D + d;
+    float o0 = 0.f, o1 = 0.f;
+    for (int s0 = 0; s0 < ns; s0 += 8) {
+      float2 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = get(o + size_t(min(s0 + u, ns - 1)) * a.G * D);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < ns) {
+          const float f = factor[(s0 + u) * 16 + q];
+          o0 += f * x[u].x;
+          o1 += f * x[u].y;
+        }
+    }
+    finish(q, d, joined[2 * q], joined[2 * q + 1], o0, o1);
   }
 }
 
@@ -428,71 +506,62 @@ __device__ __forceinline__ float2 join_sums(const float2* ml, int ns, int G, int
   return make_float2(mm, ll);
 }
 
-// Joins the runs of every (sequence, query head) in the first `heads`
-// workgroups; the others (with weights) take 1024 slots of a (sequence, kv
-// head) each.  A launch of few short loads: what counts is that the loads do
-// not wait for each other, so those of the first runs are issued before the
-// length is known (the workspace has them for all nsplit runs).
+// Joins the runs of every (sequence, query head), 256 / D to a workgroup and
+// an element a thread, in the first `joining` workgroups; the others (with
+// weights) take 1024 slots of a (sequence, kv head) each.  A launch of few
+// short loads: what counts is that the loads do not wait for each other, so
+// those of the first runs are issued before the length is known (the
+// workspace has them for all nsplit runs).  The sums go run by run, as in
+// split_kernel, and so to the same bits.
 constexpr int kJoinSlots = 1024;
 template <int DT, bool F8, int D, bool WT>
-__global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
+__global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
   typedef Half<DT> H;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  if (int(blockIdx.x) < heads) {
-    const int hq = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
+  if (int(blockIdx.x) < joining) {
+    const int head = uniform(int(blockIdx.x) * (256 / D) + int(threadIdx.x) / D), d = threadIdx.x % D;
+    if (head >= a.B * a.Hq) return;
+    const int hq = head % a.Hq, b = head / a.Hq;
     const int hk = hq / a.G, q = hq % a.G;
     const size_t row = size_t(b * a.Hkv + hk) * a.nsplit * a.G + q;
     const float2* ml = a.ml + row;
-    constexpr int TR = D / 4, NR = 256 / TR, AHEAD = 4;   // threads a row, rows at once, loads ahead
-    const int r0 = threadIdx.x / TR, d = 4 * (threadIdx.x % TR);
+    constexpr int AHEAD = 16;
     const float* o = a.o + row * D + d;
     const size_t step = size_t(a.G) * D;
-    f32x4 x[AHEAD];
-    float m[AHEAD];
+    float x[AHEAD], m[AHEAD];
     const auto fetch = [&](int i0) {
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
-        const int i = min(i0 + u * NR, a.nsplit - 1);
-        x[u] = *reinterpret_cast<const f32x4*>(o + i * step);
+        const int i = min(i0 + u, a.nsplit - 1);
+        x[u] = o[i * step];
         m[u] = ml[size_t(i) * a.G].x;
       }
     };
-    fetch(r0);
+    fetch(0);
     const int len = length_of(a, b);
     if (len <= a.chunk) return;
     const int ns = (len + a.chunk - 1) / a.chunk;
     const float2 e = join_sums(ml, ns, a.G, lane);
-    f32x4 acc = {0, 0, 0, 0};
-    for (int i0 = r0; i0 < ns; i0 += AHEAD * NR) {
-      if (i0 != r0) fetch(i0);
+    float acc = 0.f;
+    for (int i0 = 0; i0 < ns; i0 += AHEAD) {
+      if (i0) fetch(i0);
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
-        if (i0 + u * NR < ns) acc += rescale(m[u], e.x) * x[u];
+        if (i0 + u < ns) acc += rescale(m[u], e.x) * x[u];
     }
-    __shared__ f32x4 part[NR][TR];
-    part[r0][threadIdx.x % TR] = acc;
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float oo = 0.f;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) oo += part[r][threadIdx.x / 4][threadIdx.x % 4];
-      const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
-      const size_t head = size_t(b) * a.Hq + hq;
-      static_cast<typename H::T*>(a.out)[head * D + threadIdx.x] = typename H::T(e.y == 0.f ? 0.f : oo / e.y * vs);
-      if (threadIdx.x == 0 && a.lse)
-        a.lse[head] = e.y == 0.f ? -INFINITY : (e.x - kShift + __builtin_amdgcn_logf(e.y)) * kLn2;
-    }
+    const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+    static_cast<typename H::T*>(a.out)[size_t(head) * D + d] = typename H::T(e.y == 0.f ? 0.f : acc / e.y * vs);
+    if (d == 0 && a.lse) a.lse[head] = e.y == 0.f ? -INFINITY : (e.x - kShift + __builtin_amdgcn_logf(e.y)) * kLn2;
     return;
   }
   if constexpr (WT) {
     const int nb = (a.max_len + kJoinSlots - 1) / kJoinSlots;
-    int id = blockIdx.x - heads;
+    int id = blockIdx.x - joining;
     const int j0 = (id % nb) * kJoinSlots;
     id /= nb;
     const int hk = id % a.Hkv, b = id / a.Hkv;
     const int len = length_of(a, b);
     if (j0 >= len) return;
-    const int ns = (len + a.chunk - 1) / a.chunk;
     // 4 slots a thread (a page holds whole groups of 4); its page and the
     // first scores do not wait for the sums
     const int j = j0 + 4 * threadIdx.x;
@@ -505,11 +574,20 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int heads) {
     for (int u = 0; u < AHEAD; ++u) x[u] = *reinterpret_cast<const f32x4*>(s + min(u, a.G - 1) * a.score_stride);
     // per query head: what is taken off a score, and one over the sum
     __shared__ float ref[kMaxGroup], inv[kMaxGroup];
-    for (int q = wave; q < a.G; q += 4) {
-      const float2 e = join_sums(a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G + q, ns, a.G, lane);
-      if (lane == 0) {
-        ref[q] = e.x == -INFINITY ? 0.f : e.x - kShift;
-        inv[q] = e.y == 0.f ? 0.f : 1.f / e.y;
+    if (a.arrived || len <= a.chunk) {
+      for (int q = threadIdx.x; q < a.G; q += 256) {
+        const float2 e = a.heads[size_t(b) * a.Hq + size_t(hk) * a.G + q];
+        ref[q] = e.x;
+        inv[q] = e.y;
+      }
+    } else {
+      const int ns = (len + a.chunk - 1) / a.chunk;
+      for (int q = wave; q < a.G; q += 4) {
+        const float2 e = join_sums(a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G + q, ns, a.G, lane);
+        if (lane == 0) {
+          ref[q] = e.x == -INFINITY ? 0.f : e.x - kShift;
+          inv[q] = e.y == 0.f ? 0.f : 1.f / e.y;
+        }
       }
     }
     __syncthreads();
@@ -542,10 +620,10 @@ void run_split(const SplitArgs& a, bool wide, hipStream_t s) {
 }
 
 template <int DT, int CT, int D>
-void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
+void run(const SplitArgs& a, bool wide, bool joins, bool wt, hipStream_t s) {
   if (wt) run_split<DT, CT, D, true>(a, wide, s);
   else run_split<DT, CT, D, false>(a, wide, s);
-  const int heads = a.nsplit > 1 ? a.B * a.Hq : 0;
+  const int heads = joins || a.nsplit == 1 ? 0 : (a.B * a.Hq + 256 / D - 1) / (256 / D);
   constexpr bool F8 = CT == GBB_E4M3;
   if (wt) {
     const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + kJoinSlots - 1) / kJoinSlots);
@@ -555,10 +633,10 @@ void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
   }
 }
 template <int DT, int CT>
-void run_dim(const SplitArgs& a, int D, bool wide, bool wt, hipStream_t s) {
-  if (D == 64) run<DT, CT, 64>(a, wide, wt, s);
-  else if (D == 128) run<DT, CT, 128>(a, wide, wt, s);
-  else run<DT, CT, 256>(a, wide, wt, s);
+void run_dim(const SplitArgs& a, int D, bool wide, bool joins, bool wt, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, wide, joins, wt, s);
+  else if (D == 128) run<DT, CT, 128>(a, wide, joins, wt, s);
+  else run<DT, CT, 256>(a, wide, joins, wt, s);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
@@ -570,19 +648,38 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   const int G = Hq / c.kv_heads;
   p.qtiles = (G + 15) / 16;
   const int64_t pairs = int64_t(B) * c.kv_heads * p.qtiles;
-  // the longest run that still gives two workgroups a CU (the register
-  // budget's residency); short contexts end at runs of one tile a wave
+  // Runs.  Short contexts, and those of calls whose (sequence, kv head) pairs
+  // fill the chip, stay whole: a run costs about 1.5 us of a CU beside its
+  // bytes and its partial results have to be joined (256 pairs of 4000 slots:
+  // 93 us whole, 97 and 100 in runs of 2048 and 1024).  Else the longest run
+  // that gives every CU a workgroup (8 pairs of 32768 slots: 31 us in runs of
+  // 1024, 48 in 4096, 36 in 512), of at most 2048 slots so that ragged
+  // lengths balance (32 ragged of up to 8192: 105 us, 114 in 4096), and at
+  // most 16 runs below 1024 (4 pairs of 16 query heads and 8192 slots: 14 us
+  // in 512, 22 in 128); contexts above 16384 have runs enough to balance at
+  // 4096 (2 of 131072: 102 us, 105 in 2048).  Eight waves a workgroup where it has work for them
+  // (1152 ragged pairs of up to 2047 slots: 63 against 69 us), four for
+  // short runs (2048 pairs of 256: 51 against 58 us).
   const int64_t cus = device_compute_units();
   int chunk = kMaxChunk;
-  while (chunk > 128 && pairs * ((max_len + chunk - 1) / chunk) < 2 * cus) chunk /= 2;
-  p.wide = false;
+  if (max_len <= 512 || (pairs >= cus && max_len <= kMaxChunk)) {
+    p.wide = pairs < cus || max_len >= 1024;
+  } else {
+    if (max_len <= 16384) chunk = 2048;
+    const int least = max_len <= 128 * 16 ? 128 : max_len <= 256 * 16 ? 256 : max_len <= 512 * 16 ? 512 : 1024;
+    while (chunk > least && pairs * ((max_len + chunk - 1) / chunk) < cus) chunk /= 2;
+    p.wide = chunk >= 512;
+  }
   p.chunk = chunk;
   p.nsplit = std::max(1, (max_len + chunk - 1) / chunk);
   const size_t rows = size_t(B) * Hq * p.nsplit;
   p.score_stride = (size_t(max_len) + 31) & ~size_t(31);
   const bool parts = p.nsplit > 1;
-  p.ml_off = 0;
-  p.o_off = parts || with_weights ? up(rows * sizeof(float2)) : 0;
+  // one launch where the last workgroup of a sequence can join its runs
+  p.joins = !with_weights && (!parts || (p.nsplit <= kMaxJoin && pairs <= kMaxArrived));
+  p.heads_off = parts || with_weights ? kMaxArrived * sizeof(unsigned) : 0;   // nothing else lies on the counters
+  p.ml_off = p.heads_off + (with_weights ? up(size_t(B) * Hq * sizeof(float2)) : 0);
+  p.o_off = p.ml_off + (parts ? up(rows * sizeof(float2)) : 0);
   p.s_off = p.o_off + (parts ? up(rows * c.head_dim * sizeof(float)) : 0);
   p.ws_bytes = p.s_off + (with_weights ? up(size_t(B) * Hq * p.score_stride * sizeof(float)) : 0);
   return p;
@@ -601,6 +698,8 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   a.weights_out = x.weights_out;
   a.out = x.out;
   a.lse = x.lse;
+  a.arrived = p.joins && p.nsplit > 1 ? reinterpret_cast<unsigned*>(x.ws) : nullptr;
+  a.heads = reinterpret_cast<float2*>(x.ws + p.heads_off);
   a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
   a.o = reinterpret_cast<float*>(x.ws + p.o_off);
   a.scores = reinterpret_cast<float*>(x.ws + p.s_off);
@@ -621,11 +720,11 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool wt = x.weights_out != nullptr;
   if (x.dtype == GBB_F16) {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
-    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.wide, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.wide, p.joins, wt, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.wide, p.joins, wt, s);
   } else {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
-    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.wide, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.wide, p.joins, wt, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.wide, p.joins, wt, s);
   }
   return int(hipGetLastError());
 }

@@ -97,14 +97,14 @@ gbb_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 // Shapes alone, for the workspace queries (launch sizes included).
-gbb_status check_attend_shape(const gbb_paged_cache* c, int B, int q_heads, int max_len) {
+gbb_status check_attend_shape(const gbb_paged_cache* c, int B, int q_heads, int max_len, bool with_weights, AttendPlan& p) {
   gbb_status st = check_cache(c);
   if (st != GBB_OK) return st;
   if ((st = check_heads(c, q_heads)) != GBB_OK) return st;
   if (B < 0 || max_len < 1 || max_len > INT_MAX - 8192) return fail(GBB_E_ARG, "bad B or max_len (%d, %d)", B, max_len);
   if (int64_t(B) * q_heads > kMaxGroups) return fail(GBB_E_SHAPE, "B * q_heads exceeds %d", int(kMaxGroups));
   if (B) {
-    const AttendPlan p = attend_plan(*c, B, q_heads, max_len, false);
+    p = attend_plan(*c, B, q_heads, max_len, with_weights);
     const int64_t pairs = int64_t(B) * c->kv_heads;
     if (pairs * p.qtiles > kMaxGroups / p.nsplit || pairs > kMaxGroups / (1 + max_len / 256))
       return fail(GBB_E_SHAPE, "B=%d, kv_heads=%d and max_len=%d make too many workgroups", B, c->kv_heads, max_len);
@@ -175,15 +175,17 @@ extern "C" gbb_status gbb_rope_append(const gbb_paged_cache* cache, const void* 
 
 extern "C" size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_heads, int max_len,
                                                 int with_weights) {
-  if (check_attend_shape(cache, B, q_heads, max_len) != GBB_OK || B == 0) return 0;
-  return attend_plan(*cache, B, q_heads, max_len, with_weights != 0).ws_bytes;
+  AttendPlan p;
+  if (check_attend_shape(cache, B, q_heads, max_len, with_weights != 0, p) != GBB_OK || B == 0) return 0;
+  return p.ws_bytes;
 }
 
 extern "C" gbb_status gbb_paged_attention(const gbb_paged_cache* cache, const void* q, int64_t q_token, int dtype,
                                           int B, int q_heads, const int32_t* block_table, int max_pages,
                                           const int32_t* lengths, int max_len, float scale, void* out, float* lse,
                                           float* weights_out, void* workspace, size_t ws_bytes, void* stream) {
-  gbb_status st = check_attend_shape(cache, B, q_heads, max_len);
+  AttendPlan p;
+  gbb_status st = check_attend_shape(cache, B, q_heads, max_len, weights_out != nullptr, p);
   if (st != GBB_OK) return st;
   if ((st = check_dtype(cache, dtype)) != GBB_OK) return st;
   if ((st = check_sequences(cache, B, block_table, max_pages, lengths, max_len)) != GBB_OK) return st;
@@ -198,7 +200,6 @@ extern "C" gbb_status gbb_paged_attention(const gbb_paged_cache* cache, const vo
   if (!aligned(lse, 4) || !aligned(weights_out, 4)) return fail(GBB_E_ALIGN, "lse or weights_out is misaligned");
   if (weights_out && !cache->weights) return fail(GBB_E_ARG, "weights_out needs a cache with weights");
   if (overlap(q, (size_t(B - 1) * q_token + row) * 2, out, size_t(B) * row * 2)) return fail(GBB_E_ARG, "q and out overlap");
-  const AttendPlan p = attend_plan(*cache, B, q_heads, max_len, weights_out != nullptr);
   if ((st = check_workspace(workspace, ws_bytes, p.ws_bytes)) != GBB_OK) return st;
   const AttendArgs a = {q, q_token, block_table, lengths, out, lse, weights_out, static_cast<char*>(workspace), B,
                         q_heads, max_pages, max_len, dtype, scale};

@@ -17,7 +17,7 @@ import ctypes
 
 import numpy as np
 
-from .binding import _check, _dev_ptr, _np_ptr, _PagedCache, _RopeScaling, _stream, _torch, lib
+from .binding import _check, _dev_ptr, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
@@ -40,17 +40,36 @@ def _layout(layout: str) -> int:
     return _LAYOUTS[layout]
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _ptr(t, dtype, device: int, name: str, shape=None):
+    """Address of a contiguous tensor of `dtype` on GPU `device`.  These
+    checks are on the path of calls that take a few microseconds, so the
+    messages are left to _refuse."""
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != device or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        _refuse(t, dtype, device, name, shape)
+    return t.data_ptr()
 
 
-def _ints(t, shape, name):
-    p = _dev_ptr(t, _torch().int32, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be int32 {list(shape)}, got {list(t.shape)}")
-    return p
+def _refuse(t, dtype, device, name, shape):
+    _dev_ptr(t, dtype, name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
+
+
+def _device_of(t, name) -> int:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a torch tensor on a GPU")
+    return t.get_device()
+
+
+def _raw_stream(device: int) -> int:
+    """torch's current stream of a GPU as a hipStream_t, by the accessor that
+    torch's own generated code uses (the public one builds two Python objects
+    for every call, 2 us)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 # ----------------------------------------------------------------------------
@@ -69,11 +88,11 @@ def rope_table(rot: int, n_pos: int, base: float = 10000.0, scaling: str = "plai
 
 
 def _table(table, device):
-    p = _dev_ptr(table, _torch().float32, "table")
-    if table.dim() != 3 or table.shape[2] != 2:
+    p = _ptr(table, _torch().float32, device, "table")
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
         raise ValueError("table must be float32 [n_pos][rot/2][2]")
-    _same_device(device, table=table)
-    return p, table.shape[0], 2 * table.shape[1]
+    return p, shape[0], 2 * shape[1]
 
 
 def rope(x, positions, table, layout: str = "half", transpose: bool = False, out=None):
@@ -83,20 +102,23 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
     contiguous tensor.  transpose: the transposed rotation, which is the
     gradient with respect to x."""
     torch = _torch()
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
-        raise TypeError("x must be a torch tensor on a GPU")
+    device = _device_of(x, "x")
     if x.dim() != 3 or x.stride(2) != 1:
         raise ValueError("x must be [T][H][D] with contiguous heads")
     T, H, D = x.shape
-    y = out if out is not None else torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    if y.dtype != x.dtype or y.shape != x.shape or y.stride(2) != 1:
-        raise ValueError("out must be like x, with contiguous heads")
-    _same_device(x.device, out=y, positions=positions)
-    tp, n_pos, rot = _table(table, x.device)
+    if out is None:
+        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    else:
+        y = out
+        if y.dtype != x.dtype or y.shape != x.shape or y.stride(2) != 1:
+            raise ValueError("out must be like x, with contiguous heads")
+        if y.get_device() != device:
+            raise ValueError(f"out is on {y.device}, not on {x.device}")
+    tp, n_pos, rot = _table(table, device)
     xs, ys = x.stride(), y.stride()
     _check(lib().gbb_rope(x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H, D,
-                          _ints(positions, (T,), "positions"), tp, n_pos, rot, _layout(layout), int(transpose),
-                          _stream(x)))
+                          _ptr(positions, torch.int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout),
+                          int(transpose), _raw_stream(device)))
     return y
 
 
@@ -118,24 +140,19 @@ class PagedCache:
         self.weights, self.positions = weights, positions
         self.device, self.dtype = k.device, k.dtype
         self.num_pages, self.kv_heads, self.page, self.head_dim = k.shape
-        _same_device(k.device, v=v, k_scale=k_scale, v_scale=v_scale, weights=weights, positions=positions)
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is not None and tuple(t.shape) != (self.kv_heads,):
-                raise ValueError(f"{name} must be float32 [{self.kv_heads}]")
-        for name, t in (("weights", weights), ("positions", positions)):
-            if t is not None and t.shape != k.shape[:3]:
-                raise ValueError(f"{name} must be {list(k.shape[:3])}")
-
-        def ptr(t, dtype, name):
-            return None if t is None else _dev_ptr(t, dtype, name)
-
         code = _dtype_code(k.dtype)
         if code == 2:
             raise TypeError("a cache holds float16, bfloat16 or float8_e4m3fn")
-        self._c = _PagedCache(ptr(k, k.dtype, "k"), ptr(v, v.dtype, "v"), ptr(k_scale, torch.float32, "k_scale"),
-                              ptr(v_scale, torch.float32, "v_scale"), ptr(weights, torch.float32, "weights"),
-                              ptr(positions, torch.int32, "positions"), code, self.num_pages, self.page,
-                              self.kv_heads, self.head_dim)
+        self._index = _device_of(k, "k")
+
+        def ptr(t, dtype, name, shape):
+            return None if t is None else _ptr(t, dtype, self._index, name, shape)
+
+        one, slots = (self.kv_heads,), tuple(k.shape[:3])
+        self._c = _PagedCache(ptr(k, k.dtype, "k", None), ptr(v, v.dtype, "v", None),
+                              ptr(k_scale, torch.float32, "k_scale", one), ptr(v_scale, torch.float32, "v_scale", one),
+                              ptr(weights, torch.float32, "weights", slots), ptr(positions, torch.int32, "positions", slots),
+                              code, self.num_pages, self.page, self.kv_heads, self.head_dim)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -151,29 +168,31 @@ class PagedCache:
         p = torch.full(shape[:3], -1, dtype=torch.int32, device=device) if tracked else None
         return cls(k, v, k_scale, v_scale, w, p)
 
-    def _state(self, t, like, name):
-        """Pointer of an output like the cache's weights or positions."""
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must be {list(like.shape)}")
-        _same_device(self.device, **{name: t})
-        return _dev_ptr(t, like.dtype, name)
-
 
 _ws_cache: dict = {}
+_E_SPACE = -5
 
 
-def _workspace(kind: str, device, nbytes: int):
-    """A device buffer per use, device and stream, zero when it is new.  Kept
-    apart from the buffer of the gemm calls, which has to stay zero."""
+def _with_workspace(kind: str, device: int, stream: int, given, call, need):
+    """call(pointer, bytes) -> status with the caller's workspace, or with a
+    buffer kept per use, device and stream (zero when it is new; kept apart
+    from the buffer of the gemm calls, which has to stay zero).  need() is
+    only asked when a call says that the buffer is too small."""
+    if given is not None:
+        if given.get_device() != device:
+            raise ValueError(f"workspace is on {given.device}, not on GPU {device}")
+        _check(call(given.data_ptr(), given.numel() * given.element_size()))
+        return
     torch = _torch()
-    if nbytes == 0:
-        return None
-    key = (kind, device, torch.cuda.current_stream(device).cuda_stream)
+    key = (kind, device, stream)
     buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
+    if buf is None:
+        buf = _ws_cache[key] = torch.zeros(1 << 20, dtype=torch.uint8, device=torch.device("cuda", device))
+    st = call(buf.data_ptr(), buf.numel())
+    if st == _E_SPACE:
+        buf = _ws_cache[key] = torch.zeros(need(), dtype=torch.uint8, device=buf.device)
+        st = call(buf.data_ptr(), buf.numel())
+    _check(st)
 
 
 def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, layout: str = "half", out=None):
@@ -181,21 +200,20 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
     (rows may be strided), writes k and v to the cache's int32 slots [T] and
     returns q [T][q_heads][head size] (see gbb_rope_append)."""
     torch = _torch()
-    if not isinstance(qkv, torch.Tensor) or qkv.device.type != "cuda":
-        raise TypeError("qkv must be a torch tensor on a GPU")
-    width = (q_heads + 2 * cache.kv_heads) * cache.head_dim
+    device = cache._index
+    if _device_of(qkv, "qkv") != device:
+        raise ValueError(f"qkv is on {qkv.device}, not on GPU {device}")
+    D = cache.head_dim
+    width = (q_heads + 2 * cache.kv_heads) * D
     if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
         raise ValueError(f"qkv must be [T][{width}] with contiguous rows")
     T = qkv.shape[0]
-    q = out if out is not None else torch.empty((T, q_heads, cache.head_dim), dtype=qkv.dtype, device=qkv.device)
-    if tuple(q.shape) != (T, q_heads, cache.head_dim):
-        raise ValueError(f"out must be [{T}][{q_heads}][{cache.head_dim}]")
-    _same_device(cache.device, qkv=qkv, out=q, positions=positions, slots=slots)
-    tp, n_pos, rot = _table(table, cache.device)
-    stride = qkv.stride(0) if T > 1 else width
-    _check(lib().gbb_rope_append(cache._ref, qkv.data_ptr(), stride, _dtype_code(qkv.dtype), T, q_heads,
-                                 _ints(positions, (T,), "positions"), _ints(slots, (T,), "slots"), tp, n_pos, rot,
-                                 _layout(layout), _dev_ptr(q, qkv.dtype, "out"), _stream(qkv)))
+    q = out if out is not None else torch.empty((T, q_heads, D), dtype=qkv.dtype, device=qkv.device)
+    tp, n_pos, rot = _table(table, device)
+    _check(lib().gbb_rope_append(
+        cache._ref, qkv.data_ptr(), qkv.stride(0) if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
+        _ptr(positions, torch.int32, device, "positions", (T,)), _ptr(slots, torch.int32, device, "slots", (T,)), tp,
+        n_pos, rot, _layout(layout), _ptr(q, qkv.dtype, device, "out", (T, q_heads, D)), _raw_stream(device)))
     return q
 
 
@@ -213,35 +231,30 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     weights with this step's added (cache.weights itself for in place).
     Returns [B][q_heads][head size] (see gbb_paged_attention)."""
     torch = _torch()
-    if not isinstance(q, torch.Tensor) or q.device.type != "cuda":
-        raise TypeError("q must be a torch tensor on a GPU")
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.stride(2) != 1 or q.stride(1) != cache.head_dim:
-        raise ValueError(f"q must be [B][q_heads][{cache.head_dim}] with contiguous tokens")
-    B, q_heads = q.shape[0], q.shape[1]
-    o = out if out is not None else torch.empty((B, q_heads, cache.head_dim), dtype=q.dtype, device=q.device)
-    if o.shape != q.shape:
-        raise ValueError(f"out must be {list(q.shape)}")
+    device, D = cache._index, cache.head_dim
+    if _device_of(q, "q") != device:
+        raise ValueError(f"q is on {q.device}, not on GPU {device}")
+    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
+        raise ValueError(f"q must be [B][q_heads][{D}] with contiguous tokens")
+    shape = q.shape
+    B, q_heads = shape[0], shape[1]
+    o = out if out is not None else torch.empty(shape, dtype=q.dtype, device=q.device)
+    bt = _ptr(block_table, torch.int32, device, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}][pages]")
-    _same_device(cache.device, q=q, out=o, block_table=block_table, lengths=lengths, lse=lse, workspace=workspace)
-    if lse is not None and tuple(lse.shape) != (B, q_heads):
-        raise ValueError(f"lse must be float32 [{B}][{q_heads}]")
     w = None
     if weights_out is not None:
         if cache.weights is None:
             raise ValueError("the cache has no weights")
-        w = cache._state(weights_out, cache.weights, "weights_out")
-    L = lib()
-    ws = workspace
-    if ws is None:
-        ws = _workspace("attention", cache.device,
-                        L.gbb_paged_attention_workspace(cache._ref, B, q_heads, max_len, int(w is not None)))
-    _check(L.gbb_paged_attention(
-        cache._ref, q.data_ptr(), q.stride(0), _dtype_code(q.dtype), B, q_heads,
-        _dev_ptr(block_table, torch.int32, "block_table"), block_table.shape[1], _ints(lengths, (B,), "lengths"),
-        max_len, cache.head_dim ** -0.5 if scale is None else scale, _dev_ptr(o, q.dtype, "out"),
-        _dev_ptr(lse, torch.float32, "lse") if lse is not None else None, w,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream(q)))
+        w = _ptr(weights_out, torch.float32, device, "weights_out", cache.weights.shape)
+    L, stream = lib(), _raw_stream(device)
+    args = (cache._ref, q.data_ptr(), q.stride(0), _dtype_code(q.dtype), B, q_heads, bt, block_table.shape[1],
+            _ptr(lengths, torch.int32, device, "lengths", (B,)), max_len, D ** -0.5 if scale is None else scale,
+            _ptr(o, q.dtype, device, "out", shape),
+            _ptr(lse, torch.float32, device, "lse", (B, q_heads)) if lse is not None else None, w)
+    _with_workspace("attention", device, stream, workspace,
+                    lambda ws, n: L.gbb_paged_attention(*args, ws, n, stream),
+                    lambda: L.gbb_paged_attention_workspace(cache._ref, B, q_heads, max_len, int(w is not None)))
     return o
 
 
@@ -258,19 +271,18 @@ def cache_evict(cache: PagedCache, block_table, lengths, max_len: int, budget: i
     torch = _torch()
     if cache.weights is None or cache.positions is None:
         raise ValueError("eviction needs a cache with weights and positions")
-    B = block_table.shape[0]
+    device = cache._index
+    bt = _ptr(block_table, torch.int32, device, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][pages]")
+    B, pages = block_table.shape
     n = lengths_out if lengths_out is not None else torch.empty((B,), dtype=torch.int32, device=cache.device)
-    _same_device(cache.device, block_table=block_table, lengths=lengths, lengths_out=n, workspace=workspace)
-    w = cache._c.weights if weights_out is None else cache._state(weights_out, cache.weights, "weights_out")
-    p = cache._c.positions if positions_out is None else cache._state(positions_out, cache.positions, "positions_out")
-    L = lib()
-    ws = workspace
-    if ws is None:
-        ws = _workspace("evict", cache.device, L.gbb_cache_evict_workspace(cache._ref, B, max_len, budget))
-    _check(L.gbb_cache_evict(
-        cache._ref, B, _dev_ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
-        _ints(lengths, (B,), "lengths"), max_len, budget, recent, _ints(n, (B,), "lengths_out"), w, p,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream(cache.k)))
+    shape = cache.weights.shape
+    w = cache._c.weights if weights_out is None else _ptr(weights_out, torch.float32, device, "weights_out", shape)
+    p = cache._c.positions if positions_out is None else _ptr(positions_out, torch.int32, device, "positions_out", shape)
+    L, stream = lib(), _raw_stream(device)
+    args = (cache._ref, B, bt, pages, _ptr(lengths, torch.int32, device, "lengths", (B,)), max_len, budget, recent,
+            _ptr(n, torch.int32, device, "lengths_out", (B,)), w, p)
+    _with_workspace("evict", device, stream, workspace, lambda ws, size: L.gbb_cache_evict(*args, ws, size, stream),
+                    lambda: L.gbb_cache_evict_workspace(cache._ref, B, max_len, budget))
     return n
