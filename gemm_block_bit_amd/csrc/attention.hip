@@ -107,7 +107,6 @@ struct SplitArgs {
   void* out;
   float* lse;
   unsigned* arrived;  // [B][Hkv][qtiles] runs of a sequence that are done, 0 between calls; NULL: join_kernel joins
-  float2* heads;    // [B][Hq] with weights: what is taken off a score, one over the sum of exponentials
   float2* ml;       // [B][Hkv][nsplit][G] maximum (log2 domain) and sum
   float* o;         // [B][Hkv][nsplit][G][D]
   float* scores;    // [B][Hkv][G][score_stride], log2 domain
@@ -401,14 +400,13 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   const bool whole = len <= a.chunk;
   const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
   typedef typename H::T V2 __attribute__((ext_vector_type(2)));
-  // out, lse and what the weights take, from the joined sums of a head
+  // out and lse from the joined sums of a head
   const auto finish = [&](int q, int d, float m, float l, float o0, float o1) {
     const size_t head = size_t(b) * a.Hq + hq0 + q;
     const float f0 = l == 0.f ? 0.f : o0 / l * vs, f1 = l == 0.f ? 0.f : o1 / l * vs;
     *reinterpret_cast<V2*>(static_cast<typename H::T*>(a.out) + head * D + d) = V2{typename H::T(f0), typename H::T(f1)};
     if (d == 0) {
       if (a.lse) a.lse[head] = l == 0.f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
-      if (WT) a.heads[head] = make_float2(m == -INFINITY ? 0.f : m - kShift, l == 0.f ? 0.f : 1.f / l);
     }
   };
   const size_t row0 = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt;
@@ -427,6 +425,7 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
     }
     if (whole) {
       finish(q, d, mm, ll, o0, o1);
+      if (WT && d == 0) a.ml[row0 + q] = make_float2(mm, ll);
     } else {
       put(a.o + (row0 + q) * D + d, o0, o1);
       if (d == 0) put(reinterpret_cast<float*>(a.ml + row0 + q), mm, ll);
@@ -490,8 +489,12 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
 }
 
 // Maximum and sum of a query head over its ns runs, the same in all 64 lanes.
-__device__ __forceinline__ float2 join_sums(const float2* ml, int ns, int G, int lane) {
-  const float2 e = lane < ns ? ml[size_t(lane) * G] : make_float2(-INFINITY, 0.f);
+// e: lane i's run i, loaded before ns was known (first_runs).
+__device__ __forceinline__ float2 first_runs(const float2* ml, const SplitArgs& a, int lane) {
+  return ml[size_t(min(lane, a.nsplit - 1)) * a.G];
+}
+__device__ __forceinline__ float2 join_sums(float2 e, const float2* ml, int ns, int G, int lane) {
+  if (lane >= ns) e = make_float2(-INFINITY, 0.f);
   float mm = e.x, ll = 0.f;
   for (int i = lane + 64; i < ns; i += 64) mm = fmaxf(mm, ml[size_t(i) * G].x);
 #pragma unroll
@@ -538,10 +541,12 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
       }
     };
     fetch(0);
+    const float2 first = first_runs(ml, a, lane);
+    in_order();
     const int len = length_of(a, b);
     if (len <= a.chunk) return;
     const int ns = (len + a.chunk - 1) / a.chunk;
-    const float2 e = join_sums(ml, ns, a.G, lane);
+    const float2 e = join_sums(first, ml, ns, a.G, lane);
     float acc = 0.f;
     for (int i0 = 0; i0 < ns; i0 += AHEAD) {
       if (i0) fetch(i0);
@@ -560,38 +565,35 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
     const int j0 = (id % nb) * kJoinSlots;
     id /= nb;
     const int hk = id % a.Hkv, b = id / a.Hkv;
+    // 4 slots a thread (a page holds whole groups of 4)
+    const int j = j0 + 4 * threadIdx.x;
+    const int p = a.block_table[size_t(b) * a.max_pages + (min(j, a.max_len - 1) >> a.pshift)];
+    const float2* ml = a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G;
+    const float2 first = first_runs(ml + min(wave, a.G - 1), a, lane);
+    in_order();
     const int len = length_of(a, b);
     if (j0 >= len) return;
-    // 4 slots a thread (a page holds whole groups of 4); its page and the
-    // first scores do not wait for the sums
-    const int j = j0 + 4 * threadIdx.x;
-    const bool in = j < len;
-    const int p = in ? a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)] : -1;
-    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + (in ? j : 0);
+    const bool there = j < len && unsigned(p) < unsigned(a.num_pages);
+    const size_t at = ((size_t(there ? p : 0) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
+    const f32x4 old = *reinterpret_cast<const f32x4*>(a.weights + at);
+    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + (there ? j : 0);
     constexpr int AHEAD = 8;
     f32x4 x[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) x[u] = *reinterpret_cast<const f32x4*>(s + min(u, a.G - 1) * a.score_stride);
+    in_order();
     // per query head: what is taken off a score, and one over the sum
     __shared__ float ref[kMaxGroup], inv[kMaxGroup];
-    if (a.arrived || len <= a.chunk) {
-      for (int q = threadIdx.x; q < a.G; q += 256) {
-        const float2 e = a.heads[size_t(b) * a.Hq + size_t(hk) * a.G + q];
-        ref[q] = e.x;
-        inv[q] = e.y;
-      }
-    } else {
-      const int ns = (len + a.chunk - 1) / a.chunk;
-      for (int q = wave; q < a.G; q += 4) {
-        const float2 e = join_sums(a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G + q, ns, a.G, lane);
-        if (lane == 0) {
-          ref[q] = e.x == -INFINITY ? 0.f : e.x - kShift;
-          inv[q] = e.y == 0.f ? 0.f : 1.f / e.y;
-        }
+    const int ns = (len + a.chunk - 1) / a.chunk;
+    for (int q = wave; q < a.G; q += 4) {
+      const float2 e = join_sums(q == wave ? first : first_runs(ml + q, a, lane), ml + q, ns, a.G, lane);
+      if (lane == 0) {
+        ref[q] = e.x == -INFINITY ? 0.f : e.x - kShift;
+        inv[q] = e.y == 0.f ? 0.f : 1.f / e.y;
       }
     }
     __syncthreads();
-    if (unsigned(p) >= unsigned(a.num_pages)) return;
+    if (!there) return;
     f32x4 w = {0, 0, 0, 0};
     for (int q0 = 0; q0 < a.G; q0 += AHEAD) {
       if (q0) {
@@ -605,10 +607,9 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[k] += __builtin_amdgcn_exp2f(x[u][k] - ref[q0 + u]) * inv[q0 + u];
     }
-    const size_t at = ((size_t(p) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (j + k < len) a.weights_out[at + k] = a.weights[at + k] + w[k];
+      if (j + k < len) a.weights_out[at + k] = old[k] + w[k];
   }
 }
 
@@ -653,13 +654,14 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   // bytes and its partial results have to be joined (256 pairs of 4000 slots:
   // 93 us whole, 97 and 100 in runs of 2048 and 1024).  Else the longest run
   // that gives every CU a workgroup (8 pairs of 32768 slots: 31 us in runs of
-  // 1024, 48 in 4096, 36 in 512), of at most 2048 slots so that ragged
-  // lengths balance (32 ragged of up to 8192: 105 us, 114 in 4096), and at
-  // most 16 runs below 1024 (4 pairs of 16 query heads and 8192 slots: 14 us
-  // in 512, 22 in 128); contexts above 16384 have runs enough to balance at
-  // 4096 (2 of 131072: 102 us, 105 in 2048).  Eight waves a workgroup where it has work for them
-  // (1152 ragged pairs of up to 2047 slots: 63 against 69 us), four for
-  // short runs (2048 pairs of 256: 51 against 58 us).
+  // 1024, 48 in 4096, 36 in 512).  It has at most 2048 slots, so that ragged
+  // lengths balance (32 ragged of up to 8192: 105 us, 114 in 4096), but above
+  // 16384 there are runs enough for that in 4096 (2 of 131072: 102 us, 105 in
+  // 2048); and below 1024 at most 16 runs are made (4 pairs of 16 query heads
+  // and 8192 slots: 14 us in 512, 22 in 128).
+  // Eight waves a workgroup where it has work for them (1152 ragged pairs of
+  // up to 2047 slots: 63 against 69 us), four for short runs (2048 pairs of
+  // 256: 51 against 58 us).
   const int64_t cus = device_compute_units();
   int chunk = kMaxChunk;
   if (max_len <= 512 || (pairs >= cus && max_len <= kMaxChunk)) {
@@ -677,9 +679,8 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   const bool parts = p.nsplit > 1;
   // one launch where the last workgroup of a sequence can join its runs
   p.joins = !with_weights && (!parts || (p.nsplit <= kMaxJoin && pairs <= kMaxArrived));
-  p.heads_off = parts || with_weights ? kMaxArrived * sizeof(unsigned) : 0;   // nothing else lies on the counters
-  p.ml_off = p.heads_off + (with_weights ? up(size_t(B) * Hq * sizeof(float2)) : 0);
-  p.o_off = p.ml_off + (parts ? up(rows * sizeof(float2)) : 0);
+  p.ml_off = parts || with_weights ? kMaxArrived * sizeof(unsigned) : 0;   // nothing else lies on the counters
+  p.o_off = p.ml_off + (parts || with_weights ? up(rows * sizeof(float2)) : 0);
   p.s_off = p.o_off + (parts ? up(rows * c.head_dim * sizeof(float)) : 0);
   p.ws_bytes = p.s_off + (with_weights ? up(size_t(B) * Hq * p.score_stride * sizeof(float)) : 0);
   return p;
@@ -699,7 +700,6 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   a.out = x.out;
   a.lse = x.lse;
   a.arrived = p.joins && p.nsplit > 1 ? reinterpret_cast<unsigned*>(x.ws) : nullptr;
-  a.heads = reinterpret_cast<float2*>(x.ws + p.heads_off);
   a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
   a.o = reinterpret_cast<float*>(x.ws + p.o_off);
   a.scores = reinterpret_cast<float*>(x.ws + p.s_off);

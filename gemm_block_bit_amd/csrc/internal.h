@@ -136,7 +136,7 @@ struct AttendPlan {
   int chunk, nsplit, qtiles;
   bool wide;   // workgroups that fill a CU
   bool joins;  // the last workgroup of a sequence joins its runs (else a second launch)
-  size_t heads_off, ml_off, o_off, s_off, ws_bytes;   // workspace sections
+  size_t ml_off, o_off, s_off, ws_bytes;   // workspace sections
   size_t score_stride;                     // scores per query head (with weights)
 };
 AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights);
