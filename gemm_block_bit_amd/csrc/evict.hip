@@ -205,10 +205,11 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   }
   for (int i = tid; i < kBins[0] + kBins[1] + kBins[2]; i += kThreads) hist[i] = 0;
 
-  constexpr bool HOLD = NB <= 4;   // registers enough to hold weights and positions to the end
+  constexpr bool HOLD = NB <= 4;   // registers enough for weights and positions to stay in them
+  static_assert(HOLD || !FINISH, "a launch that finishes holds them to the end");
   int page[NB];
-  f32x4 w[NB];
-  i32x4 p[NB];
+  f32x4 w[HOLD ? NB : 1];
+  i32x4 p[HOLD ? NB : 1];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
@@ -220,18 +221,24 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   const auto place = [&](int i) {   // of run i's first slot
     return ((size_t(page[i]) * a.Hkv + hk) << a.pshift) + (min(4096 * i + 4 * tid, (len - 1) & ~3) & ((1 << a.pshift) - 1));
   };
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    w[i] = *reinterpret_cast<const f32x4*>(a.weights + place(i));
-    p[i] = *reinterpret_cast<const i32x4*>(a.positions + place(i));
-  }
   const auto slot = [&](int i, int e) { return 4096 * i + 4 * tid + e; };
   int newest = INT32_MIN;
+  const auto load_w = [&](int i) { return *reinterpret_cast<const f32x4*>(a.weights + place(i)); };
+  const auto load_p = [&](int i) { return *reinterpret_cast<const i32x4*>(a.positions + place(i)); };
+  if constexpr (HOLD) {
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i) {
+      w[i] = load_w(i);
+      p[i] = load_p(i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const i32x4 q = HOLD ? p[HOLD ? i : 0] : load_p(i);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (slot(i, e) < len) newest = max(newest, p[i][e]);
+      if (slot(i, e) < len) newest = max(newest, q[e]);
+  }
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
   if (lane == 0) tops[wave] = newest;
@@ -246,10 +253,14 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   // the distance to the newest position is exact in 32 unsigned bits
   uint32_t key[NB][4];
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int i = 0; i < NB; ++i) {
+    const f32x4 v = HOLD ? w[HOLD ? i : 0] : load_w(i);
+    const i32x4 q = HOLD ? p[HOLD ? i : 0] : load_p(i);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      key[i][e] = uint32_t(newest) - uint32_t(p[i][e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(w[i][e]);
+      key[i][e] = uint32_t(newest) - uint32_t(q[e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(v[e]);
+    if (!HOLD && i % 4 == 3) asm volatile("" ::: "memory");   // four runs' loads at a time
+  }
 
   // the budget-th largest key, digit by digit, until all that share the
   // digits so far stay
@@ -257,23 +268,26 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   const auto round = [&](auto bins, uint32_t* h, uint32_t* s, int shift) {
     constexpr int BINS = decltype(bins)::value;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i) {
+      if (slot(i, 0) - 4 * tid >= len) continue;
+      uint32_t digit[4];
+      bool in[4];
+      bool one = true;   // all four in, with the digit of the wave's first
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool in = slot(i, e) < len && (key[i][e] & mask) == prefix;
-        const uint64_t who = __ballot(in);
-        if (!who) continue;
-        const uint32_t digit = (key[i][e] >> shift) & (BINS - 1);
-        if (in) {
-          // one addition for a wave whose keys agree (equal weights, new tokens)
-          const uint32_t first = uint32_t(uniform(int(digit)));
-          if (__ballot(digit == first) == who) {
-            if (lane == __builtin_ctzll(who)) atomicAdd(&h[digit], uint32_t(__popcll(who)));
-          } else {
-            atomicAdd(&h[digit], 1u);
-          }
-        }
+        in[e] = slot(i, e) < len && (key[i][e] & mask) == prefix;
+        digit[e] = (key[i][e] >> shift) & (BINS - 1);
+        one = one && in[e] && digit[e] == uint32_t(uniform(int(digit[0])));
       }
+      if (__all(one)) {
+        // one addition for a wave whose keys agree (equal weights, new tokens)
+        if (lane == 0) atomicAdd(&h[digit[0]], 256u);
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in[e]) atomicAdd(&h[digit[e]], 1u);
+    }
     __syncthreads();
     const uint32_t d = find_digit<BINS>(h, s, need, lane, wave);
     prefix |= d << shift;
@@ -345,21 +359,16 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     if (j >= len) continue;
     uint32_t hole = rank[i] & 0xffff, fill = rank[i] >> 16;
     const uint64_t x = place(i);
-    if (n[i]) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool k = kept[i] >> e & 1, low = j + e < stay;
-        if (low && !k) dst[hole++] = x + e;
-        if (!low && k) src[fill++] = x + e;
-      }
-    }
+    const uint32_t low4 = (1u << min(max(stay - j, 0), 4)) - 1;
+    for (uint32_t m = ~kept[i] & low4; m; m &= m - 1) dst[hole++] = x + __builtin_ctz(m);
+    for (uint32_t m = kept[i] & ~low4; m; m &= m - 1) src[fill++] = x + __builtin_ctz(m);
     if constexpr (FINISH) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool k = kept[i] >> e & 1, low = j + e < stay;
         if (low ? a.other && k : j + e < len && !k) {
-          a.weights_out[x + e] = !low ? 0.f : HOLD ? w[i][e] : a.weights[x + e];
-          a.positions_out[x + e] = !low ? -1 : HOLD ? p[i][e] : a.positions[x + e];
+          a.weights_out[x + e] = low ? w[i][e] : 0.f;
+          a.positions_out[x + e] = low ? p[i][e] : -1;
         }
       }
     } else {
@@ -377,7 +386,6 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
 
 // Rows of any length, with keys and words in the workspace: several times
 // slower a slot, for rows that registers do not hold.
-template <bool FINISH>
 __global__ __launch_bounds__(kThreads) void select_long_kernel(EvictKernelArgs a) {
   constexpr int THREADS = kThreads, WAVES = kWaves, BINS = 2048;
   __shared__ uint32_t lds[WAVES];
@@ -388,14 +396,14 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(EvictKernelArgs a
   const int len = max(0, min(a.lengths[b], a.max_len));
   const Slots at = {a.block_table + size_t(b) * a.max_pages, hk, a.Hkv, a.pshift};
   if (len <= a.budget) {
-    leave(a, at, pair, hk, b, len, FINISH);
+    leave(a, at, pair, hk, b, len, false);
     return;
   }
   const int stay = a.budget;
   const bool bad = missing(a, at, len);
   if (tid == 0 && hk == 0) a.lengths_out[b] = bad ? len : stay;
   if (bad) {
-    if (tid == 0 && !FINISH) a.count[pair] = -1;
+    if (tid == 0) a.count[pair] = -1;
     return;
   }
   uint32_t* keys = a.keys + size_t(pair) * a.key_stride;
@@ -542,19 +550,9 @@ __global__ __launch_bounds__(kThreads) void select_long_kernel(EvictKernelArgs a
     const uint64_t bit = uint64_t(1) << lane, under = bit - 1;
     if (~stays & low & bit) dst[above[w] + __popcll(~stays & low & under)] = at(j);
     if (stays & ~low & bit) src[equal[w] + __popcll(stays & ~low & under)] = at(j);
-    if constexpr (FINISH) {
-      if (j < len) settle(a, at, j, stay, stays & bit);
-    } else if (lane < 16) {
-      a.flags[size_t(pair) * (a.key_stride / 4) + 16 * w + lane] = uint8_t(stays >> (4 * lane) & 15);
-    }
+    if (lane < 16) a.flags[size_t(pair) * (a.key_stride / 4) + 16 * w + lane] = uint8_t(stays >> (4 * lane) & 15);
   }
-  if constexpr (FINISH) {
-    __syncthreads();
-    const int piece = tid & ((1 << a.lshift) - 1), per = THREADS >> a.lshift;
-    for (int i = tid >> a.lshift; i < int(holes); i += per) move_row(a, dst[i], src[i], piece);
-  } else if (tid == 0) {
-    a.count[pair] = int(holes);
-  }
+  if (tid == 0) a.count[pair] = int(holes);
 }
 
 __global__ __launch_bounds__(256) void move_kernel(EvictKernelArgs a) {
@@ -577,8 +575,12 @@ size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int NB>
 void run_select(const EvictKernelArgs& a, unsigned pairs, bool finish, hipStream_t s) {
-  if (finish) hipLaunchKernelGGL((select_kernel<NB, true>), dim3(pairs), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((select_kernel<NB, false>), dim3(pairs), dim3(kThreads), 0, s, a);
+  if constexpr (NB <= 4)
+    if (finish) {
+      hipLaunchKernelGGL((select_kernel<NB, true>), dim3(pairs), dim3(kThreads), 0, s, a);
+      return;
+    }
+  hipLaunchKernelGGL((select_kernel<NB, false>), dim3(pairs), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
@@ -628,13 +630,12 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
   a.lshift = __builtin_ctz(unsigned(c.head_dim * (c.dtype == GBB_E4M3 ? 1 : 2) / 16));
   a.other = x.weights_out != c.weights || x.positions_out != c.positions;
   const unsigned pairs = unsigned(x.B) * c.kv_heads;
-  const bool finish = p.most <= size_t(kFew);
+  const bool finish = p.most <= size_t(kFew) && x.max_len <= 16384;
   if (x.max_len <= 4096) run_select<1>(a, pairs, finish, s);
   else if (x.max_len <= 8192) run_select<2>(a, pairs, finish, s);
   else if (x.max_len <= 16384) run_select<4>(a, pairs, finish, s);
   else if (x.max_len <= kMaxHeld) run_select<8>(a, pairs, finish, s);
-  else if (finish) hipLaunchKernelGGL((select_long_kernel<true>), dim3(pairs), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((select_long_kernel<false>), dim3(pairs), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL(select_long_kernel, dim3(pairs), dim3(kThreads), 0, s, a);
   if (!finish) {
     const size_t per = 256 >> a.lshift;
     const size_t most = std::max((p.most + per - 1) / per, (size_t(x.max_len) + 255) / 256);
