@@ -107,7 +107,7 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
         raise ValueError("x must be [T][H][D] with contiguous heads")
     T, H, D = x.shape
     if out is None:
-        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         y = out
         if y.dtype != x.dtype or y.shape != x.shape or y.stride(2) != 1:
@@ -238,7 +238,7 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
         raise ValueError(f"q must be [B][q_heads][{D}] with contiguous tokens")
     shape = q.shape
     B, q_heads = shape[0], shape[1]
-    o = out if out is not None else torch.empty(shape, dtype=q.dtype, device=q.device)
+    o = out if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
     bt = _ptr(block_table, torch.int32, device, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}][pages]")
