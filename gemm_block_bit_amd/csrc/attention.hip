@@ -78,9 +78,8 @@ template <> struct Half<GBB_BF16> {
 // 16 bytes a lane from memory to LDS at `to` (the same in all lanes) plus 16
 // bytes times the lane.  The compiler does not wait for such a load before
 // LDS reads: loads_left<N>() waits until at most the N vector memory
-// operations issued last are under way (they complete in order), in_order()
-// keeps the compiler from moving memory operations across it, and
-// reads_done() awaits LDS reads, before a load overwrites what they read.
+// operations issued last are under way (they complete in order) and
+// in_order() keeps the compiler from moving memory operations across it.
 __device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* to) {
   __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
                                        reinterpret_cast<uintptr_t>(from)),
@@ -92,7 +91,35 @@ __device__ __forceinline__ void loads_left() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
-__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// N pieces of 16 bytes from LDS, at the byte offsets at[] plus OFF, awaited.
+// Written out because the compiler, where it sees the reads, awaits every
+// vector memory load before them, V's among them.
+template <int OFF> __device__ __forceinline__ void from_lds(u32x4 (&x)[1], const uint32_t (&at)[1]) {
+  asm volatile("ds_read_b128 %0, %1 offset:%2\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x[0]) : "v"(at[0]), "n"(OFF) : "memory");
+}
+template <int OFF> __device__ __forceinline__ void from_lds(u32x4 (&x)[2], const uint32_t (&at)[2]) {
+  asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x[0]), "=&v"(x[1])
+               : "v"(at[0]), "v"(at[1]), "n"(OFF)
+               : "memory");
+}
+template <int OFF> __device__ __forceinline__ void from_lds(u32x4 (&x)[4], const uint32_t (&at)[4]) {
+  asm volatile("ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+               "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF)
+               : "memory");
+}
+template <int OFF> __device__ __forceinline__ void from_lds(u32x4 (&x)[8], const uint32_t (&at)[8]) {
+  asm volatile("ds_read_b128 %0, %8 offset:%16\n\tds_read_b128 %1, %9 offset:%16\n\t"
+               "ds_read_b128 %2, %10 offset:%16\n\tds_read_b128 %3, %11 offset:%16\n\t"
+               "ds_read_b128 %4, %12 offset:%16\n\tds_read_b128 %5, %13 offset:%16\n\t"
+               "ds_read_b128 %6, %14 offset:%16\n\tds_read_b128 %7, %15 offset:%16\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "v"(at[6]), "v"(at[7]), "n"(OFF)
+               : "memory");
+}
 
 struct SplitArgs {
   const void* q;
@@ -112,6 +139,7 @@ struct SplitArgs {
   float* scores;    // [B][Hkv][G][score_stride], log2 domain
   size_t score_stride;
   int64_t q_token;
+  bool joins;       // no second launch
   int B, Hq, Hkv, G, qtiles, num_pages, pshift, max_pages, max_len, chunk, nsplit;
   float scale;      // scale * log2(e)
 };
@@ -136,6 +164,40 @@ __device__ __forceinline__ void put(float* p, float x, float y) {
 __device__ __forceinline__ float2 get(const float* p) {
   const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return make_float2(__builtin_bit_cast(float, uint32_t(v)), __builtin_bit_cast(float, uint32_t(v >> 32)));
+}
+
+// weights_out = weights + sum over the kv head's query heads of
+// 2^(score - ref) inv, for the slots j ... j + 3, j + STEP ... below len (a
+// page holds whole groups of 4).
+template <int STEP>
+__device__ __forceinline__ void add_weights(const SplitArgs& a, int b, int hk, int len, int j, const float* ref,
+                                            const float* inv) {
+  for (; j < len; j += STEP) {
+    const int p = a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)];
+    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + j;
+    constexpr int AHEAD = 8;
+    f32x4 x[AHEAD];
+    const auto fetch = [&](int q0) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) x[u] = *reinterpret_cast<const f32x4*>(s + min(q0 + u, a.G - 1) * a.score_stride);
+    };
+    fetch(0);
+    const bool there = unsigned(p) < unsigned(a.num_pages);
+    const size_t at = ((size_t(there ? p : 0) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
+    const f32x4 old = *reinterpret_cast<const f32x4*>(a.weights + at);
+    f32x4 w = {0, 0, 0, 0};
+    for (int q0 = 0; q0 < a.G; q0 += AHEAD) {
+      if (q0) fetch(q0);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (q0 + u < a.G)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] += __builtin_amdgcn_exp2f(x[u][k] - ref[q0 + u]) * inv[q0 + u];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (there && j + k < len) a.weights_out[at + k] = old[k] + w[k];
+  }
 }
 
 template <int DT, int CT, int D, bool WT, bool WIDE>
@@ -255,31 +317,37 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
         }
     }
   };
+  uint32_t k_at[KP];   // this lane's pieces of row c in LDS
+#pragma unroll
+  for (int j = 0; j < KP; ++j)
+    k_at[j] = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)mine)) +
+              c * ROW + ((4 * j + g4) ^ swizzle(c)) * 16;
   const auto compute = [&](int i) {
     const int key0 = k0 + 32 * (wave + NW * i);
     f32x4 s[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       s[e] = f32x4{0, 0, 0, 0};
+      u32x4 kk[KP];
+      if (e == 0) from_lds<0>(kk, k_at);
+      else from_lds<16 * ROW>(kk, k_at);
 #pragma unroll
       for (int j = 0; j < KP; ++j) {
-        const u32x4 kk = *reinterpret_cast<const u32x4*>(mine + (16 * e + c) * ROW + ((4 * j + g4) ^ swizzle(c)) * 16);
         if constexpr (F8) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = kk[2 * h], w1 = kk[2 * h + 1];
+            const uint32_t w0 = kk[j][2 * h], w1 = kk[j][2 * h + 1];
             const u32x4 x = {H::template widen<false>(w0), H::template widen<true>(w0),
                              H::template widen<false>(w1), H::template widen<true>(w1)};
             s[e] = H::mfma(__builtin_bit_cast(V8, x), qf[2 * j + h], s[e]);
           }
         } else {
-          s[e] = H::mfma(__builtin_bit_cast(V8, kk), qf[j], s[e]);
+          s[e] = H::mfma(__builtin_bit_cast(V8, kk[j]), qf[j], s[e]);
         }
       }
       s[e] *= scale;
     }
     if (i + 1 < n) {
-      reads_done();
       load_k(i + 1);
       in_order();
     }
@@ -376,7 +444,10 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
     load_v(0);
   }
   for (int i = 0; i < n; ++i) {
-    loads_left<8 * NV>();   // K's loads are older than V's 8 NV
+    // this tile's K; younger are its V's 8 NV loads and, with weights, the last
+    // tile's two stores of scores
+    if (WT && i) loads_left<8 * NV + 2>();
+    else loads_left<8 * NV>();
     compute(i);
     in_order();
     if (i + 1 < n) load_v(i + 1);
@@ -400,13 +471,19 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   const bool whole = len <= a.chunk;
   const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
   typedef typename H::T V2 __attribute__((ext_vector_type(2)));
-  // out and lse from the joined sums of a head
+  // out and lse from the joined sums of a head; with weights also what is
+  // taken off its scores and one over its sum
+  __shared__ float ref[16], inv[16];
   const auto finish = [&](int q, int d, float m, float l, float o0, float o1) {
     const size_t head = size_t(b) * a.Hq + hq0 + q;
     const float f0 = l == 0.f ? 0.f : o0 / l * vs, f1 = l == 0.f ? 0.f : o1 / l * vs;
     *reinterpret_cast<V2*>(static_cast<typename H::T*>(a.out) + head * D + d) = V2{typename H::T(f0), typename H::T(f1)};
     if (d == 0) {
       if (a.lse) a.lse[head] = l == 0.f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
+      if (WT) {
+        ref[q] = m == -INFINITY ? 0.f : m - kShift;
+        inv[q] = l == 0.f ? 0.f : 1.f / l;
+      }
     }
   };
   const size_t row0 = (size_t(b * a.Hkv + hk) * a.nsplit + sp) * a.G + 16 * qt;
@@ -431,7 +508,15 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       if (d == 0) put(reinterpret_cast<float*>(a.ml + row0 + q), mm, ll);
     }
   }
-  if (whole || !a.arrived) return;
+  if (whole) {
+    if (WT && a.joins) {
+      loads_left<0>();   // the waves' scores are written
+      __syncthreads();
+      add_weights<4 * THREADS>(a, b, hk, len, 4 * threadIdx.x, ref, inv);
+    }
+    return;
+  }
+  if (!a.arrived) return;
 
   // The workgroup that is the last of its sequence to get here joins all
   // runs, in their order whichever it is.  Partial results are written and
@@ -565,23 +650,11 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
     const int j0 = (id % nb) * kJoinSlots;
     id /= nb;
     const int hk = id % a.Hkv, b = id / a.Hkv;
-    // 4 slots a thread (a page holds whole groups of 4)
-    const int j = j0 + 4 * threadIdx.x;
-    const int p = a.block_table[size_t(b) * a.max_pages + (min(j, a.max_len - 1) >> a.pshift)];
     const float2* ml = a.ml + size_t(b * a.Hkv + hk) * a.nsplit * a.G;
     const float2 first = first_runs(ml + min(wave, a.G - 1), a, lane);
     in_order();
     const int len = length_of(a, b);
     if (j0 >= len) return;
-    const bool there = j < len && unsigned(p) < unsigned(a.num_pages);
-    const size_t at = ((size_t(there ? p : 0) * a.Hkv + hk) << a.pshift) + (j & ((1 << a.pshift) - 1));
-    const f32x4 old = *reinterpret_cast<const f32x4*>(a.weights + at);
-    const float* s = a.scores + (size_t(b) * a.Hq + size_t(hk) * a.G) * a.score_stride + (there ? j : 0);
-    constexpr int AHEAD = 8;
-    f32x4 x[AHEAD];
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) x[u] = *reinterpret_cast<const f32x4*>(s + min(u, a.G - 1) * a.score_stride);
-    in_order();
     // per query head: what is taken off a score, and one over the sum
     __shared__ float ref[kMaxGroup], inv[kMaxGroup];
     const int ns = (len + a.chunk - 1) / a.chunk;
@@ -593,23 +666,7 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
       }
     }
     __syncthreads();
-    if (!there) return;
-    f32x4 w = {0, 0, 0, 0};
-    for (int q0 = 0; q0 < a.G; q0 += AHEAD) {
-      if (q0) {
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-          x[u] = *reinterpret_cast<const f32x4*>(s + min(q0 + u, a.G - 1) * a.score_stride);
-      }
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u)
-        if (q0 + u < a.G)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] += __builtin_amdgcn_exp2f(x[u][k] - ref[q0 + u]) * inv[q0 + u];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (j + k < len) a.weights_out[at + k] = old[k] + w[k];
+    add_weights<kJoinSlots>(a, b, hk, min(len, j0 + kJoinSlots), j0 + 4 * threadIdx.x, ref, inv);
   }
 }
 
@@ -621,10 +678,11 @@ void run_split(const SplitArgs& a, bool wide, hipStream_t s) {
 }
 
 template <int DT, int CT, int D>
-void run(const SplitArgs& a, bool wide, bool joins, bool wt, hipStream_t s) {
+void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
   if (wt) run_split<DT, CT, D, true>(a, wide, s);
   else run_split<DT, CT, D, false>(a, wide, s);
-  const int heads = joins || a.nsplit == 1 ? 0 : (a.B * a.Hq + 256 / D - 1) / (256 / D);
+  if (a.joins) return;
+  const int heads = a.nsplit == 1 ? 0 : (a.B * a.Hq + 256 / D - 1) / (256 / D);
   constexpr bool F8 = CT == GBB_E4M3;
   if (wt) {
     const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + kJoinSlots - 1) / kJoinSlots);
@@ -634,10 +692,10 @@ void run(const SplitArgs& a, bool wide, bool joins, bool wt, hipStream_t s) {
   }
 }
 template <int DT, int CT>
-void run_dim(const SplitArgs& a, int D, bool wide, bool joins, bool wt, hipStream_t s) {
-  if (D == 64) run<DT, CT, 64>(a, wide, joins, wt, s);
-  else if (D == 128) run<DT, CT, 128>(a, wide, joins, wt, s);
-  else run<DT, CT, 256>(a, wide, joins, wt, s);
+void run_dim(const SplitArgs& a, int D, bool wide, bool wt, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, wide, wt, s);
+  else if (D == 128) run<DT, CT, 128>(a, wide, wt, s);
+  else run<DT, CT, 256>(a, wide, wt, s);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
@@ -677,8 +735,12 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   const size_t rows = size_t(B) * Hq * p.nsplit;
   p.score_stride = (size_t(max_len) + 31) & ~size_t(31);
   const bool parts = p.nsplit > 1;
-  // one launch where the last workgroup of a sequence can join its runs
-  p.joins = !with_weights && (!parts || (p.nsplit <= kMaxJoin && pairs <= kMaxArrived));
+  // One launch where the last workgroup of a sequence can join its runs.  With
+  // weights, where there are none to join and a workgroup has all query heads
+  // of its kv head: a second launch finds the scores of all runs without
+  // their having to be written past the caches (16 ragged of up to 4097: 40
+  // us, 44 with the scores at device scope and one launch).
+  p.joins = with_weights ? !parts && p.qtiles == 1 : !parts || (p.nsplit <= kMaxJoin && pairs <= kMaxArrived);
   p.ml_off = parts || with_weights ? kMaxArrived * sizeof(unsigned) : 0;   // nothing else lies on the counters
   p.o_off = p.ml_off + (parts || with_weights ? up(rows * sizeof(float2)) : 0);
   p.s_off = p.o_off + (parts ? up(rows * c.head_dim * sizeof(float)) : 0);
@@ -699,6 +761,7 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   a.weights_out = x.weights_out;
   a.out = x.out;
   a.lse = x.lse;
+  a.joins = p.joins;
   a.arrived = p.joins && p.nsplit > 1 ? reinterpret_cast<unsigned*>(x.ws) : nullptr;
   a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
   a.o = reinterpret_cast<float*>(x.ws + p.o_off);
@@ -720,11 +783,11 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool wt = x.weights_out != nullptr;
   if (x.dtype == GBB_F16) {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.wide, p.joins, wt, s);
-    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.wide, p.joins, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.wide, wt, s);
   } else {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.wide, p.joins, wt, s);
-    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.wide, p.joins, wt, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.wide, wt, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.wide, wt, s);
   }
   return int(hipGetLastError());
 }
