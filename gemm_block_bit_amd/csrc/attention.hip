@@ -33,6 +33,7 @@
 // second adds exp(s - max) / sum over the kv head's query heads, one thread
 // a slot, without atomics.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "internal.h"
@@ -42,7 +43,7 @@ namespace gbb {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;   // see above: 2^14 < 65504
@@ -75,17 +76,19 @@ template <> struct Half<GBB_BF16> {
   }
 };
 
-// 16 bytes a lane from memory to LDS at `to` (the same in all lanes) plus 16
-// bytes times the lane.  The compiler does not wait for such a load before
-// LDS reads: loads_left<N>() waits until at most the N vector memory
+// `bytes` of memory from `base`; loads past them give zeros.
+typedef __amdgpu_buffer_rsrc_t Span;
+__device__ __forceinline__ Span span(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);   // raw bytes
+}
+// 16 bytes a lane, at byte `at` of s, to LDS at `to` (the same in all lanes)
+// plus 16 bytes times the lane.  The compiler does not wait for such a load
+// before LDS reads: loads_left<N>() waits until at most the N vector memory
 // operations issued last are under way (they complete in order) and
 // in_order() keeps the compiler from moving memory operations across it.
-__device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
-                                       reinterpret_cast<uintptr_t>(from)),
-                                   (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+__device__ __forceinline__ void to_lds(Span s, int at, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(s, (__attribute__((address_space(3))) void*)to, 16, at, 0, 0, 0);
 }
-
 template <int N>
 __device__ __forceinline__ void loads_left() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -214,11 +217,13 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 15, g4 = lane >> 4;
   int id = blockIdx.x;
-  const int qt = id % a.qtiles;
+  // (divisions are done in vector registers; what follows addresses memory by
+  // scalar ones)
+  const int qt = uniform(id % a.qtiles);
   id /= a.qtiles;
-  const int hk = id % a.Hkv;
+  const int hk = uniform(id % a.Hkv);
   id /= a.Hkv;
-  const int b = id % a.B, sp = id / a.B;
+  const int b = uniform(id % a.B), sp = uniform(id / a.B);
   const int rows = min(16, a.G - 16 * qt);           // query heads of this tile
   const int hq0 = hk * a.G + 16 * qt;
   const int k0 = sp * a.chunk;
@@ -275,44 +280,46 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   // which spreads the 16 rows that lanes read at once over all banks.
   constexpr int LPR = ROW / 16, RPI = 64 / LPR;      // lanes a row, rows an instruction
   constexpr auto swizzle = [](int r) { return (ROW >= 256 ? r : r / (256 / ROW)) & (LPR < 16 ? LPR - 1 : 15); };
-  // Pages hold whole 16-slot halves, so a half's rows are always memory of
-  // the cache; a page that is not there is read as page 0 and masked.
-  const auto half_at = [&](int i, int s) {
-    const int p = max(0, __builtin_amdgcn_readlane(page, 2 * i + s));
+  // The rows of 16-slot half s of tile i that take part: a page holds whole
+  // halves, and rows past the length or of a page that is not there read as
+  // zeros, whatever their memory holds.
+  const auto rows_at = [&](const uint8_t* base, int i, int s) {
+    const int p = __builtin_amdgcn_readlane(page, 2 * i + s);
     const int key = k0 + 32 * (wave + NW * i) + 16 * s;
-    return (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * ROW;
+    const size_t off = (size_t(max(p, 0)) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * ROW;
+    return span(base + off, uniform(p < 0 ? 0 : max(0, min(k1 - key, 16)) * ROW));
   };
   uint32_t vr[2][4][NV][VW];
   const auto load_k = [&](int i) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint8_t* kb = a.k + half_at(i, s);
+      const Span rows = rows_at(a.k, i, s);
 #pragma unroll
       for (int j = 0; j < KP; ++j) {
         const int r = j * RPI + lane / LPR;
-        to_lds(kb + r * ROW + ((lane % LPR) ^ swizzle(r)) * 16, mine + s * 16 * ROW + j * 1024);
+        to_lds(rows, r * ROW + ((lane % LPR) ^ swizzle(r)) * 16, mine + s * 16 * ROW + j * 1024);
       }
     }
   };
   const auto load_v = [&](int i) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint8_t* vb = a.v + half_at(i, s) + 4 * g4 * ROW + c * VB;
+      const Span rows = rows_at(a.v, i, s);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-          const uint8_t* p2 = vb + r * ROW + u * 256;
+          const int at = (4 * g4 + r) * ROW + u * 256 + c * VB;
           if constexpr (VW == 4) {
-            const u32x4 x = ld16(p2);
+            const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, 0);
 #pragma unroll
             for (int w = 0; w < 4; ++w) vr[s][r][u][w] = x[w];
           } else if constexpr (VW == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p2);
-            vr[s][r][u][0] = x.x;
-            vr[s][r][u][1] = x.y;
+            const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rows, at, 0, 0);
+            vr[s][r][u][0] = x[0];
+            vr[s][r][u][1] = x[1];
           } else {
-            vr[s][r][u][0] = *reinterpret_cast<const uint32_t*>(p2);
+            vr[s][r][u][0] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0);
           }
         }
     }
@@ -322,7 +329,9 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   for (int j = 0; j < KP; ++j)
     k_at[j] = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)mine)) +
               c * ROW + ((4 * j + g4) ^ swizzle(c)) * 16;
-  const auto compute = [&](int i) {
+  // NEXT: there is a next tile, whose K is loaded.  Known at compile time so
+  // that the waits for V can count the loads behind it.
+  const auto compute = [&](int i, auto NEXT) {
     const int key0 = k0 + 32 * (wave + NW * i);
     f32x4 s[2];
 #pragma unroll
@@ -347,25 +356,19 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       }
       s[e] *= scale;
     }
-    if (i + 1 < n) {
+    if constexpr (decltype(NEXT)::value) {
+      in_order();
       load_k(i + 1);
       in_order();
     }
-    // a tile that the length or a missing page cuts: those slots take no
-    // part, and whatever their memory holds must not reach the product
+    // slots of a tile that the length or a missing page cuts
     const int p0 = __builtin_amdgcn_readlane(page, 2 * i), p1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
     if (key0 + 32 > k1 || (p0 | p1) < 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (key0 + 16 * e + 4 * g4 + r >= k1 || (e ? p1 : p0) < 0) {
-            s[e][r] = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < NV; ++u)
-#pragma unroll
-              for (int w = 0; w < VW; ++w) vr[e][r][u][w] = 0;
-          }
+          s[e][r] = key0 + 16 * e + 4 * g4 + r >= k1 || (e ? p1 : p0) < 0 ? -INFINITY : s[e][r];
     }
     if constexpr (WT) {
       if (c < rows) {
@@ -443,14 +446,21 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
     in_order();
     load_v(0);
   }
-  for (int i = 0; i < n; ++i) {
-    // this tile's K; younger are its V's 8 NV loads and, with weights, the last
-    // tile's two stores of scores
+  const auto await_k = [&](int i) {
+    // younger than this tile's K are its V's 8 NV loads and, with weights, the
+    // last tile's two stores of scores
     if (WT && i) loads_left<8 * NV + 2>();
     else loads_left<8 * NV>();
-    compute(i);
+  };
+  for (int i = 0; i + 1 < n; ++i) {
+    await_k(i);
+    compute(i, std::true_type());
     in_order();
-    if (i + 1 < n) load_v(i + 1);
+    load_v(i + 1);
+  }
+  if (n > 0) {
+    await_k(n - 1);
+    compute(n - 1, std::false_type());
   }
 
   // join the waves
