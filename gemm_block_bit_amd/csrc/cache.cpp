@@ -116,8 +116,10 @@ gbb_status check_evict_shape(const gbb_paged_cache* c, int B, int max_len, int b
   const gbb_status st = check_cache(c);
   if (st != GBB_OK) return st;
   if (B < 0 || max_len < 1 || max_len > INT_MAX - 8192) return fail(GBB_E_ARG, "bad B or max_len (%d, %d)", B, max_len);
+  if (max_len > kMaxEvictLen) return fail(GBB_E_SHAPE, "max_len=%d exceeds %d", max_len, kMaxEvictLen);
   if (budget < 1) return fail(GBB_E_ARG, "budget must be at least 1 (%d)", budget);
-  if (int64_t(B) * c->kv_heads > kMaxGroups / 4) return fail(GBB_E_SHAPE, "B * kv_heads exceeds %d", int(kMaxGroups / 4));
+  if (int64_t(B) * c->kv_heads > kMaxGroups / 4 / (1 + max_len / 4096))
+    return fail(GBB_E_SHAPE, "B=%d, kv_heads=%d and max_len=%d make too many workgroups", B, c->kv_heads, max_len);
   return GBB_OK;
 }
 

@@ -10,13 +10,20 @@
 // a slot, and 2 rows read and written a moved slot, are what it takes.
 //
 // One workgroup of 16 waves selects for a (sequence, kv head): the threads
-// hold the keys in registers, 4 slots to a load (rows above 32768 slots go
-// through the workspace), the budget-th largest is found 11 bits at a time
-// from histograms in LDS, and ranks in slot order are prefix sums of each
-// thread's counts.  Where few rows
-// can move, as in a cache that is one token over its budget, the same
-// workgroup moves them; else a second launch moves rows and writes weights
-// and positions over as many workgroups as the slots give.
+// hold the keys in registers, 4 slots to a load (rows above 32768 slots are
+// spread over workgroups and launches instead), the budget-th largest is
+// found 11 bits at a time from histograms in LDS, and ranks in slot order are
+// prefix sums of each thread's counts.  Where few rows can move, as in a
+// cache that is one token over its budget, the same workgroup moves them;
+// else a second launch moves rows and writes weights and positions over as
+// many workgroups as the slots give.
+//
+// Measured (GPU time): 256 pairs of 2049 slots cut by one 9.1 us, of which
+// about 7 are the chain of dependent steps in a workgroup (load, newest
+// position, three digits, two prefix sums); 16 pairs of 32768 slots of 128
+// fp16 elements cut to 4096 40 us: 21 in 16 workgroups that each read their
+// row twice (no more than 16 of the 256 CUs have work), 15 in the moves (4
+// TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -43,8 +50,7 @@ struct EvictKernelArgs {
   int32_t* count;    // [B Hkv] rows to move, -1: the sequence is left as it is
   uint64_t* dst;     // [B Hkv][most] places (Slots), in the order of slots
   uint64_t* src;
-  uint32_t* keys;    // [B Hkv][key_stride], for rows that registers do not hold
-  uint64_t* words;   // [B Hkv][3][key_stride / 64], with the keys
+  uint32_t* keys;    // [B Hkv][key_stride], for spread rows
   uint8_t* flags;    // [B Hkv][key_stride / 4]: which of 4 slots are kept, a bit each
   size_t key_stride, most;
   int Hkv, num_pages, pshift, max_pages, max_len, budget, recent, lshift;
@@ -384,175 +390,268 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   }
 }
 
-// Rows of any length, with keys and words in the workspace: several times
-// slower a slot, for rows that registers do not hold.
-__global__ __launch_bounds__(kThreads) void select_long_kernel(EvictKernelArgs a) {
-  constexpr int THREADS = kThreads, WAVES = kWaves, BINS = 2048;
-  __shared__ uint32_t lds[WAVES];
-  __shared__ uint32_t hist[BINS];
-  __shared__ uint32_t chosen[2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
-  const int len = max(0, min(a.lengths[b], a.max_len));
-  const Slots at = {a.block_table + size_t(b) * a.max_pages, hk, a.Hkv, a.pshift};
-  if (len <= a.budget) {
-    leave(a, at, pair, hk, b, len, false);
-    return;
-  }
-  const int stay = a.budget;
-  const bool bad = missing(a, at, len);
-  if (tid == 0 && hk == 0) a.lengths_out[b] = bad ? len : stay;
-  if (bad) {
-    if (tid == 0) a.count[pair] = -1;
-    return;
-  }
-  uint32_t* keys = a.keys + size_t(pair) * a.key_stride;
-  const size_t third = a.key_stride / 64;
-  uint64_t* kept = a.words + size_t(pair) * 3 * third;
-  uint64_t* above = kept + third;   // keys above the budget-th, and equal to it
-  uint64_t* equal = above + third;
-  const int nwords = (len + 63) / 64;
+// Rows that registers do not hold are spread over workgroups of 4096 slots
+// each (a segment): the same selection in launches that meet in the workspace
+// (newest position; keys and first digit; second digit; third digit; places),
+// each workgroup summing the segments' histograms for itself.  8 pairs of
+// 65536 slots cut to 8192: 59 us, 142 with one workgroup a pair that keeps its
+// keys in the workspace.
+constexpr int kSegment = 4 * kThreads;
+struct Found {
+  uint32_t prefix, mask, need, all;   // all: every key that shares the digits so far stays
+};
+struct SpreadArgs {
+  int32_t* newest;    // [B Hkv][segments]
+  int32_t* missing;   // [B Hkv][segments]
+  uint32_t* above;    // [2][B Hkv][segments] keys above the digits found so far
+  Found* found;       // [2][B Hkv] after the first and the second digit
+  uint32_t* hist;     // [B Hkv][segments][2048 + 2048 + 1024]
+  int segments, pairs;
+};
+constexpr int kHists = kBins[0] + kBins[1] + kBins[2];
 
-  // keys, and the newest position
+// What a workgroup of a spread launch works on.
+struct Segment {
+  int pair, seg, hk, b, len, used;   // used: segments below the length
+  Slots at;
+};
+__device__ __forceinline__ Segment segment(const EvictKernelArgs& a, const SpreadArgs& s) {
+  Segment g;
+  g.seg = int(blockIdx.x) % s.segments;
+  g.pair = int(blockIdx.x) / s.segments;
+  g.hk = g.pair % a.Hkv;
+  g.b = g.pair / a.Hkv;
+  g.len = max(0, min(a.lengths[g.b], a.max_len));
+  g.used = (g.len + kSegment - 1) / kSegment;
+  g.at = {a.block_table + size_t(g.b) * a.max_pages, g.hk, a.Hkv, a.pshift};
+  return g;
+}
+__device__ __forceinline__ bool spread_missing(const SpreadArgs& s, const Segment& g) {
+  int bad = 0;
+  for (int i = threadIdx.x; i < g.used; i += kThreads) bad |= s.missing[size_t(g.pair) * s.segments + i];
+  return __syncthreads_or(bad);
+}
+
+__global__ __launch_bounds__(kThreads) void spread_newest_kernel(EvictKernelArgs a, SpreadArgs s) {
+  __shared__ int tops[kWaves];
+  const Segment g = segment(a, s);
+  const int j = g.seg * kSegment + 4 * int(threadIdx.x);
+  const bool in = j < g.len;
+  const int page = in ? g.at.table[j >> a.pshift] : 0;
+  const int bad = __syncthreads_or(unsigned(page) >= unsigned(a.num_pages));
+  if (g.seg >= g.used) return;
   int newest = INT32_MIN;
-  for (int j0 = tid; j0 < len; j0 += 4 * THREADS) {
-    float w[4];
-    int p[4];
+  if (!bad && in) {
+    const i32x4 p = *reinterpret_cast<const i32x4*>(a.positions + g.at(j));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const size_t x = at(min(j0 + u * THREADS, len - 1));
-      w[u] = a.weights[x];
-      p[u] = a.positions[x];
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      newest = max(newest, p[u]);
-      if (j0 + u * THREADS < len) keys[j0 + u * THREADS] = rank_of(w[u]);
-    }
+    for (int e = 0; e < 4; ++e)
+      if (j + e < g.len) newest = max(newest, p[e]);
   }
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
-  if (lane == 0) lds[wave] = uint32_t(newest);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = newest;
   __syncthreads();
-  for (int w = 0; w < WAVES; ++w) newest = max(newest, int(lds[w]));
-  if (a.recent) {   // positions above `old` are kept first
-    const int64_t old = int64_t(newest) - a.recent;
-    for (int j0 = tid; j0 < len; j0 += 4 * THREADS) {
-      int p[4];
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWaves; ++w) newest = max(newest, tops[w]);
+    s.newest[size_t(g.pair) * s.segments + g.seg] = newest;
+    s.missing[size_t(g.pair) * s.segments + g.seg] = bad;
+  }
+}
+
+// The digit of `sum` (LDS) that continues f.
+template <int ROUND>
+__device__ __forceinline__ Found next_digit(Found f, const uint32_t* sum, uint32_t* sums, int lane, int wave) {
+  const uint32_t d = find_digit<kBins[ROUND]>(sum, sums, f.need, lane, wave);
+  f.prefix |= d << kShift[ROUND];
+  f.mask |= uint32_t(kBins[ROUND] - 1) << kShift[ROUND];
+  f.all = sum[d] == f.need;
+  return f;
+}
+constexpr int kHistAt[3] = {0, kBins[0], kBins[0] + kBins[1]};
+// Sum over a pair's segments of the histogram of digit ROUND, to LDS.
+template <int ROUND>
+__device__ __forceinline__ void sum_hists(const SpreadArgs& s, const Segment& g, uint32_t* to) {
+  const uint32_t* h = s.hist + size_t(g.pair) * s.segments * kHists + kHistAt[ROUND];
+  for (int i = threadIdx.x; i < kBins[ROUND]; i += kThreads) {
+    uint32_t n = 0;
+    for (int k = 0; k < g.used; ++k) n += h[size_t(k) * kHists + i];
+    to[i] = n;
+  }
+  __syncthreads();
+}
+
+// Digit ROUND: its segment's histogram, after the digit before it is found.
+// The first also makes the keys.
+template <int ROUND>
+__global__ __launch_bounds__(kThreads) void spread_hist_kernel(EvictKernelArgs a, SpreadArgs s) {
+  __shared__ uint32_t hist[kBins[0]], sums[kWaves];
+  __shared__ uint32_t over;
+  const Segment g = segment(a, s);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  if (ROUND == 0 && g.len <= a.budget) {
+    if (g.seg == 0) leave(a, g.at, g.pair, g.hk, g.b, g.len, false);
+    return;
+  }
+  if (g.len <= a.budget || g.seg >= g.used) return;
+  const bool bad = spread_missing(s, g);
+  if (ROUND == 0 && g.seg == 0 && tid == 0) {
+    if (g.hk == 0) a.lengths_out[g.b] = bad ? g.len : a.budget;
+    if (bad) a.count[g.pair] = -1;
+  }
+  if (bad) return;
+  const int j = g.seg * kSegment + 4 * tid;
+  uint32_t* keys = a.keys + size_t(g.pair) * a.key_stride;
+  uint32_t key[4];
+  Found f = {0, 0, uint32_t(a.budget), 0};
+  if constexpr (ROUND == 0) {
+    int newest = INT32_MIN;
+    for (int i = tid; i < g.used; i += kThreads) newest = max(newest, s.newest[size_t(g.pair) * s.segments + i]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) p[u] = a.positions[at(min(j0 + u * THREADS, len - 1))];
+    for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
+    if (lane == 0) sums[wave] = uint32_t(newest);
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) newest = max(newest, int(sums[w]));
+    const size_t x = g.at(min(j, (g.len - 1) & ~3));
+    const f32x4 w = *reinterpret_cast<const f32x4*>(a.weights + x);
+    const i32x4 p = *reinterpret_cast<const i32x4*>(a.positions + x);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j0 + u * THREADS < len && int64_t(p[u]) > old) keys[j0 + u * THREADS] = 0xffffffffu;
+    for (int e = 0; e < 4; ++e)
+      key[e] = uint32_t(newest) - uint32_t(p[e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(w[e]);
+    if (j < g.len) *reinterpret_cast<u32x4*>(keys + j) = u32x4{key[0], key[1], key[2], key[3]};
+  } else {
+    const u32x4 k = j < g.len ? *reinterpret_cast<const u32x4*>(keys + j) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) key[e] = k[e];
+    if constexpr (ROUND == 2) f = s.found[g.pair];
+    const Found last = f;
+    if (!f.all) {
+      sum_hists<ROUND - 1>(s, g, hist);
+      f = next_digit<ROUND - 1>(f, hist, sums, lane, wave);
+      __syncthreads();
+    }
+    // keys of this segment that the new digit puts above
+    uint32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      n += j + e < g.len && (key[e] & last.mask) == last.prefix && (key[e] & f.mask) > f.prefix;
+    if (tid == 0) over = 0;
+    __syncthreads();
+    const uint32_t w = wave_scan(n);
+    if (lane == 63 && w) atomicAdd(&over, w);
+    __syncthreads();
+    if (tid == 0) {
+      s.above[(size_t(ROUND - 1) * s.pairs + g.pair) * s.segments + g.seg] = over;
+      if (g.seg == 0) s.found[size_t(ROUND - 1) * s.pairs + g.pair] = f;
+    }
+    if (f.all) return;
+  }
+  for (int i = tid; i < kBins[ROUND]; i += kThreads) hist[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bool in = j + e < g.len && (key[e] & f.mask) == f.prefix;
+    const uint32_t digit = (key[e] >> kShift[ROUND]) & (kBins[ROUND] - 1);
+    if (__all(in && digit == uint32_t(uniform(int(digit))))) {
+      if (lane == 0) atomicAdd(&hist[digit], 64u);
+    } else if (in) {
+      atomicAdd(&hist[digit], 1u);
     }
   }
+  __syncthreads();
+  uint32_t* h = s.hist + (size_t(g.pair) * s.segments + g.seg) * kHists + kHistAt[ROUND];
+  for (int i = tid; i < kBins[ROUND]; i += kThreads) h[i] = hist[i];
+}
 
-  // the budget-th largest key, and how many equal to it stay: digits of 11,
-  // 11 and 10 bits
-  uint32_t prefix = 0, mask = 0, need = uint32_t(a.budget);
-#pragma unroll 1
-  for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
-    const uint32_t bins = shift ? BINS : 1024;
-    for (uint32_t i = tid; i < bins; i += THREADS) hist[i] = 0;
+// The places to fill and what fills them.
+constexpr int kMaxSegments = kMaxEvictLen / kSegment;
+__global__ __launch_bounds__(kThreads) void spread_place_kernel(EvictKernelArgs a, SpreadArgs s) {
+  __shared__ uint32_t hist[kBins[2]], sums[kWaves], lds[kWaves];
+  __shared__ uint32_t seg_kept[kMaxSegments], seg_equal[kMaxSegments];
+  const Segment g = segment(a, s);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  if (g.len <= a.budget || g.seg >= g.used) return;
+  if (spread_missing(s, g)) return;
+  const int stay = a.budget;
+  const Found f0 = s.found[g.pair], f1 = s.found[s.pairs + g.pair];
+  Found f = f1;
+  const int round = f0.all ? 0 : f1.all ? 1 : 2;   // the digit that decides
+  if (round == 2) {
+    sum_hists<2>(s, g, hist);
+    f = next_digit<2>(f, hist, sums, lane, wave);
     __syncthreads();
-    for (int j = tid; j < len; j += THREADS) {
-      const uint32_t k = keys[j];
-      const bool in = (k & mask) == prefix;
-      const uint32_t digit = (k >> shift) & (bins - 1);
-      const uint64_t who = __ballot(in);
-      if (in) {
-        // one addition for a wave whose keys agree (equal weights)
-        const uint32_t first = uint32_t(uniform(int(digit)));
-        if (__ballot(digit == first) == who) {
-          if (lane == __builtin_ctzll(who)) atomicAdd(&hist[digit], uint32_t(__popcll(who)));
-        } else {
-          atomicAdd(&hist[digit], 1u);
-        }
-      }
-    }
-    __syncthreads();
-    // thread t: the digits from bins - 1 - t n down
-    const int n = int(bins) / THREADS > 0 ? int(bins) / THREADS : 1;
-    const int top = int(bins) - 1 - tid * n;
-    uint32_t sum = 0, total;
-    for (int i = 0; i < n; ++i) sum += top - i >= 0 ? hist[top - i] : 0;
-    uint32_t over = scan<WAVES>(sum, lds, total);
-    if (over < need && over + sum >= need) {
-      for (int i = 0; i < n; ++i) {
-        const uint32_t h = hist[top - i];
-        if (over < need && over + h >= need) {
-          chosen[0] = uint32_t(top - i);
-          chosen[1] = need - over;
-        }
-        over += h;
-      }
-    }
-    __syncthreads();
-    prefix |= chosen[0] << shift;
-    need = chosen[1];
-    mask |= (bins - 1) << shift;
   }
-
-  // a word a wave: which keys are above and which equal
-  for (int w = wave; w < nwords; w += WAVES) {
-    const int j = 64 * w + lane;
-    const uint32_t k = j < len ? keys[j] : 0;
-    const uint64_t gt = __ballot(j < len && k > prefix), eq = __ballot(j < len && k == prefix);
+  // per segment: keys above the deciding prefix, and keys with it
+  const int shift = kShift[round], bins = kBins[round];
+  const uint32_t digit = (f.prefix >> shift) & uint32_t(bins - 1);
+  for (int k = wave; k < g.used; k += kWaves) {
+    const uint32_t* h = s.hist + (size_t(g.pair) * s.segments + k) * kHists + kHistAt[round];
+    uint32_t n = 0;
+    if (round == 2)
+      for (int i = lane; i < bins; i += 64) n += uint32_t(i) > digit ? h[i] : 0;
+    n = lane_of(wave_scan(n), 63);
     if (lane == 0) {
-      above[w] = gt;
-      equal[w] = eq;
+      n += s.above[size_t(g.pair) * s.segments + k];
+      if (round > 0) n += s.above[(size_t(s.pairs) + g.pair) * s.segments + k];
+      seg_kept[k] = n;
+      seg_equal[k] = h[digit];
     }
   }
   __syncthreads();
-  // of the equal ones the first `need` stay
-  uint32_t before = 0;
-  for (int w0 = 0; w0 < nwords; w0 += THREADS) {
-    const int w = w0 + tid;
-    const uint64_t eq = w < nwords ? equal[w] : 0;
-    uint32_t total;
-    const uint32_t rank = before + scan<WAVES>(uint32_t(__popcll(eq)), lds, total);
-    before += total;
-    if (w < nwords) {
-      uint64_t take = rank < need ? eq : 0;
-      while (take && rank + uint32_t(__popcll(take)) > need) take &= ~(uint64_t(1) << (63 - __builtin_clzll(take)));
-      kept[w] = above[w] | take;
+  if (tid == 0) {   // prefix sums in the order of segments: equal keys, then kept ones
+    uint32_t eq = 0;
+    for (int k = 0; k < g.used; ++k) {
+      const uint32_t e = seg_equal[k];
+      seg_kept[k] += eq < f.need ? min(f.need - eq, e) : 0;
+      seg_equal[k] = eq;
+      eq += e;
+    }
+    uint32_t n = 0;
+    for (int k = 0; k < g.used; ++k) {
+      const uint32_t e = seg_kept[k];
+      seg_kept[k] = n;
+      n += e;
     }
   }
   __syncthreads();
-  // ranks of the holes below the new length and of what fills them: prefix
-  // sums over words, in the place of `above` (holes) and `equal` (fills)
-  uint32_t holes = 0, fills = 0;
-  for (int w0 = 0; w0 < nwords; w0 += THREADS) {
-    const int w = w0 + tid;
-    uint32_t h = 0, f = 0;
-    if (w < nwords) {
-      const int below = min(max(stay - 64 * w, 0), 64);
-      const uint64_t low = below == 64 ? ~uint64_t(0) : (uint64_t(1) << below) - 1;
-      h = uint32_t(__popcll(~kept[w] & low));
-      f = uint32_t(__popcll(kept[w] & ~low));
+  // a bit a slot of this thread's four in a segment
+  const uint32_t* keys = a.keys + size_t(g.pair) * a.key_stride;
+  const auto kept_in = [&](int seg) {
+    const int j = seg * kSegment + 4 * tid;
+    const u32x4 k = j < g.len ? *reinterpret_cast<const u32x4*>(keys + j) : u32x4{0, 0, 0, 0};
+    uint32_t equal = 0, bits = 0, total;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      equal += j + e < g.len && (k[e] & f.mask) == f.prefix;
+      bits |= uint32_t(j + e < g.len && (k[e] & f.mask) >= f.prefix) << e;
     }
-    uint32_t th, tf;
-    const uint32_t rh = holes + scan<WAVES>(h, lds, th), rf = fills + scan<WAVES>(f, lds, tf);
-    if (w < nwords) {
-      above[w] = rh;
-      equal[w] = rf;
-    }
-    holes += th;
-    fills += tf;
-  }
-  __syncthreads();
-  uint64_t* dst = a.dst + size_t(pair) * a.most;
-  uint64_t* src = a.src + size_t(pair) * a.most;
-  for (int w = wave; w < nwords; w += WAVES) {
-    const uint64_t stays = kept[w];
-    const int j = 64 * w + lane, below = min(max(stay - 64 * w, 0), 64);
-    const uint64_t low = below == 64 ? ~uint64_t(0) : (uint64_t(1) << below) - 1;
-    const uint64_t bit = uint64_t(1) << lane, under = bit - 1;
-    if (~stays & low & bit) dst[above[w] + __popcll(~stays & low & under)] = at(j);
-    if (stays & ~low & bit) src[equal[w] + __popcll(stays & ~low & under)] = at(j);
-    if (lane < 16) a.flags[size_t(pair) * (a.key_stride / 4) + 16 * w + lane] = uint8_t(stays >> (4 * lane) & 15);
-  }
-  if (tid == 0) a.count[pair] = int(holes);
+    uint32_t rank = seg_equal[seg] + scan<kWaves>(equal, lds, total);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < g.len && (k[e] & f.mask) == f.prefix && rank++ >= f.need) bits &= ~(1u << e);
+    return bits;
+  };
+  const auto low_bits = [&](int seg) { return (1u << min(max(stay - seg * kSegment - 4 * tid, 0), 4)) - 1; };
+  // kept slots below the new length: those before the segment that it cuts,
+  // and that segment's own
+  const int cut = stay / kSegment;
+  uint32_t total;
+  scan<kWaves>(uint32_t(__popc(kept_in(cut) & low_bits(cut))), lds, total);
+  const uint32_t kept_low = seg_kept[cut] + total;
+
+  const uint32_t kept = kept_in(g.seg), low = low_bits(g.seg);
+  const uint32_t before = seg_kept[g.seg] + scan<kWaves>(uint32_t(__popc(kept)), lds, total);   // kept slots before j
+  const int j = g.seg * kSegment + 4 * tid;
+  if (g.seg == 0 && tid == 0) a.count[g.pair] = stay - int(kept_low);
+  if (j >= g.len) return;
+  a.flags[size_t(g.pair) * (a.key_stride / 4) + j / 4] = uint8_t(kept);
+  const uint64_t x = g.at(j);
+  uint64_t* dst = a.dst + size_t(g.pair) * a.most;
+  uint64_t* src = a.src + size_t(g.pair) * a.most;
+  // a hole's rank is the slots before it less the kept ones, a fill's the
+  // kept ones before it less those that lie low
+  uint32_t hole = uint32_t(j) - before, fill = before + uint32_t(__popc(kept & low)) - kept_low;
+  for (uint32_t m = ~kept & low; m; m &= m - 1) dst[hole++] = x + __builtin_ctz(m);
+  for (uint32_t m = kept & ~low; m; m &= m - 1) src[fill++] = x + __builtin_ctz(m);
 }
 
 __global__ __launch_bounds__(256) void move_kernel(EvictKernelArgs a) {
@@ -593,10 +692,17 @@ EvictPlan evict_plan(const gbb_paged_cache& c, int B, int max_len, int budget) {
   p.count_off = 0;
   p.dst_off = up(pairs * 4);
   p.src_off = p.dst_off + up(pairs * p.most * 8);
-  p.word_off = p.src_off + up(pairs * p.most * 8);
-  p.flag_off = p.word_off + (max_len > kMaxHeld ? up(pairs * 3 * (p.key_stride / 64) * 8) : 0);
+  p.flag_off = p.src_off + up(pairs * p.most * 8);
   p.key_off = p.flag_off + up(pairs * (p.key_stride / 4));
-  p.ws_bytes = p.key_off + (max_len > kMaxHeld ? up(pairs * p.key_stride * 4) : 0);
+  // (held rows are faster up to where registers end, however few they are: 16
+  // pairs of 32768 slots 32 us, spread 50)
+  p.spread = max_len > kMaxHeld;
+  p.segments = (max_len + kSegment - 1) / kSegment;
+  const size_t segs = pairs * p.segments;
+  p.seg_off = p.key_off + (p.spread ? up(pairs * p.key_stride * 4) : 0);
+  p.found_off = p.seg_off + (p.spread ? up(segs * 4 * 4) : 0);   // newest, missing, two counts
+  p.hist_off = p.found_off + (p.spread ? up(pairs * 2 * sizeof(Found)) : 0);
+  p.ws_bytes = p.hist_off + (p.spread ? up(segs * kHists * 4) : 0);
   return p;
 }
 
@@ -616,7 +722,6 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
   a.dst = reinterpret_cast<uint64_t*>(x.ws + p.dst_off);
   a.src = reinterpret_cast<uint64_t*>(x.ws + p.src_off);
   a.keys = reinterpret_cast<uint32_t*>(x.ws + p.key_off);
-  a.words = reinterpret_cast<uint64_t*>(x.ws + p.word_off);
   a.flags = reinterpret_cast<uint8_t*>(x.ws + p.flag_off);
   a.key_stride = p.key_stride;
   a.most = p.most;
@@ -630,12 +735,32 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
   a.lshift = __builtin_ctz(unsigned(c.head_dim * (c.dtype == GBB_E4M3 ? 1 : 2) / 16));
   a.other = x.weights_out != c.weights || x.positions_out != c.positions;
   const unsigned pairs = unsigned(x.B) * c.kv_heads;
-  const bool finish = p.most <= size_t(kFew) && x.max_len <= 16384;
-  if (x.max_len <= 4096) run_select<1>(a, pairs, finish, s);
-  else if (x.max_len <= 8192) run_select<2>(a, pairs, finish, s);
-  else if (x.max_len <= 16384) run_select<4>(a, pairs, finish, s);
-  else if (x.max_len <= kMaxHeld) run_select<8>(a, pairs, finish, s);
-  else hipLaunchKernelGGL(select_long_kernel, dim3(pairs), dim3(kThreads), 0, s, a);
+  const bool finish = !p.spread && p.most <= size_t(kFew) && x.max_len <= 16384;
+  if (p.spread) {
+    SpreadArgs g;
+    const size_t segs = size_t(pairs) * p.segments;
+    g.newest = reinterpret_cast<int32_t*>(x.ws + p.seg_off);
+    g.missing = g.newest + segs;
+    g.above = reinterpret_cast<uint32_t*>(g.missing + segs);
+    g.found = reinterpret_cast<Found*>(x.ws + p.found_off);
+    g.hist = reinterpret_cast<uint32_t*>(x.ws + p.hist_off);
+    g.segments = p.segments;
+    g.pairs = int(pairs);
+    const dim3 grid(static_cast<unsigned>(segs)), block(kThreads);
+    hipLaunchKernelGGL(spread_newest_kernel, grid, block, 0, s, a, g);
+    hipLaunchKernelGGL((spread_hist_kernel<0>), grid, block, 0, s, a, g);
+    hipLaunchKernelGGL((spread_hist_kernel<1>), grid, block, 0, s, a, g);
+    hipLaunchKernelGGL((spread_hist_kernel<2>), grid, block, 0, s, a, g);
+    hipLaunchKernelGGL(spread_place_kernel, grid, block, 0, s, a, g);
+  } else if (x.max_len <= 4096) {
+    run_select<1>(a, pairs, finish, s);
+  } else if (x.max_len <= 8192) {
+    run_select<2>(a, pairs, finish, s);
+  } else if (x.max_len <= 16384) {
+    run_select<4>(a, pairs, finish, s);
+  } else {
+    run_select<8>(a, pairs, finish, s);
+  }
   if (!finish) {
     const size_t per = 256 >> a.lshift;
     const size_t most = std::max((p.most + per - 1) / per, (size_t(x.max_len) + 255) / 256);

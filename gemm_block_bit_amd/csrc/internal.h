@@ -154,10 +154,13 @@ struct AttendArgs {
 };
 int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPlan& p, void* stream);
 
+constexpr int kMaxEvictLen = 512 * 4096;   // slots of a sequence that gbb_cache_evict takes
 struct EvictPlan {
   size_t key_stride;    // ranking keys per (sequence, kv head), a multiple of 64
   size_t most;          // rows that can move per (sequence, kv head)
-  size_t count_off, dst_off, src_off, word_off, flag_off, key_off, ws_bytes;
+  bool spread;          // rows over workgroups of 4096 slots each
+  int segments;         // such workgroups a row
+  size_t count_off, dst_off, src_off, flag_off, key_off, seg_off, found_off, hist_off, ws_bytes;
 };
 EvictPlan evict_plan(const gbb_paged_cache& c, int B, int max_len, int budget);
 struct EvictArgs {

@@ -566,7 +566,8 @@ size_t gbb_cache_evict_workspace(const gbb_paged_cache* cache, int B, int max_le
  *              (both must be there), and may be the same memory; in other
  *              memory, all slots below lengths[b] are written.  Slots from
  *              the new length up to lengths[b] get weight 0 and position -1.
- *   0 <= recent <= budget, 1 <= budget, 1 <= max_len <= max_pages * page.
+ *   0 <= recent <= budget, 1 <= budget, 1 <= max_len <= max_pages * page,
+ *   max_len <= 2^21.
  * k and v change in place.  Two sequences must not share a page.  A sequence
  * with an entry outside [0, num_pages) among its pages is left as it is.
  * B = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN,

@@ -105,6 +105,33 @@ def test_long(n, budget, recent, weight):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("weight", ["heavy", "ties", "equal", "wild", "close"])
+@pytest.mark.parametrize("budget,recent,in_place", [(1, 0, True), (4096, 100, False), (4095, 0, True), (4100, 4100, True),
+                                                    (8192, 1000, True), (8999, 5, False), (5000, 64, False)])
+def test_rows_over_several_workgroups(budget, recent, in_place, weight):
+    """Rows above 32768 slots (a bound on the lengths above it takes short ones
+    the same way), with the new length at, before and after the bounds of
+    4096 slots that workgroups take."""
+    run_and_check([33000, 9000, 8192, 4097, 8193, 100, 0], 1, 64, 64, "e4m3", budget, recent, budget, weight, in_place)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [0, 70, 515])
+def test_long_row_with_a_missing_page(page):
+    def table(bt):
+        bt[0, page] = -3
+    run_and_check([33000, 8800], 1, 64, 64, "e4m3", 4500, 8, page, table=table)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("n,budget,recent", [(12000, 11950, 64), (12000, 40, 10), (16384, 16383, 0), (16385, 16384, 100),
+                                             (20000, 7000, 1000), (32768, 20000, 0), (32768, 32767, 5)])
+def test_rows_in_registers(n, budget, recent, in_place):
+    run_and_check([n, n // 3, budget + 1], 1, 64, 128, "e4m3", budget, recent, n, "ties", in_place, max_len=n)
+
+
+@pytest.mark.gpu
 def test_one_very_long_sequence():
     run_and_check([40000], 1, 64, 256, "e4m3", 3000, 500, 40)
 
