@@ -18,9 +18,9 @@
 // else a second launch moves rows and writes weights and positions over as
 // many workgroups as the slots give.
 //
-// Measured (GPU time): 256 pairs of 2049 slots cut by one 9.1 us, of which
-// about 7 are the chain of dependent steps in a workgroup (load, newest
-// position, three digits, two prefix sums); 16 pairs of 32768 slots of 128
+// Measured (GPU time): 256 pairs of 2049 slots cut by one 6.7 us, of which
+// about 4.5 are the chain of dependent steps in a workgroup (page, load, newest
+// position, smallest key, places, move); 16 pairs of 32768 slots of 128
 // fp16 elements cut to 4096 40 us: 21 in 16 workgroups that each read their
 // row twice (no more than 16 of the 256 CUs have work), 15 in the moves (4
 // TB/s).
@@ -35,7 +35,8 @@ namespace gbb {
 namespace {
 
 constexpr int kMaxHeld = 32 * 1024;   // slots a row whose keys a workgroup's registers hold
-constexpr int kFew = 64;              // rows that the selecting workgroup moves itself
+constexpr int kOneByOne = 4;          // slots that are found one by one
+constexpr int kFew = 64;               // rows that the selecting workgroup moves itself
 
 struct EvictKernelArgs {
   const int32_t* block_table;
@@ -136,6 +137,19 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2 and 3
   return x;
 }
+// The least of the wave's values, in all lanes.
+__device__ __forceinline__ uint32_t wave_least(uint32_t x) {
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x111, 0xf, 0xf, false)));
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x112, 0xf, 0xf, false)));
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x114, 0xf, 0xf, false)));
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x118, 0xf, 0xf, false)));
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x142, 0xa, 0xf, false)));
+  x = min(x, uint32_t(__builtin_amdgcn_update_dpp(-1, x, 0x143, 0xc, 0xf, false)));
+  return uint32_t(__builtin_amdgcn_readlane(int(x), 63));
+}
+// The largest of the wave's signed values: the order of complements with the
+// sign bit as a digit.
+__device__ __forceinline__ int wave_largest(int x) { return int(~wave_least(~(uint32_t(x) ^ 0x80000000u)) ^ 0x80000000u); }
 __device__ __forceinline__ uint32_t lane_of(uint32_t x, int lane) {
   return uint32_t(__builtin_amdgcn_readlane(int(x), lane));
 }
@@ -199,6 +213,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   __shared__ uint32_t hist[kBins[0] + kBins[1] + kBins[2]];
   __shared__ uint32_t sums[3][kWaves], counts[2][NB * kWaves];
   __shared__ int tops[kWaves];
+  __shared__ uint64_t leasts[2][kWaves];
   __shared__ uint64_t few[2][kFew];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int pair = blockIdx.x, hk = pair % a.Hkv, b = pair / a.Hkv;
@@ -245,8 +260,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     for (int e = 0; e < 4; ++e)
       if (slot(i, e) < len) newest = max(newest, q[e]);
   }
-#pragma unroll
-  for (int k = 1; k < 64; k *= 2) newest = max(newest, __shfl_xor(newest, k));
+  newest = wave_largest(newest);
   if (lane == 0) tops[wave] = newest;
   bad = __syncthreads_or(bad);
   if (tid == 0 && hk == 0) a.lengths_out[b] = bad ? len : stay;
@@ -254,8 +268,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     if (tid == 0 && !FINISH) a.count[pair] = -1;
     return;
   }
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) newest = max(newest, tops[i]);
+  newest = wave_largest(tops[lane & (kWaves - 1)]);
   // the distance to the newest position is exact in 32 unsigned bits
   uint32_t key[NB][4];
 #pragma unroll
@@ -267,42 +280,6 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
       key[i][e] = uint32_t(newest) - uint32_t(q[e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(v[e]);
     if (!HOLD && i % 4 == 3) asm volatile("" ::: "memory");   // four runs' loads at a time
   }
-
-  // the budget-th largest key, digit by digit, until all that share the
-  // digits so far stay
-  uint32_t prefix = 0, mask = 0, need = uint32_t(stay);
-  const auto round = [&](auto bins, uint32_t* h, uint32_t* s, int shift) {
-    constexpr int BINS = decltype(bins)::value;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      if (slot(i, 0) - 4 * tid >= len) continue;
-      uint32_t digit[4];
-      bool in[4];
-      bool one = true;   // all four in, with the digit of the wave's first
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        in[e] = slot(i, e) < len && (key[i][e] & mask) == prefix;
-        digit[e] = (key[i][e] >> shift) & (BINS - 1);
-        one = one && in[e] && digit[e] == uint32_t(uniform(int(digit[0])));
-      }
-      if (__all(one)) {
-        // one addition for a wave whose keys agree (equal weights, new tokens)
-        if (lane == 0) atomicAdd(&h[digit[0]], 256u);
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (in[e]) atomicAdd(&h[digit[e]], 1u);
-    }
-    __syncthreads();
-    const uint32_t d = find_digit<BINS>(h, s, need, lane, wave);
-    prefix |= d << shift;
-    mask |= uint32_t(BINS - 1) << shift;
-    return h[d] == need;
-  };
-  bool all = round(std::integral_constant<int, kBins[0]>(), hist, sums[0], kShift[0]);
-  if (!all) all = round(std::integral_constant<int, kBins[1]>(), hist + kBins[0], sums[1], kShift[1]);
-  if (!all) all = round(std::integral_constant<int, kBins[2]>(), hist + kBins[0] + kBins[1], sums[2], kShift[2]);
 
   // Sums of mine[] over the runs before this thread's run i, in slot order.
   const auto before = [&](uint32_t (&mine)[NB], uint32_t* lds, uint32_t (&out)[NB]) {
@@ -328,25 +305,94 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   };
   uint32_t kept[NB];   // a bit a slot
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    kept[i] = 0;
+  for (int i = 0; i < NB; ++i) kept[i] = (1u << min(max(len - slot(i, 0), 0), 4)) - 1;
+  if (HOLD && len - stay <= kOneByOne) {
+    // few to drop: the smallest key, of equal ones the last slot, one by one
+    // (256 pairs of 2049 slots cut by 1 or 4: 6.7 and 8.4 us, 9.1 by digits)
+    for (int k = 0; k < len - stay; ++k) {
+      uint32_t least = ~0u, last = ~0u;   // a key, and the complement of a slot
 #pragma unroll
-    for (int e = 0; e < 4; ++e) kept[i] |= uint32_t(slot(i, e) < len && (key[i][e] & mask) >= prefix) << e;
-  }
-  if (!all) {   // of the keys equal to the last the first `need` stay
-    uint32_t n[NB], rank[NB];
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      n[i] = 0;
+        for (int e = 0; e < 4; ++e)
+          if (kept[i] >> e & 1) {
+            last = key[i][e] <= least ? ~uint32_t(slot(i, e)) : last;
+            least = min(least, key[i][e]);
+          }
+      const auto join = [&] {   // over the lanes
+        const uint32_t m = wave_least(least);
+        last = wave_least(least == m ? last : ~0u);
+        least = m;
+      };
+      join();
+      if (lane == 0) leasts[k & 1][wave] = uint64_t(least) << 32 | last;
+      __syncthreads();
+      const uint64_t other = leasts[k & 1][lane & (kWaves - 1)];
+      least = uint32_t(other >> 32);
+      last = uint32_t(other);
+      join();
+      const int gone = int(~last);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) n[i] += slot(i, e) < len && key[i][e] == prefix;
+      for (int i = 0; i < NB; ++i)
+        if (gone >> 2 == slot(i, 0) >> 2) kept[i] &= ~(1u << (gone & 3));
     }
-    before(n, counts[0], rank);
+  } else {
+    // the budget-th largest key, digit by digit, until all that share the
+    // digits so far stay
+    uint32_t prefix = 0, mask = 0, need = uint32_t(stay);
+    const auto round = [&](auto bins, uint32_t* h, uint32_t* s, int shift) {
+      constexpr int BINS = decltype(bins)::value;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        if (slot(i, 0) - 4 * tid >= len) continue;
+        uint32_t digit[4];
+        bool in[4];
+        bool one = true;   // all four in, with the digit of the wave's first
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          in[e] = slot(i, e) < len && (key[i][e] & mask) == prefix;
+          digit[e] = (key[i][e] >> shift) & (BINS - 1);
+          one = one && in[e] && digit[e] == uint32_t(uniform(int(digit[0])));
+        }
+        if (__all(one)) {
+          // one addition for a wave whose keys agree (equal weights, new tokens)
+          if (lane == 0) atomicAdd(&h[digit[0]], 256u);
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (in[e]) atomicAdd(&h[digit[e]], 1u);
+      }
+      __syncthreads();
+      const uint32_t d = find_digit<BINS>(h, s, need, lane, wave);
+      prefix |= d << shift;
+      mask |= uint32_t(BINS - 1) << shift;
+      return h[d] == need;
+    };
+    bool all = round(std::integral_constant<int, kBins[0]>(), hist, sums[0], kShift[0]);
+    if (!all) all = round(std::integral_constant<int, kBins[1]>(), hist + kBins[0], sums[1], kShift[1]);
+    if (!all) all = round(std::integral_constant<int, kBins[2]>(), hist + kBins[0] + kBins[1], sums[2], kShift[2]);
+
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (slot(i, e) < len && key[i][e] == prefix && rank[i]++ >= need) kept[i] &= ~(1u << e);
+        if ((key[i][e] & mask) < prefix) kept[i] &= ~(1u << e);
+    if (!all) {   // of the keys equal to the last the first `need` stay
+      uint32_t n[NB], rank[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        n[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n[i] += slot(i, e) < len && key[i][e] == prefix;
+      }
+      before(n, counts[0], rank);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (slot(i, e) < len && key[i][e] == prefix && rank[i]++ >= need) kept[i] &= ~(1u << e);
+    }
   }
   // holes below the new length (low half) and what fills them (high half)
   uint32_t n[NB], rank[NB];
