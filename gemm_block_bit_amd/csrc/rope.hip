@@ -44,12 +44,12 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[E]) {
 
 // A head is E-element units: rot / 2 / E units of pairs in the half layout
 // (unit u takes elements u E ... and rot/2 + u E ...), rot / E units in the
-// interleaved one, then (D - rot) / E units that are copied.
+// interleaved one, then (D - rot) / EC units of EC elements that are copied.
 struct Units {
   int pairs, copies;
 };
-__host__ __device__ __forceinline__ Units units(int D, int rot, int layout, int E) {
-  return {(layout == GBB_ROPE_HALF ? rot / 2 : rot) / E, (D - rot) / E};
+__host__ __device__ __forceinline__ Units units(int D, int rot, int layout, int E, int EC) {
+  return {(layout == GBB_ROPE_HALF ? rot / 2 : rot) / E, (D - rot) / EC};
 }
 
 // The table entries of unit u of the token's row: E pairs (half) or E / 2.
@@ -68,7 +68,7 @@ struct Angles {
   }
 };
 
-template <int DT, int E, bool HALF>
+template <int DT, int E, int EC, bool HALF>
 __global__ __launch_bounds__(1024) void rope_kernel(RopeArgs a, Units n, int hp, int tp) {
   typedef typename Elem<DT>::T T;
   const int nu = n.pairs + n.copies;
@@ -80,13 +80,13 @@ __global__ __launch_bounds__(1024) void rope_kernel(RopeArgs a, Units n, int hp,
   const T* x = static_cast<const T*>(a.x) + t * a.x_token;
   T* y = static_cast<T*>(a.y) + t * a.y_token;
   if (u >= n.pairs) {
-    const int d = a.rot + (u - n.pairs) * E;
+    const int d = a.rot + (u - n.pairs) * EC;
     for (int h = blockIdx.y * hp + h0; h < a.H; h += gridDim.y * hp) {
-      float v[E];
-      load_vec<T, E>(x + h * a.x_head + d, v);
+      float v[EC];
+      load_vec<T, EC>(x + h * a.x_head + d, v);
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = there ? v[i] : 0.f;
-      store_vec<T, E>(y + h * a.y_head + d, v);
+      for (int i = 0; i < EC; ++i) v[i] = there ? v[i] : 0.f;
+      store_vec<T, EC>(y + h * a.y_head + d, v);
     }
     return;
   }
@@ -240,21 +240,31 @@ Shape shape(int T, int H, int nu) {
   return s;
 }
 
-template <int DT, int E>
+template <int DT, int E, int EC>
 void run_rope(const RopeArgs& a, hipStream_t s) {
-  const Units n = units(a.D, a.rot, a.layout, E);
+  const Units n = units(a.D, a.rot, a.layout, E, EC);
   const Shape g = shape(a.T, a.H, n.pairs + n.copies);
   if (a.layout == GBB_ROPE_HALF)
-    hipLaunchKernelGGL((rope_kernel<DT, E, true>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
+    hipLaunchKernelGGL((rope_kernel<DT, E, EC, true>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
   else if constexpr (E > 1)
-    hipLaunchKernelGGL((rope_kernel<DT, E, false>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
+    hipLaunchKernelGGL((rope_kernel<DT, E, EC, false>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
+}
+template <int DT>
+void run_widths(const RopeArgs& a, int E, int EC, hipStream_t s) {
+  constexpr int W = DT == GBB_F32 ? 4 : 8;   // elements of 16 bytes
+  if constexpr (W == 8)
+    if (E == 8) return run_rope<DT, 8, 8>(a, s);
+  if (E == 4) return EC == 8 && W == 8 ? run_rope<DT, 4, W>(a, s) : run_rope<DT, 4, 4>(a, s);
+  if (E == 2) return EC == W ? run_rope<DT, 2, W>(a, s) : EC == 4 ? run_rope<DT, 2, 4>(a, s) : run_rope<DT, 2, 2>(a, s);
+  return EC == W ? run_rope<DT, 1, W>(a, s) : EC == 4 ? run_rope<DT, 1, 4>(a, s) : EC == 2 ? run_rope<DT, 1, 2>(a, s) : run_rope<DT, 1, 1>(a, s);
 }
 
 template <int DT, int CT>
 void run_append(const gbb_paged_cache& c, const AppendArgs& a, hipStream_t s) {
   const bool half = a.layout == GBB_ROPE_HALF;
   const bool wide = (half ? a.rot / 2 : a.rot) % 8 == 0;
-  const Units n = wide ? units(c.head_dim, a.rot, a.layout, 8) : units(c.head_dim, a.rot, a.layout, half ? 1 : 2);
+  const int E = wide ? 8 : half ? 1 : 2;
+  const Units n = units(c.head_dim, a.rot, a.layout, E, E);
   const Shape g = shape(a.T, a.Hq + 2 * c.kv_heads, n.pairs + n.copies);
   if (wide && half)
     hipLaunchKernelGGL((append_kernel<DT, CT, 8, true>), g.grid, dim3(g.threads), 0, s, a, c, n, g.hp, g.tp);
@@ -279,22 +289,16 @@ int launch_rope(const RopeArgs& a, void* stream) {
                         uintptr_t(a.y_head * es);
   const bool half = a.layout == GBB_ROPE_HALF;
   int E = 16 / es;
-  while (E > (half ? 1 : 2) && (run % E || (a.D - a.rot) % E || all % uintptr_t(E * es))) E /= 2;
-  if (a.dtype == GBB_F32) {
-    if (E == 4) run_rope<GBB_F32, 4>(a, s);
-    else if (E == 2) run_rope<GBB_F32, 2>(a, s);
-    else run_rope<GBB_F32, 1>(a, s);
-  } else if (a.dtype == GBB_BF16) {
-    if (E == 8) run_rope<GBB_BF16, 8>(a, s);
-    else if (E == 4) run_rope<GBB_BF16, 4>(a, s);
-    else if (E == 2) run_rope<GBB_BF16, 2>(a, s);
-    else run_rope<GBB_BF16, 1>(a, s);
-  } else {
-    if (E == 8) run_rope<GBB_F16, 8>(a, s);
-    else if (E == 4) run_rope<GBB_F16, 4>(a, s);
-    else if (E == 2) run_rope<GBB_F16, 2>(a, s);
-    else run_rope<GBB_F16, 1>(a, s);
-  }
+  while (E > (half ? 1 : 2) && (run % E || all % uintptr_t(E * es))) E /= 2;
+  // and the widest copies (16384 tokens of 32 heads of 96, 24
+  // rotated in halves: 54 us, 67 with copies as narrow as the pairs)
+  const int rest = a.D - a.rot;
+  int EC = 16 / es;
+  while (EC > E && (rest % EC || (all | uintptr_t(a.rot * es)) % uintptr_t(EC * es))) EC /= 2;
+  while (E > (half ? 1 : 2) && (rest % E || uintptr_t(a.rot * es) % uintptr_t(E * es)) && EC <= E) E /= 2, EC = E;
+  if (a.dtype == GBB_F32) run_widths<GBB_F32>(a, E, EC, s);
+  else if (a.dtype == GBB_BF16) run_widths<GBB_BF16>(a, E, EC, s);
+  else run_widths<GBB_F16>(a, E, EC, s);
   return int(hipGetLastError());
 }
 
