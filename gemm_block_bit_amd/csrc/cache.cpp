@@ -141,8 +141,12 @@ extern "C" gbb_status gbb_rope(const void* x, int64_t x_token, int64_t x_head, v
   if (!x || !y) return fail(GBB_E_ARG, "x and y must not be NULL");
   const size_t es = dtype == GBB_F32 ? 4 : 2;
   if (!aligned(x, es) || !aligned(y, es)) return fail(GBB_E_ALIGN, "x or y is not aligned to its elements");
-  // y's rows must be memory of their own; x's may repeat (a broadcast input)
-  if ((H > 1 && y_head < D) || (T > 1 && y_token < (H - 1) * y_head + D))
+  // y's rows must be memory of their own, a token's heads or a head's tokens
+  // together; x's may repeat (a broadcast input)
+  const auto apart = [&](int64_t inner, int ni, int64_t outer, int no) {
+    return (ni == 1 || inner >= D) && (no == 1 || outer >= (ni - 1) * inner + D);
+  };
+  if (!apart(y_head, H, y_token, T) && !apart(y_token, T, y_head, H))
     return fail(GBB_E_SHAPE, "y's strides %lld, %lld make its heads overlap", (long long)y_token, (long long)y_head);
   const size_t nx = (size_t(T - 1) * x_token + size_t(H - 1) * x_head + D) * es;
   const size_t ny = (size_t(T - 1) * y_token + size_t(H - 1) * y_head + D) * es;

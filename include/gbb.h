@@ -453,14 +453,15 @@ gbb_status gbb_rope_table(int rot, int n_pos, double base, const gbb_rope_scalin
  * for a table with attention 1, its inverse).
  *   x, y       device, `dtype` GBB_F16, GBB_BF16 or GBB_F32: element d of
  *              head h of token t is at t * token stride + h * head stride
- *              + d (strides in elements, 16-byte alignment not required).
- *              y == x with equal strides works in place; otherwise x and y
- *              must not overlap.
+ *              + d (strides in elements, 16-byte alignment not required;
+ *              tokens or heads may be the outer dimension, and x's strides
+ *              may be 0).  y == x with equal strides works in place;
+ *              otherwise x and y must not overlap.
  *   positions  device int32 [T]; table device float [n_pos][rot/2][2].  A
  *              token whose position is outside [0, n_pos) is padding: its
  *              y is zero.
  * T = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE (D odd or above 1024,
- * rot odd, below 2 or above D, heads of a token that overlap), GBB_E_ALIGN
+ * rot odd, below 2 or above D, heads of y that overlap), GBB_E_ALIGN
  * (a pointer that is not aligned to its element), GBB_E_DEVICE. */
 gbb_status gbb_rope(const void* x, int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head,
                     int dtype, int T, int H, int D, const int32_t* positions, const float* table, int n_pos,

@@ -188,6 +188,31 @@ def test_rope_strides_and_odd_addresses(off, head, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(1, 4), (6, 1), (6, 4)])
+def test_rope_heads_outside_tokens(T, H):
+    """Views of [H][T][D] memory, in place and as the output: the same bits as
+    the contiguous call."""
+    d = dev()
+    table = torch.from_numpy(gbb.rope_table(64, 16)).to(d)
+    pos = torch.arange(T, dtype=torch.int32, device=d) + 3
+    x = torch.randn(H, T, 64, device=d, dtype=torch.bfloat16)
+    want = gbb.rope(x.transpose(0, 1).contiguous(), pos, table)
+    assert torch.equal(gbb.rope(x.transpose(0, 1), pos, table), want)
+    y = torch.zeros_like(x)
+    gbb.rope(x.transpose(0, 1), pos, table, out=y.transpose(0, 1))
+    assert torch.equal(y.transpose(0, 1), want)
+    v = x.transpose(0, 1)
+    assert torch.equal(gbb.rope(v, pos, table, out=v), want)
+
+
+def test_rope_heads_outside_tokens_that_overlap():
+    L = gbb.lib()
+    x, y, p, t = 1 << 20, 2 << 20, 3 << 20, 4 << 20   # never read
+    for yt, yh in ((64, 64 * 4 - 1), (63, 1024), (64, 64)):   # 4 tokens of 2 heads of 64
+        assert L.gbb_rope(x, 64, 256, y, yt, yh, 0, 4, 2, 64, p, t, 8, 64, 0, 0, None) == -2
+
+
+@pytest.mark.gpu
 def test_rope_broadcast_input_padding_and_empty():
     d = dev()
     table = torch.from_numpy(gbb.rope_table(64, 16)).to(d)
