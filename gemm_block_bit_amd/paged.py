@@ -183,16 +183,24 @@ def _with_workspace(kind: str, device: int, stream: int, given, call, need):
             raise ValueError(f"workspace is on {given.device}, not on GPU {device}")
         _check(call(given.data_ptr(), given.numel() * given.element_size()))
         return
-    torch = _torch()
     key = (kind, device, stream)
     buf = _ws_cache.get(key)
     if buf is None:
-        buf = _ws_cache[key] = torch.zeros(1 << 20, dtype=torch.uint8, device=torch.device("cuda", device))
+        buf = _ws_cache[key] = _new_workspace(1 << 20, device)
     st = call(buf.data_ptr(), buf.numel())
     if st == _E_SPACE:
-        buf = _ws_cache[key] = torch.zeros(need(), dtype=torch.uint8, device=buf.device)
+        buf = _ws_cache[key] = _new_workspace(need(), device)
         st = call(buf.data_ptr(), buf.numel())
     _check(st)
+
+
+def _new_workspace(nbytes: int, device: int):
+    """Not during a capture: the buffer would be the graph's memory, and its
+    clearing a part of every replay."""
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("a call that is captured in a graph needs its workspace given")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
 
 
 def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, layout: str = "half", out=None):
@@ -234,7 +242,7 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     device, D = cache._index, cache.head_dim
     if _device_of(q, "q") != device:
         raise ValueError(f"q is on {q.device}, not on GPU {device}")
-    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
+    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or (q.stride(1) != D and q.shape[1] != 1):
         raise ValueError(f"q must be [B][q_heads][{D}] with contiguous tokens")
     shape = q.shape
     B, q_heads = shape[0], shape[1]

@@ -304,6 +304,29 @@ def test_in_a_graph():
 
 
 @pytest.mark.gpu
+def test_a_capture_needs_its_workspace_given(monkeypatch):
+    """A buffer made during a capture would be the graph's."""
+    monkeypatch.setattr(gbb.paged, "_ws_cache", {})
+    s = Setup([900, 40], 4, 2, 64, seed=14)
+    q, out = s.q.to(dev()), torch.zeros(2, 4, 64, device=dev(), dtype=torch.float16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="workspace"):
+            gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len, out=out)
+        q.add_(0)
+    s.check(gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len, out=out))
+
+
+@pytest.mark.gpu
+def test_one_head_of_any_stride():
+    """The stride of a dimension of one element says nothing."""
+    s = Setup([70, 5], 1, 1, 64, seed=15)
+    first = s.run()
+    q = s.q.to(dev()).as_strided((2, 1, 64), (64, 7, 1))
+    assert torch.equal(gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len), first)
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits():
     """Pages whose byte offsets pass 2^32 in a cache of 6 GiB a side."""
     d = dev()
