@@ -216,12 +216,17 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
     if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
         raise ValueError(f"qkv must be [T][{width}] with contiguous rows")
     T = qkv.shape[0]
-    q = out if out is not None else torch.empty((T, q_heads, D), dtype=qkv.dtype, device=qkv.device)
+    if out is None:
+        q = qkv.new_empty(T, q_heads, D)
+        qp = q.data_ptr()
+    else:
+        q = out
+        qp = _ptr(q, qkv.dtype, device, "out", (T, q_heads, D))
     tp, n_pos, rot = _table(table, device)
     _check(lib().gbb_rope_append(
         cache._ref, qkv.data_ptr(), qkv.stride(0) if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
         _ptr(positions, torch.int32, device, "positions", (T,)), _ptr(slots, torch.int32, device, "slots", (T,)), tp,
-        n_pos, rot, _layout(layout), _ptr(q, qkv.dtype, device, "out", (T, q_heads, D)), _raw_stream(device)))
+        n_pos, rot, _layout(layout), qp, _raw_stream(device)))
     return q
 
 
@@ -246,7 +251,12 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
         raise ValueError(f"q must be [B][q_heads][{D}] with contiguous tokens")
     shape = q.shape
     B, q_heads = shape[0], shape[1]
-    o = out if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
+    if out is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op = o.data_ptr()
+    else:
+        o = out
+        op = _ptr(o, q.dtype, device, "out", shape)
     bt = _ptr(block_table, torch.int32, device, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}][pages]")
@@ -258,8 +268,7 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     L, stream = lib(), _raw_stream(device)
     args = (cache._ref, q.data_ptr(), q.stride(0), _dtype_code(q.dtype), B, q_heads, bt, block_table.shape[1],
             _ptr(lengths, torch.int32, device, "lengths", (B,)), max_len, D ** -0.5 if scale is None else scale,
-            _ptr(o, q.dtype, device, "out", shape),
-            _ptr(lse, torch.float32, device, "lse", (B, q_heads)) if lse is not None else None, w)
+            op, _ptr(lse, torch.float32, device, "lse", (B, q_heads)) if lse is not None else None, w)
     _with_workspace("attention", device, stream, workspace,
                     lambda ws, n: L.gbb_paged_attention(*args, ws, n, stream),
                     lambda: L.gbb_paged_attention_workspace(cache._ref, B, q_heads, max_len, int(w is not None)))
