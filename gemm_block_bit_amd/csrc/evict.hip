@@ -21,9 +21,9 @@
 // Measured (GPU time): 256 pairs of 2049 slots cut by one 6.7 us, of which
 // about 4.5 are the chain of dependent steps in a workgroup (page, load, newest
 // position, smallest key, places, move); 16 pairs of 32768 slots of 128
-// fp16 elements cut to 4096 40 us: 21 in 16 workgroups that each read their
-// row twice (no more than 16 of the 256 CUs have work), 15 in the moves (4
-// TB/s).
+// fp16 elements cut to 4096 34 us: 20 in the selection, where 16 of the 256
+// CUs have work (4 of it the row's loads, the rest some 30 instructions a key),
+// and 15 in the moves (4 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -126,6 +126,10 @@ __device__ __forceinline__ void settle(const EvictKernelArgs& a, const Slots& at
 constexpr int kThreads = 1024, kWaves = 16;
 constexpr int kBins[3] = {2048, 2048, 1024};   // digits of 11, 11 and 10 bits
 constexpr int kShift[3] = {21, 10, 0};
+// Words a bin of the first digit has in select_kernel, a lane's by its number:
+// weights crowd a few exponents, and additions to one word go one by one (16
+// pairs of 32768: 20.1 us; 20.6 with 2 words, 20.9 with 8).
+constexpr int kCopies = 4;
 
 // Inclusive sum over the wave's lanes up to this one.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
@@ -154,15 +158,23 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t x, int lane) {
   return uint32_t(__builtin_amdgcn_readlane(int(x), lane));
 }
 
+template <int COPIES>
+__device__ __forceinline__ uint32_t bin(const uint32_t* hist, int i) {
+  uint32_t s = 0;
+#pragma unroll
+  for (int c = 0; c < COPIES; ++c) s += hist[i * COPIES + c];
+  return s;
+}
+
 // The digit that holds the need-th largest entry of a histogram, in every
 // wave: sums of 16 groups of bins first, then the bins of one group.  After:
-// need is the rank within the digit.
-template <int BINS>
+// need is the rank within the digit.  Each bin is the sum of COPIES words.
+template <int BINS, int COPIES = 1>
 __device__ __forceinline__ uint32_t find_digit(const uint32_t* hist, uint32_t* sums, uint32_t& need, int lane, int wave) {
   constexpr int G = BINS / kWaves, N = G / 64;   // bins a group, bins a lane
   uint32_t s = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) s += hist[wave * G + lane * N + i];
+  for (int i = 0; i < N; ++i) s += bin<COPIES>(hist, wave * G + lane * N + i);
   s = wave_scan(s);
   if (lane == 63) sums[wave] = s;
   __syncthreads();
@@ -174,7 +186,7 @@ __device__ __forceinline__ uint32_t find_digit(const uint32_t* hist, uint32_t* s
   // lane i: bins from the group's top down
   uint32_t h[N], sum = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum += h[i] = hist[group * G + G - 1 - lane * N - i];
+  for (int i = 0; i < N; ++i) sum += h[i] = bin<COPIES>(hist, group * G + G - 1 - lane * N - i);
   const uint32_t is = wave_scan(sum);
   const int at = __builtin_ctzll(__ballot(is >= need));
   need -= lane_of(is, at) - lane_of(sum, at);
@@ -210,7 +222,7 @@ __device__ __forceinline__ void leave(const EvictKernelArgs& a, const Slots& at,
 // runs).  FINISH: this launch moves the rows too (at most kFew).
 template <int NB, bool FINISH>
 __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
-  __shared__ uint32_t hist[kBins[0] + kBins[1] + kBins[2]];
+  __shared__ __align__(16) uint32_t hist[kCopies * kBins[0] + kBins[1] + kBins[2]];
   __shared__ uint32_t sums[3][kWaves], counts[2][NB * kWaves];
   __shared__ int tops[kWaves];
   __shared__ uint64_t leasts[2][kWaves];
@@ -224,13 +236,14 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     leave(a, at, pair, hk, b, len, FINISH);
     return;
   }
-  for (int i = tid; i < kBins[0] + kBins[1] + kBins[2]; i += kThreads) hist[i] = 0;
+  const bool one_by_one = NB <= 4 && len - stay <= kOneByOne;
+  if (!one_by_one)
+    for (int i = tid; i < int(sizeof(hist) / 16); i += kThreads) reinterpret_cast<i32x4*>(hist)[i] = i32x4{0, 0, 0, 0};
 
-  constexpr bool HOLD = NB <= 4;   // registers enough for weights and positions to stay in them
-  static_assert(HOLD || !FINISH, "a launch that finishes holds them to the end");
+  static_assert(NB <= 4 || !FINISH, "a launch that finishes holds weights and positions in registers to the end");
   int page[NB];
-  f32x4 w[HOLD ? NB : 1];
-  i32x4 p[HOLD ? NB : 1];
+  f32x4 w[NB];
+  i32x4 p[NB];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
@@ -243,22 +256,19 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     return ((size_t(page[i]) * a.Hkv + hk) << a.pshift) + (min(4096 * i + 4 * tid, (len - 1) & ~3) & ((1 << a.pshift) - 1));
   };
   const auto slot = [&](int i, int e) { return 4096 * i + 4 * tid + e; };
+  // slots of the run i that is loaded that are below the length
+  const auto below = [&](int i) { return 4096 * (i + 1) <= len ? 4 : len - min(slot(i, 0), (len - 1) & ~3); };
   int newest = INT32_MIN;
-  const auto load_w = [&](int i) { return *reinterpret_cast<const f32x4*>(a.weights + place(i)); };
-  const auto load_p = [&](int i) { return *reinterpret_cast<const i32x4*>(a.positions + place(i)); };
-  if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      w[i] = load_w(i);
-      p[i] = load_p(i);
-    }
+  for (int i = 0; i < NB; ++i) {
+    w[i] = *reinterpret_cast<const f32x4*>(a.weights + place(i));
+    p[i] = *reinterpret_cast<const i32x4*>(a.positions + place(i));
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const i32x4 q = HOLD ? p[HOLD ? i : 0] : load_p(i);
+    const int n = below(i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (slot(i, e) < len) newest = max(newest, q[e]);
+    for (int e = 0; e < 4; ++e) newest = e < n ? max(newest, p[i][e]) : newest;
   }
   newest = wave_largest(newest);
   if (lane == 0) tops[wave] = newest;
@@ -269,17 +279,17 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     return;
   }
   newest = wave_largest(tops[lane & (kWaves - 1)]);
-  // the distance to the newest position is exact in 32 unsigned bits
+  // The distance to the newest position is exact in 32 unsigned bits.  Slots
+  // that are not there have the smallest key and come after all that are, so
+  // that none of them is among the budget largest.
   uint32_t key[NB][4];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const f32x4 v = HOLD ? w[HOLD ? i : 0] : load_w(i);
-    const i32x4 q = HOLD ? p[HOLD ? i : 0] : load_p(i);
+  for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      key[i][e] = uint32_t(newest) - uint32_t(q[e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(v[e]);
-    if (!HOLD && i % 4 == 3) asm volatile("" ::: "memory");   // four runs' loads at a time
-  }
+    for (int e = 0; e < 4; ++e) {
+      key[i][e] = uint32_t(newest) - uint32_t(p[i][e]) < uint32_t(a.recent) ? 0xffffffffu : rank_of(w[i][e]);
+      if (4096 * (i + 1) > len && slot(i, e) >= len) key[i][e] = 0;
+    }
 
   // Sums of mine[] over the runs before this thread's run i, in slot order.
   const auto before = [&](uint32_t (&mine)[NB], uint32_t* lds, uint32_t (&out)[NB]) {
@@ -306,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
   uint32_t kept[NB];   // a bit a slot
 #pragma unroll
   for (int i = 0; i < NB; ++i) kept[i] = (1u << min(max(len - slot(i, 0), 0), 4)) - 1;
-  if (HOLD && len - stay <= kOneByOne) {
+  if (one_by_one) {
     // few to drop: the smallest key, of equal ones the last slot, one by one
     // (256 pairs of 2049 slots cut by 1 or 4: 6.7 and 8.4 us, 9.1 by digits)
     for (int k = 0; k < len - stay; ++k) {
@@ -340,38 +350,45 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
     // the budget-th largest key, digit by digit, until all that share the
     // digits so far stay
     uint32_t prefix = 0, mask = 0, need = uint32_t(stay);
-    const auto round = [&](auto bins, uint32_t* h, uint32_t* s, int shift) {
-      constexpr int BINS = decltype(bins)::value;
+    const auto round = [&](auto bins, auto copies, uint32_t* h, uint32_t* s, int shift) {
+      constexpr int BINS = decltype(bins)::value, COPIES = decltype(copies)::value;
+      constexpr bool FIRST = COPIES > 1;   // all keys are in
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        if (slot(i, 0) - 4 * tid >= len) continue;
+        if (4096 * i >= len) continue;
         uint32_t digit[4];
         bool in[4];
-        bool one = true;   // all four in, with the digit of the wave's first
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          in[e] = slot(i, e) < len && (key[i][e] & mask) == prefix;
+          in[e] = FIRST || (key[i][e] & mask) == prefix;
           digit[e] = (key[i][e] >> shift) & (BINS - 1);
-          one = one && in[e] && digit[e] == uint32_t(uniform(int(digit[0])));
         }
-        if (__all(one)) {
-          // one addition for a wave whose keys agree (equal weights, new tokens)
-          if (lane == 0) atomicAdd(&h[digit[0]], 256u);
-          continue;
+        const uint32_t first = uint32_t(uniform(int(digit[0])));
+        if (__all(in[0] && digit[0] == first)) {
+          bool one = true;
+#pragma unroll
+          for (int e = 1; e < 4; ++e) one = one && in[e] && digit[e] == first;
+          if (__all(one)) {
+            // one addition for a wave whose keys agree (equal weights, new tokens)
+            if (lane == 0) atomicAdd(&h[first * COPIES], 256u);
+            continue;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (in[e]) atomicAdd(&h[digit[e]], 1u);
+          if (in[e]) atomicAdd(&h[digit[e] * COPIES + lane % COPIES], 1u);
       }
       __syncthreads();
-      const uint32_t d = find_digit<BINS>(h, s, need, lane, wave);
+      const uint32_t d = find_digit<BINS, COPIES>(h, s, need, lane, wave);
       prefix |= d << shift;
       mask |= uint32_t(BINS - 1) << shift;
-      return h[d] == need;
+      return bin<COPIES>(h, int(d)) == need;
     };
-    bool all = round(std::integral_constant<int, kBins[0]>(), hist, sums[0], kShift[0]);
-    if (!all) all = round(std::integral_constant<int, kBins[1]>(), hist + kBins[0], sums[1], kShift[1]);
-    if (!all) all = round(std::integral_constant<int, kBins[2]>(), hist + kBins[0] + kBins[1], sums[2], kShift[2]);
+    constexpr auto one_copy = std::integral_constant<int, 1>();
+    uint32_t* h1 = hist + kCopies * kBins[0];
+    bool all = round(std::integral_constant<int, kBins[0]>(), std::integral_constant<int, kCopies>(), hist, sums[0], kShift[0]);
+    if (!all) all = round(std::integral_constant<int, kBins[1]>(), one_copy, h1, sums[1], kShift[1]);
+    if (!all) all = round(std::integral_constant<int, kBins[2]>(), one_copy, h1 + kBins[1], sums[2], kShift[2]);
 
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -384,14 +401,14 @@ __global__ __launch_bounds__(kThreads) void select_kernel(EvictKernelArgs a) {
       for (int i = 0; i < NB; ++i) {
         n[i] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) n[i] += slot(i, e) < len && key[i][e] == prefix;
+        for (int e = 0; e < 4; ++e) n[i] += key[i][e] == prefix;
       }
       before(n, counts[0], rank);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (slot(i, e) < len && key[i][e] == prefix && rank[i]++ >= need) kept[i] &= ~(1u << e);
+          if (key[i][e] == prefix && rank[i]++ >= need) kept[i] &= ~(1u << e);
     }
   }
   // holes below the new length (low half) and what fills them (high half)

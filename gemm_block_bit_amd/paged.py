@@ -177,30 +177,28 @@ def _with_workspace(kind: str, device: int, stream: int, given, call, need):
     """call(pointer, bytes) -> status with the caller's workspace, or with a
     buffer kept per use, device and stream (zero when it is new; kept apart
     from the buffer of the gemm calls, which has to stay zero).  need() is
-    only asked when a call says that the buffer is too small."""
+    only asked when a call says that the buffer is too small.  A call that is
+    captured in a graph gets a buffer of the graph's own, cleared in every
+    replay: one that is kept would be shared with calls outside the graph."""
     if given is not None:
         if given.get_device() != device:
             raise ValueError(f"workspace is on {given.device}, not on GPU {device}")
         _check(call(given.data_ptr(), given.numel() * given.element_size()))
         return
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.zeros(max(need(), 16), dtype=torch.uint8, device=torch.device("cuda", device))
+        _check(call(buf.data_ptr(), buf.numel()))
+        return
     key = (kind, device, stream)
     buf = _ws_cache.get(key)
     if buf is None:
-        buf = _ws_cache[key] = _new_workspace(1 << 20, device)
+        buf = _ws_cache[key] = torch.zeros(1 << 20, dtype=torch.uint8, device=torch.device("cuda", device))
     st = call(buf.data_ptr(), buf.numel())
     if st == _E_SPACE:
-        buf = _ws_cache[key] = _new_workspace(need(), device)
+        buf = _ws_cache[key] = torch.zeros(need(), dtype=torch.uint8, device=buf.device)
         st = call(buf.data_ptr(), buf.numel())
     _check(st)
-
-
-def _new_workspace(nbytes: int, device: int):
-    """Not during a capture: the buffer would be the graph's memory, and its
-    clearing a part of every replay."""
-    torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("a call that is captured in a graph needs its workspace given")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
 
 
 def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, layout: str = "half", out=None):

@@ -304,17 +304,25 @@ def test_in_a_graph():
 
 
 @pytest.mark.gpu
-def test_a_capture_needs_its_workspace_given(monkeypatch):
-    """A buffer made during a capture would be the graph's."""
-    monkeypatch.setattr(gbb.paged, "_ws_cache", {})
+def test_a_capture_keeps_its_workspace_to_itself(monkeypatch):
+    """Captured without a workspace: replays beside eager calls give the eager
+    bits, and nothing of the graph's memory stays for calls outside it."""
     s = Setup([900, 40], 4, 2, 64, seed=14)
     q, out = s.q.to(dev()), torch.zeros(2, 4, 64, device=dev(), dtype=torch.float16)
+    kept = {}
+    monkeypatch.setattr(gbb.paged, "_ws_cache", kept)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        with pytest.raises(RuntimeError, match="workspace"):
-            gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len, out=out)
-        q.add_(0)
-    s.check(gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len, out=out))
+        gbb.paged_attention(s.cache, q, s.btd, s.lend, s.max_len, out=out)
+    assert not kept
+    for i in range(4):
+        s.q = torch.roll(s.q, 1, 0) * (1 - i / 8)
+        q.copy_(s.q)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        s.check(out)
+        assert torch.equal(s.run(), out)
 
 
 @pytest.mark.gpu
