@@ -63,13 +63,19 @@ def _device_of(t, name) -> int:
     return t.get_device()
 
 
+_get_stream = None
+
+
 def _raw_stream(device: int) -> int:
     """torch's current stream of a GPU as a hipStream_t, by the accessor that
     torch's own generated code uses (the public one builds two Python objects
     for every call, 2 us)."""
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+    global _get_stream
+    if _get_stream is None:
+        torch = _torch()
+        _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _get_stream(device)
 
 
 # ----------------------------------------------------------------------------
@@ -291,12 +297,13 @@ def cache_evict(cache: PagedCache, block_table, lengths, max_len: int, budget: i
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][pages]")
     B, pages = block_table.shape
-    n = lengths_out if lengths_out is not None else torch.empty((B,), dtype=torch.int32, device=cache.device)
+    lp = _ptr(lengths, torch.int32, device, "lengths", (B,))
+    n = lengths_out if lengths_out is not None else torch.empty_like(lengths)
     shape = cache.weights.shape
     w = cache._c.weights if weights_out is None else _ptr(weights_out, torch.float32, device, "weights_out", shape)
     p = cache._c.positions if positions_out is None else _ptr(positions_out, torch.int32, device, "positions_out", shape)
     L, stream = lib(), _raw_stream(device)
-    args = (cache._ref, B, bt, pages, _ptr(lengths, torch.int32, device, "lengths", (B,)), max_len, budget, recent,
+    args = (cache._ref, B, bt, pages, lp, max_len, budget, recent,
             _ptr(n, torch.int32, device, "lengths_out", (B,)), w, p)
     _with_workspace("evict", device, stream, workspace, lambda ws, size: L.gbb_cache_evict(*args, ws, size, stream),
                     lambda: L.gbb_cache_evict_workspace(cache._ref, B, max_len, budget))
