@@ -58,24 +58,28 @@ def _refuse(t, dtype, device, name, shape):
 
 
 def _device_of(t, name) -> int:
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+    try:
+        device = t.get_device()
+    except AttributeError:
+        device = -1
+    if device < 0:
         raise TypeError(f"{name} must be a torch tensor on a GPU")
-    return t.get_device()
+    return device
 
 
-_get_stream = None
+_int32 = _float32 = _raw_stream = _capturing = None
 
 
-def _raw_stream(device: int) -> int:
-    """torch's current stream of a GPU as a hipStream_t, by the accessor that
-    torch's own generated code uses (the public one builds two Python objects
-    for every call, 2 us)."""
-    global _get_stream
-    if _get_stream is None:
-        torch = _torch()
-        _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return _get_stream(device)
+def _resolve() -> None:
+    """What every call needs of torch, looked up once.  The stream as a
+    hipStream_t is taken by the accessor that torch's own generated code uses
+    (the public one builds two Python objects for every call, 2 us)."""
+    global _int32, _float32, _raw_stream, _capturing
+    torch = _torch()
+    _float32, _capturing = torch.float32, torch.cuda.is_current_stream_capturing
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _int32 = torch.int32
 
 
 # ----------------------------------------------------------------------------
@@ -94,7 +98,7 @@ def rope_table(rot: int, n_pos: int, base: float = 10000.0, scaling: str = "plai
 
 
 def _table(table, device):
-    p = _ptr(table, _torch().float32, device, "table")
+    p = _ptr(table, _float32, device, "table")
     shape = table.shape
     if len(shape) != 3 or shape[2] != 2:
         raise ValueError("table must be float32 [n_pos][rot/2][2]")
@@ -107,13 +111,15 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
     positions [T].  out: where to write (x itself for in place), else a new
     contiguous tensor.  transpose: the transposed rotation, which is the
     gradient with respect to x."""
-    torch = _torch()
+    if _int32 is None:
+        _resolve()
     device = _device_of(x, "x")
-    if x.dim() != 3 or x.stride(2) != 1:
+    shape, xs = x.shape, x.stride()
+    if len(shape) != 3 or xs[2] != 1:
         raise ValueError("x must be [T][H][D] with contiguous heads")
-    T, H, D = x.shape
+    T, H, D = shape
     if out is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = x.new_empty(T, H, D)
     else:
         y = out
         if y.dtype != x.dtype or y.shape != x.shape or y.stride(2) != 1:
@@ -121,9 +127,9 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
         if y.get_device() != device:
             raise ValueError(f"out is on {y.device}, not on {x.device}")
     tp, n_pos, rot = _table(table, device)
-    xs, ys = x.stride(), y.stride()
+    ys = y.stride()
     _check(lib().gbb_rope(x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H, D,
-                          _ptr(positions, torch.int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout),
+                          _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout),
                           int(transpose), _raw_stream(device)))
     return y
 
@@ -139,7 +145,7 @@ class PagedCache:
     must keep their storage."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, weights=None, positions=None):
-        torch = _torch()
+        _resolve()
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [pages][kv heads][page][head size] of one dtype")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -156,8 +162,8 @@ class PagedCache:
 
         one, slots = (self.kv_heads,), tuple(k.shape[:3])
         self._c = _PagedCache(ptr(k, k.dtype, "k", None), ptr(v, v.dtype, "v", None),
-                              ptr(k_scale, torch.float32, "k_scale", one), ptr(v_scale, torch.float32, "v_scale", one),
-                              ptr(weights, torch.float32, "weights", slots), ptr(positions, torch.int32, "positions", slots),
+                              ptr(k_scale, _float32, "k_scale", one), ptr(v_scale, _float32, "v_scale", one),
+                              ptr(weights, _float32, "weights", slots), ptr(positions, _int32, "positions", slots),
                               code, self.num_pages, self.page, self.kv_heads, self.head_dim)
         self._ref = ctypes.byref(self._c)
 
@@ -179,47 +185,52 @@ _ws_cache: dict = {}
 _E_SPACE = -5
 
 
-def _with_workspace(kind: str, device: int, stream: int, given, call, need):
-    """call(pointer, bytes) -> status with the caller's workspace, or with a
-    buffer kept per use, device and stream (zero when it is new; kept apart
-    from the buffer of the gemm calls, which has to stay zero).  need() is
-    only asked when a call says that the buffer is too small.  A call that is
-    captured in a graph gets a buffer of the graph's own, cleared in every
+def _with_workspace(kind: str, device: int, given, call, args, need):
+    """call(*args, workspace, bytes, stream) with the caller's workspace, or
+    with a buffer kept per use, device and stream (zero when it is new; kept
+    apart from the buffer of the gemm calls, which has to stay zero).  need()
+    is only asked when a call says that the buffer is too small.  A call that
+    is captured in a graph gets a buffer of the graph's own, cleared in every
     replay: one that is kept would be shared with calls outside the graph."""
+    stream = _raw_stream(device)
     if given is not None:
         if given.get_device() != device:
             raise ValueError(f"workspace is on {given.device}, not on GPU {device}")
-        _check(call(given.data_ptr(), given.numel() * given.element_size()))
+        _check(call(*args, given.data_ptr(), given.numel() * given.element_size(), stream))
         return
-    torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
-        buf = torch.zeros(max(need(), 16), dtype=torch.uint8, device=torch.device("cuda", device))
-        _check(call(buf.data_ptr(), buf.numel()))
+    if _capturing():
+        buf = _zeros(max(need(), 16), device)
+        _check(call(*args, buf.data_ptr(), buf.numel(), stream))
         return
     key = (kind, device, stream)
     buf = _ws_cache.get(key)
     if buf is None:
-        buf = _ws_cache[key] = torch.zeros(1 << 20, dtype=torch.uint8, device=torch.device("cuda", device))
-    st = call(buf.data_ptr(), buf.numel())
+        buf = _ws_cache[key] = _zeros(1 << 20, device)
+    st = call(*args, buf.data_ptr(), buf.numel(), stream)
     if st == _E_SPACE:
-        buf = _ws_cache[key] = torch.zeros(need(), dtype=torch.uint8, device=buf.device)
-        st = call(buf.data_ptr(), buf.numel())
+        buf = _ws_cache[key] = _zeros(need(), device)
+        st = call(*args, buf.data_ptr(), buf.numel(), stream)
     _check(st)
+
+
+def _zeros(nbytes: int, device: int):
+    torch = _torch()
+    return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
 
 
 def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, layout: str = "half", out=None):
     """Rotates the q and k heads of qkv [T][(q_heads + 2 kv heads) head size]
     (rows may be strided), writes k and v to the cache's int32 slots [T] and
     returns q [T][q_heads][head size] (see gbb_rope_append)."""
-    torch = _torch()
     device = cache._index
     if _device_of(qkv, "qkv") != device:
         raise ValueError(f"qkv is on {qkv.device}, not on GPU {device}")
     D = cache.head_dim
     width = (q_heads + 2 * cache.kv_heads) * D
-    if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
+    shape, stride = qkv.shape, qkv.stride()
+    if len(shape) != 2 or shape[1] != width or stride[1] != 1:
         raise ValueError(f"qkv must be [T][{width}] with contiguous rows")
-    T = qkv.shape[0]
+    T = shape[0]
     if out is None:
         q = qkv.new_empty(T, q_heads, D)
         qp = q.data_ptr()
@@ -228,8 +239,8 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
         qp = _ptr(q, qkv.dtype, device, "out", (T, q_heads, D))
     tp, n_pos, rot = _table(table, device)
     _check(lib().gbb_rope_append(
-        cache._ref, qkv.data_ptr(), qkv.stride(0) if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
-        _ptr(positions, torch.int32, device, "positions", (T,)), _ptr(slots, torch.int32, device, "slots", (T,)), tp,
+        cache._ref, qkv.data_ptr(), stride[0] if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
+        _ptr(positions, _int32, device, "positions", (T,)), _ptr(slots, _int32, device, "slots", (T,)), tp,
         n_pos, rot, _layout(layout), qp, _raw_stream(device)))
     return q
 
@@ -247,35 +258,32 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     float32 [B][q_heads] to fill.  weights_out: where to write the cache's
     weights with this step's added (cache.weights itself for in place).
     Returns [B][q_heads][head size] (see gbb_paged_attention)."""
-    torch = _torch()
     device, D = cache._index, cache.head_dim
     if _device_of(q, "q") != device:
         raise ValueError(f"q is on {q.device}, not on GPU {device}")
-    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or (q.stride(1) != D and q.shape[1] != 1):
+    shape, stride = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != D or stride[2] != 1 or (stride[1] != D and shape[1] != 1):
         raise ValueError(f"q must be [B][q_heads][{D}] with contiguous tokens")
-    shape = q.shape
-    B, q_heads = shape[0], shape[1]
+    B, q_heads, _ = shape
     if out is None:
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        o = q.new_empty(B, q_heads, D)
         op = o.data_ptr()
     else:
         o = out
         op = _ptr(o, q.dtype, device, "out", shape)
-    bt = _ptr(block_table, torch.int32, device, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    bt, table_shape = _ptr(block_table, _int32, device, "block_table"), block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}][pages]")
     w = None
     if weights_out is not None:
         if cache.weights is None:
             raise ValueError("the cache has no weights")
-        w = _ptr(weights_out, torch.float32, device, "weights_out", cache.weights.shape)
-    L, stream = lib(), _raw_stream(device)
-    args = (cache._ref, q.data_ptr(), q.stride(0), _dtype_code(q.dtype), B, q_heads, bt, block_table.shape[1],
-            _ptr(lengths, torch.int32, device, "lengths", (B,)), max_len, D ** -0.5 if scale is None else scale,
-            op, _ptr(lse, torch.float32, device, "lse", (B, q_heads)) if lse is not None else None, w)
-    _with_workspace("attention", device, stream, workspace,
-                    lambda ws, n: L.gbb_paged_attention(*args, ws, n, stream),
-                    lambda: L.gbb_paged_attention_workspace(cache._ref, B, q_heads, max_len, int(w is not None)))
+        w = _ptr(weights_out, _float32, device, "weights_out", cache.weights.shape)
+    args = (cache._ref, q.data_ptr(), stride[0], _dtype_code(q.dtype), B, q_heads, bt, table_shape[1],
+            _ptr(lengths, _int32, device, "lengths", (B,)), max_len, D ** -0.5 if scale is None else scale,
+            op, _ptr(lse, _float32, device, "lse", (B, q_heads)) if lse is not None else None, w)
+    _with_workspace("attention", device, workspace, lib().gbb_paged_attention, args,
+                    lambda: paged_attention_workspace(cache, B, q_heads, max_len, w is not None))
     return o
 
 
@@ -289,22 +297,20 @@ def cache_evict(cache: PagedCache, block_table, lengths, max_len: int, budget: i
     the `recent` newest positions and the slots of the largest weight (see
     gbb_cache_evict).  weights_out, positions_out: default in place.  Returns
     the new lengths, int32 [B] (lengths_out if given)."""
-    torch = _torch()
     if cache.weights is None or cache.positions is None:
         raise ValueError("eviction needs a cache with weights and positions")
     device = cache._index
-    bt = _ptr(block_table, torch.int32, device, "block_table")
+    bt = _ptr(block_table, _int32, device, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][pages]")
     B, pages = block_table.shape
-    lp = _ptr(lengths, torch.int32, device, "lengths", (B,))
-    n = lengths_out if lengths_out is not None else torch.empty_like(lengths)
+    lp = _ptr(lengths, _int32, device, "lengths", (B,))
+    n = lengths_out if lengths_out is not None else lengths.new_empty(B)
     shape = cache.weights.shape
-    w = cache._c.weights if weights_out is None else _ptr(weights_out, torch.float32, device, "weights_out", shape)
-    p = cache._c.positions if positions_out is None else _ptr(positions_out, torch.int32, device, "positions_out", shape)
-    L, stream = lib(), _raw_stream(device)
+    w = cache._c.weights if weights_out is None else _ptr(weights_out, _float32, device, "weights_out", shape)
+    p = cache._c.positions if positions_out is None else _ptr(positions_out, _int32, device, "positions_out", shape)
     args = (cache._ref, B, bt, pages, lp, max_len, budget, recent,
-            _ptr(n, torch.int32, device, "lengths_out", (B,)), w, p)
-    _with_workspace("evict", device, stream, workspace, lambda ws, size: L.gbb_cache_evict(*args, ws, size, stream),
-                    lambda: L.gbb_cache_evict_workspace(cache._ref, B, max_len, budget))
+            _ptr(n, _int32, device, "lengths_out", (B,)), w, p)
+    _with_workspace("evict", device, workspace, lib().gbb_cache_evict, args,
+                    lambda: cache_evict_workspace(cache, B, max_len, budget))
     return n
