@@ -205,6 +205,9 @@ extern "C" gbb_status gbb_paged_attention(const gbb_paged_cache* cache, const vo
     return fail(GBB_E_ALIGN, "q and out must be 16-byte aligned and q_token a multiple of 8");
   if (!aligned(lse, 4) || !aligned(weights_out, 4)) return fail(GBB_E_ALIGN, "lse or weights_out is misaligned");
   if (weights_out && !cache->weights) return fail(GBB_E_ARG, "weights_out needs a cache with weights");
+  const size_t n = size_t(cache->num_pages) * cache->kv_heads * cache->page * 4;
+  if (weights_out && weights_out != cache->weights && overlap(weights_out, n, cache->weights, n))
+    return fail(GBB_E_ARG, "weights_out overlaps the cache's weights in part");
   if (overlap(q, (size_t(B - 1) * q_token + row) * 2, out, size_t(B) * row * 2)) return fail(GBB_E_ARG, "q and out overlap");
   if ((st = check_workspace(workspace, ws_bytes, p.ws_bytes)) != GBB_OK) return st;
   const AttendArgs a = {q, q_token, block_table, lengths, out, lse, weights_out, static_cast<char*>(workspace), B,

@@ -510,7 +510,8 @@ gbb_status gbb_rope_append(const gbb_paged_cache* cache, const void* qkv, int64_
 /* Bytes of workspace of gbb_paged_attention (0 on a bad argument or where
  * none is needed).  It must be zero before its first use; every call leaves
  * it ready for the next one of any size, but not zero: it must not be shared
- * with calls that want a zero workspace (gbb_gemm_*). */
+ * with calls that want a zero workspace (gbb_gemm_*), with gbb_cache_evict,
+ * which leaves it in any state, or with a call that may run at the same time. */
 size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_heads, int max_len, int with_weights);
 
 /* Attention of one new token per sequence over the cache:
@@ -535,7 +536,7 @@ size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_
  *              for an empty sequence: what joining the outputs over parts of
  *              a context takes.
  *   weights_out NULL, or like the cache's weights (which must be there, and
- *              may be the same memory): for every slot j < lengths[b] the
+ *              may be the same memory, but not overlap it in part): for every slot j < lengths[b] the
  *              cache's weight plus the sum of p_j over the kv head's query
  *              heads.  Other slots are not written.  No atomics: results do
  *              not depend on the order of execution.  Two sequences of a
@@ -549,7 +550,8 @@ gbb_status gbb_paged_attention(const gbb_paged_cache* cache, const void* q, int6
                                void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace of gbb_cache_evict (0 on a bad argument).  Its contents
- * need no initialisation. */
+ * need no initialisation.  Calls that may run at the same time need separate
+ * workspaces. */
 size_t gbb_cache_evict_workspace(const gbb_paged_cache* cache, int B, int max_len, int budget);
 
 /* Eviction by accumulated attention weight.  For every sequence b and kv

@@ -388,3 +388,13 @@ def test_argument_refusals():
     assert L.gbb_paged_attention_workspace(None, 2, 4, 64, 0) == 0
     small, big = (L.gbb_paged_attention_workspace(ctypes.byref(cc), 2, 4, 10000, w) for w in (0, 1))
     assert 0 < small < big
+
+
+def test_weights_out_that_overlaps_in_part_is_refused():
+    L, C = gbb.lib(), gbb.binding._PagedCache
+    w = 3 << 20   # never read; 4 pages of 2 kv heads of 16 slots: 512 bytes
+    c = C(k=1 << 20, v=2 << 20, k_scale=None, v_scale=None, weights=w, positions=None, dtype=0, num_pages=4, page=16,
+          kv_heads=2, head_dim=64)
+    for at in (w + 4, w + 508, w - 508):
+        assert L.gbb_paged_attention(ctypes.byref(c), 8 << 20, 256, 0, 2, 4, 9 << 20, 4, 10 << 20, 64, 1.0, 11 << 20,
+                                     None, at, 1 << 24, 1 << 30, None) == -1
