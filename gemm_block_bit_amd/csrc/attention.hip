@@ -698,8 +698,8 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
 template <int DT, int CT, int D, bool WT>
 void run_split(const SplitArgs& a, bool wide, hipStream_t s) {
   const unsigned grid = unsigned(a.B) * a.Hkv * a.qtiles * a.nsplit;
-  if (wide) hipLaunchKernelGGL((split_kernel<DT, CT, D, WT, true>), dim3(grid), dim3(64 * waves(true)), 0, s, a);
-  else hipLaunchKernelGGL((split_kernel<DT, CT, D, WT, false>), dim3(grid), dim3(256), 0, s, a);
+  if (wide) start((split_kernel<DT, CT, D, WT, true>), dim3(grid), dim3(64 * waves(true)), s, a);
+  else start((split_kernel<DT, CT, D, WT, false>), dim3(grid), dim3(256), s, a);
 }
 
 template <int DT, int CT, int D>
@@ -711,9 +711,9 @@ void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
   constexpr bool F8 = CT == GBB_E4M3;
   if (wt) {
     const unsigned more = unsigned(a.B) * a.Hkv * unsigned((a.max_len + kJoinSlots - 1) / kJoinSlots);
-    hipLaunchKernelGGL((join_kernel<DT, F8, D, true>), dim3(unsigned(heads) + more), dim3(256), 0, s, a, heads);
+    start((join_kernel<DT, F8, D, true>), dim3(unsigned(heads) + more), dim3(256), s, a, heads);
   } else if (heads) {
-    hipLaunchKernelGGL((join_kernel<DT, F8, D, false>), dim3(unsigned(heads)), dim3(256), 0, s, a, heads);
+    start((join_kernel<DT, F8, D, false>), dim3(unsigned(heads)), dim3(256), s, a, heads);
   }
 }
 template <int DT, int CT>

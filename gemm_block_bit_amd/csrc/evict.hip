@@ -739,10 +739,10 @@ template <int NB>
 void run_select(const EvictKernelArgs& a, unsigned pairs, bool finish, hipStream_t s) {
   if constexpr (NB <= 4)
     if (finish) {
-      hipLaunchKernelGGL((select_kernel<NB, true>), dim3(pairs), dim3(kThreads), 0, s, a);
+      start((select_kernel<NB, true>), dim3(pairs), dim3(kThreads), s, a);
       return;
     }
-  hipLaunchKernelGGL((select_kernel<NB, false>), dim3(pairs), dim3(kThreads), 0, s, a);
+  start((select_kernel<NB, false>), dim3(pairs), dim3(kThreads), s, a);
 }
 
 }  // namespace
@@ -810,11 +810,11 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
     g.segments = p.segments;
     g.pairs = int(pairs);
     const dim3 grid(static_cast<unsigned>(segs)), block(kThreads);
-    hipLaunchKernelGGL(spread_newest_kernel, grid, block, 0, s, a, g);
-    hipLaunchKernelGGL((spread_hist_kernel<0>), grid, block, 0, s, a, g);
-    hipLaunchKernelGGL((spread_hist_kernel<1>), grid, block, 0, s, a, g);
-    hipLaunchKernelGGL((spread_hist_kernel<2>), grid, block, 0, s, a, g);
-    hipLaunchKernelGGL(spread_place_kernel, grid, block, 0, s, a, g);
+    start(spread_newest_kernel, grid, block, s, a, g);
+    start((spread_hist_kernel<0>), grid, block, s, a, g);
+    start((spread_hist_kernel<1>), grid, block, s, a, g);
+    start((spread_hist_kernel<2>), grid, block, s, a, g);
+    start(spread_place_kernel, grid, block, s, a, g);
   } else if (x.max_len <= 4096) {
     run_select<1>(a, pairs, finish, s);
   } else if (x.max_len <= 8192) {
@@ -828,7 +828,7 @@ int launch_evict(const gbb_paged_cache& c, const EvictArgs& x, const EvictPlan& 
     const size_t per = 256 >> a.lshift;
     const size_t most = std::max((p.most + per - 1) / per, (size_t(x.max_len) + 255) / 256);
     const unsigned gy = unsigned(std::min<size_t>(most, std::max(1u, 4096u / pairs)));
-    hipLaunchKernelGGL(move_kernel, dim3(pairs, gy), dim3(256), 0, s, a);
+    start(move_kernel, dim3(pairs, gy), dim3(256), s, a);
   }
   return int(hipGetLastError());
 }

@@ -250,9 +250,9 @@ void run_rope(const RopeArgs& a, hipStream_t s) {
   const Units n = units(a.D, a.rot, a.layout, E, EC);
   const Shape g = shape(a.T, a.H, n.pairs + n.copies);
   if (a.layout == GBB_ROPE_HALF)
-    hipLaunchKernelGGL((rope_kernel<DT, E, EC, true>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
+    start((rope_kernel<DT, E, EC, true>), g.grid, dim3(g.threads), s, a, n, g.hp, g.tp);
   else if constexpr (E > 1)
-    hipLaunchKernelGGL((rope_kernel<DT, E, EC, false>), g.grid, dim3(g.threads), 0, s, a, n, g.hp, g.tp);
+    start((rope_kernel<DT, E, EC, false>), g.grid, dim3(g.threads), s, a, n, g.hp, g.tp);
 }
 template <int DT>
 void run_widths(const RopeArgs& a, int E, int EC, hipStream_t s) {
@@ -272,13 +272,13 @@ void run_append(const gbb_paged_cache& c, const AppendArgs& a, hipStream_t s) {
   const Units n = units(c.head_dim, a.rot, a.layout, E, E);
   const Shape g = shape(a.T, a.Hq + 2 * c.kv_heads, n.pairs + n.copies);
   if (wide && half)
-    hipLaunchKernelGGL((append_kernel<DT, CT, 8, true>), g.grid, dim3(g.threads), 0, s, a, c, n, g.hp, g.tp);
+    start((append_kernel<DT, CT, 8, true>), g.grid, dim3(g.threads), s, a, c, n, g.hp, g.tp);
   else if (wide)
-    hipLaunchKernelGGL((append_kernel<DT, CT, 8, false>), g.grid, dim3(g.threads), 0, s, a, c, n, g.hp, g.tp);
+    start((append_kernel<DT, CT, 8, false>), g.grid, dim3(g.threads), s, a, c, n, g.hp, g.tp);
   else if (half)
-    hipLaunchKernelGGL((append_kernel<DT, CT, 1, true>), g.grid, dim3(g.threads), 0, s, a, c, n, g.hp, g.tp);
+    start((append_kernel<DT, CT, 1, true>), g.grid, dim3(g.threads), s, a, c, n, g.hp, g.tp);
   else
-    hipLaunchKernelGGL((append_kernel<DT, CT, 2, false>), g.grid, dim3(g.threads), 0, s, a, c, n, g.hp, g.tp);
+    start((append_kernel<DT, CT, 2, false>), g.grid, dim3(g.threads), s, a, c, n, g.hp, g.tp);
 }
 
 }  // namespace
