@@ -43,7 +43,7 @@
 // over the kv head's query heads, one thread a slot, without atomics.
 //
 // Measured: 32 sequences of up to 8192 slots (64 / 8 heads of 128, bf16,
-// 523 MB) 103 us, 5.1 TB/s; 2 of 131072 (32 / 8, e4m3, 537 MB) 98 us, 5.5
+// 523 MB) 104 us, 5.0 TB/s; 2 of 131072 (32 / 8, e4m3, 537 MB) 99 us, 5.4
 // TB/s; a plain read kernel reaches 5.2 to 5.5 TB/s here.  1 of 1000 slots (32
 // / 8, fp16) 7 us, a chain of dependent steps: launch, page, K and V, scores,
 // the joins in the workgroup and over the runs.
@@ -732,27 +732,40 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   const int G = Hq / c.kv_heads;
   p.qtiles = (G + 15) / 16;
   const int64_t pairs = int64_t(B) * c.kv_heads * p.qtiles;
-  // Runs.  Short contexts, and those of calls whose (sequence, kv head) pairs
-  // fill the chip, stay whole: a run costs about 1.5 us of a CU beside its
-  // bytes and its partial results have to be joined (256 pairs of 4000 slots:
-  // 93 us whole, 97 and 100 in runs of 2048 and 1024).  Else the longest run
-  // that gives every CU a workgroup (8 pairs of 32768 slots: 31 us in runs of
-  // 1024, 48 in 4096, 36 in 512).  It has at most 2048 slots, so that ragged
-  // lengths balance (32 ragged of up to 8192: 105 us, 114 in 4096), but above
-  // 16384 there are runs enough for that in 4096 (2 of 131072: 102 us, 105 in
-  // 2048); and below 1024 at most 16 runs are made (4 pairs of 16 query heads
-  // and 8192 slots: 14 us in 512, 22 in 128).
+  // Runs.  A run costs about 1.5 us of a CU beside its bytes and its partial
+  // results have to be joined, and few CUs read faster each.  So contexts stay
+  // whole where they are short and where the (sequence, kv head) pairs alone
+  // keep the chip busy: one for every CU up to 4096 slots (256 pairs of 4000: 93
+  // us whole, 97 and 100 in runs of 2048 and 1024), three for five CUs up to
+  // 2048 of up to 128 elements (160 pairs of 2000: 32 us, 41 in 1024; of up to
+  // 2000: 21, 18.5 in 1024), three for eight up to 1024 (96 of 1000: 12 and
+  // 13.5 in 256; of up to 1000: 11 and 12).
+  // Else the longest run that makes three for five CUs (24 pairs of 8000: 20 us
+  // in 192 runs of 1024, 24 in 512; 8 of 60000: 48 in 240 of 2048, 53 in 1024;
+  // 8 of 32768: 31 in 256 of 1024, 33 in 128 of 2048, 48 in 64 of 4096).  It
+  // has at most 2048 slots, and those one for every CU, so that ragged lengths
+  // balance (32 ragged of up to 8192: 105 us, 114 in 4096; 80 pairs of up to
+  // 5000: 21 in 1024, 25 in 240 of 2048), but above 16384 there are runs enough
+  // for that (2 of 131072: 99 us in 4096, 102 in 2048; 9 ragged pairs of up to
+  // 107545: 34 to 38 and 40); and below 1024 at most 16 runs are made (4 pairs
+  // of 16 query heads and 8192 slots: 14 us in 512, 22 in 128).
   // Eight waves a workgroup where it has work for them (1152 ragged pairs of
   // up to 2047 slots: 63 against 69 us), four for short runs (2048 pairs of
   // 256: 51 against 58 us).
   const int64_t cus = device_compute_units();
   int chunk = kMaxChunk;
-  if (max_len <= 512 || (pairs >= cus && max_len <= kMaxChunk)) {
+  if (max_len <= 512 || (pairs >= cus && max_len <= kMaxChunk) || (8 * pairs >= 3 * cus && max_len <= 1024) ||
+      (5 * pairs >= 3 * cus && max_len <= 2048 && c.head_dim < 256)) {
     p.wide = pairs < cus || max_len >= 1024;
   } else {
-    if (max_len <= 16384) chunk = 2048;
+    const bool ragged = max_len <= 16384;   // runs are few for a sequence
+    if (ragged) chunk = 2048;
     const int least = max_len <= 128 * 16 ? 128 : max_len <= 256 * 16 ? 256 : max_len <= 512 * 16 ? 512 : 1024;
-    while (chunk > least && pairs * ((max_len + chunk - 1) / chunk) < cus) chunk /= 2;
+    const auto enough = [&] {
+      const int64_t runs = pairs * ((max_len + chunk - 1) / chunk);
+      return ragged && chunk == 2048 ? runs >= cus : 5 * runs >= 3 * cus;
+    };
+    while (chunk > least && !enough()) chunk /= 2;
     p.wide = chunk >= 512;
   }
   p.chunk = chunk;
