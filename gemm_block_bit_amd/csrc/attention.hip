@@ -28,8 +28,10 @@
 // while the next scores are; every wait counts the loads behind it.
 //
 // P is rounded to 16 bits for the matrix cores; what the rounding drops is
-// multiplied too, as a second operand, so a product carries about 22 (fp16)
-// or 16 (bf16) bits of P and the output's own rounding is what is left.
+// multiplied too, as further operands: one for fp16, which then carries 22
+// bits of P (its exponential's argument is good to 21), two for bf16, which
+// carries all 24 (17 with one: a value that the others nearly cancel loses
+// its digits).  So the output's own rounding is what is left.
 // exp2 is taken 14 powers above the running maximum's 0, so that fp16 keeps
 // small probabilities out of its subnormals; the sums carry the same factor.
 // e4m3 elements widen to 16 bits exactly; their scales go into the scores'
@@ -70,6 +72,7 @@ constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles 
 // 16-bit element types of q, P and out.
 template <int DT> struct Half;
 template <> struct Half<GBB_F16> {
+  static constexpr int PARTS = 2;   // operands that P is given in
   typedef _Float16 T;
   typedef half8 V8;
   static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
@@ -81,6 +84,7 @@ template <> struct Half<GBB_F16> {
   }
 };
 template <> struct Half<GBB_BF16> {
+  static constexpr int PARTS = 3;
   typedef __bf16 T;
   typedef bf16x8 V8;
   static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
@@ -404,20 +408,23 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       for (int j = 0; j < NT; ++j) o[j] *= f;
     }
     const float ref = m == -INFINITY ? 0.f : m - kShift;
-    V8 ph, pl;
+    V8 part[H::PARTS];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float p = __builtin_amdgcn_exp2f(s[e][r] - ref);
+        float p = __builtin_amdgcn_exp2f(s[e][r] - ref);
         l += p;
-        const typename H::T h = typename H::T(p);
-        ph[4 * e + r] = h;
-        pl[4 * e + r] = typename H::T(p - float(h));
+#pragma unroll
+        for (int i = 0; i < H::PARTS; ++i) {
+          const typename H::T h = typename H::T(p);
+          part[i][4 * e + r] = h;
+          p -= float(h);   // exact
+        }
       }
     auto product = [&](int tile, const u32x4& x) {
-      o[tile] = H::mfma(__builtin_bit_cast(V8, x), ph, o[tile]);
-      o[tile] = H::mfma(__builtin_bit_cast(V8, x), pl, o[tile]);
+#pragma unroll
+      for (int i = 0; i < H::PARTS; ++i) o[tile] = H::mfma(__builtin_bit_cast(V8, x), part[i], o[tile]);
     };
 #pragma unroll
     for (int u = 0; u < NV; ++u)
