@@ -255,6 +255,22 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+class _Kept:
+    """A device buffer that is kept for one (device, stream), and the lock
+    under which its calls are enqueued.  A call may take several launches that
+    meet in the buffer; the library is called without Python's own lock, so
+    another thread's launches could come between them on the same stream."""
+    __slots__ = ("lock", "buf")
+
+    def __init__(self):
+        self.lock, self.buf = threading.Lock(), None
+
+
+def _kept(cache: dict, key) -> _Kept:
+    k = cache.get(key)
+    return cache.setdefault(key, _Kept()) if k is None else k
+
+
 _ws_cache: dict = {}
 
 
@@ -262,18 +278,22 @@ def gemm_mixed_w_workspace(N: int, K: int, M: int) -> int:
     return lib().gbb_gemm_mixed_w_workspace(N, K, M)
 
 
-def _workspace(device, nbytes: int):
-    """A zero-initialised device buffer per (device, stream) reused across
-    calls; the library leaves its counters zero after every call."""
+def _with_workspace(device, given, nbytes: int, call) -> None:
+    """call(pointer, bytes) with the caller's workspace, or where nbytes of
+    one are needed with a zero-initialised device buffer per (device, stream)
+    reused across calls; the library leaves its counters zero after every
+    call."""
     torch = _torch()
-    if nbytes == 0:
-        return None
-    key = (device, torch.cuda.current_stream(device).cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
+    if given is not None:
+        _check(call(given.data_ptr(), given.numel()))
+    elif nbytes == 0:
+        _check(call(None, 0))
+    else:
+        kept = _kept(_ws_cache, (device, torch.cuda.current_stream(device).cuda_stream))
+        with kept.lock:
+            if kept.buf is None or kept.buf.numel() < nbytes:
+                kept.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            _check(call(kept.buf.data_ptr(), kept.buf.numel()))
 
 
 def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=None):
@@ -283,12 +303,10 @@ def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=N
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = lib().gbb_gemm_mixed_w_path_workspace(N, K, M, path)   # 0 when the call needs none
-    ws = workspace if workspace is not None else _workspace(x.device, need)
-    _check(lib().gbb_gemm_mixed_w_path(
-        _dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
-        _dev_ptr(y, torch.float16, "y"), M,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-        path, _stream(x)))
+    args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
+            _dev_ptr(y, torch.float16, "y"), M)
+    _with_workspace(x.device, workspace, need,
+                    lambda ws, n: lib().gbb_gemm_mixed_w_path(*args, ws, n, path, _stream(x)))
     return y
 
 
@@ -433,11 +451,10 @@ def gemm_mixed_w_64x64_path(image, N: int, K: int, x, path: int, out=None, works
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
     need = lib().gbb_gemm_mixed_w_64x64_path_workspace(N, K, M, path)
-    ws = workspace if workspace is not None else _workspace(x.device, need)
-    _check(lib().gbb_gemm_mixed_w_64x64_path(
-        _dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
-        _dev_ptr(y, torch.float16, "y"), M, ws.data_ptr() if ws is not None else None,
-        ws.numel() if ws is not None else 0, path, _stream(x)))
+    args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
+            _dev_ptr(y, torch.float16, "y"), M)
+    _with_workspace(x.device, workspace, need,
+                    lambda ws, n: lib().gbb_gemm_mixed_w_64x64_path(*args, ws, n, path, _stream(x)))
     return y
 
 
@@ -476,9 +493,8 @@ def gemm_w48a8(image, N: int, K: int, n8: int, xq, xs, ga: int | None = None, ou
     if not split:
         _check(lib().gbb_gemm_w48a8(*args, _stream(xq)))
         return y
-    ws = workspace if workspace is not None else _workspace(xq.device, gemm_w48a8_workspace(N, K, n8, M, ga))
-    _check(lib().gbb_gemm_w48a8_split(*args, ws.data_ptr() if ws is not None else None,
-                                      ws.numel() if ws is not None else 0, _stream(xq)))
+    need = 0 if workspace is not None else gemm_w48a8_workspace(N, K, n8, M, ga)
+    _with_workspace(xq.device, workspace, need, lambda ws, n: lib().gbb_gemm_w48a8_split(*args, ws, n, _stream(xq)))
     return y
 
 

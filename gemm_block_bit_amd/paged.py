@@ -17,7 +17,7 @@ import ctypes
 
 import numpy as np
 
-from .binding import _check, _dev_ptr, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
+from .binding import _check, _dev_ptr, _kept, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
@@ -188,8 +188,9 @@ _E_SPACE = -5
 def _with_workspace(kind: str, device: int, given, call, args, need):
     """call(*args, workspace, bytes, stream) with the caller's workspace, or
     with a buffer kept per use, device and stream (zero when it is new; kept
-    apart from the buffer of the gemm calls, which has to stay zero).  need()
-    is only asked when a call says that the buffer is too small.  A call that
+    apart from the buffer of the gemm calls, which has to stay zero), one call
+    at a time.  need() is only asked when a call says that the buffer is too
+    small.  A call that
     is captured in a graph gets a buffer of the graph's own, cleared in every
     replay: one that is kept would be shared with calls outside the graph."""
     stream = _raw_stream(device)
@@ -202,15 +203,15 @@ def _with_workspace(kind: str, device: int, given, call, args, need):
         buf = _zeros(max(need(), 16), device)
         _check(call(*args, buf.data_ptr(), buf.numel(), stream))
         return
-    key = (kind, device, stream)
-    buf = _ws_cache.get(key)
-    if buf is None:
-        buf = _ws_cache[key] = _zeros(1 << 20, device)
-    st = call(*args, buf.data_ptr(), buf.numel(), stream)
-    if st == _E_SPACE:
-        buf = _ws_cache[key] = _zeros(need(), device)
-        st = call(*args, buf.data_ptr(), buf.numel(), stream)
-    _check(st)
+    kept = _kept(_ws_cache, (kind, device, stream))
+    with kept.lock:
+        if kept.buf is None:
+            kept.buf = _zeros(1 << 20, device)
+        st = call(*args, kept.buf.data_ptr(), kept.buf.numel(), stream)
+        if st == _E_SPACE:
+            kept.buf = _zeros(need(), device)
+            st = call(*args, kept.buf.data_ptr(), kept.buf.numel(), stream)
+        _check(st)
 
 
 def _zeros(nbytes: int, device: int):
