@@ -278,14 +278,25 @@ def gemm_mixed_w_workspace(N: int, K: int, M: int) -> int:
     return lib().gbb_gemm_mixed_w_workspace(N, K, M)
 
 
-def _with_workspace(device, given, nbytes: int, call) -> None:
-    """call(pointer, bytes) with the caller's workspace, or where nbytes of
-    one are needed with a zero-initialised device buffer per (device, stream)
-    reused across calls; the library leaves its counters zero after every
+def _given(ws, device: int):
+    """Address and bytes of a caller's workspace on GPU `device`: all of its
+    bytes are the library's, so it may not be a view with gaps."""
+    if ws.get_device() != device:
+        raise ValueError(f"workspace is on {ws.device}, not on GPU {device}")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _with_workspace(x, given, nbytes: int, call) -> None:
+    """call(pointer, bytes) with the caller's workspace on x's device, or where
+    nbytes of one are needed with a zero-initialised device buffer per (device,
+    stream) reused across calls; the library leaves its counters zero after every
     call."""
     torch = _torch()
+    device = x.device
     if given is not None:
-        _check(call(given.data_ptr(), given.numel()))
+        _check(call(*_given(given, x.get_device())))
     elif nbytes == 0:
         _check(call(None, 0))
     else:
@@ -305,7 +316,7 @@ def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=N
     need = lib().gbb_gemm_mixed_w_path_workspace(N, K, M, path)   # 0 when the call needs none
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
-    _with_workspace(x.device, workspace, need,
+    _with_workspace(x, workspace, need,
                     lambda ws, n: lib().gbb_gemm_mixed_w_path(*args, ws, n, path, _stream(x)))
     return y
 
@@ -361,12 +372,13 @@ class Batched:
         dev = calls[0][3].device
         self._ws = workspace if workspace is not None else torch.zeros(max(need, 256), dtype=torch.uint8,
                                                                        device=dev)
+        self._ws_at = _given(self._ws, calls[0][3].get_device())
         self._calls = list(calls)
 
     def launch(self):
         torch = _torch()
         _check(lib().gbb_gemm_mixed_w_batched(self.n, self._images, self._N, self._K, self._x, self._y, self.M,
-                                              self._ws.data_ptr(), self._ws.numel(),
+                                              *self._ws_at,
                                               torch.cuda.current_stream(self._ws.device).cuda_stream))
 
 
@@ -397,7 +409,7 @@ class Graph:
         ys = (ctypes.c_void_p * n)(*[_dev_ptr(c[4], torch.float16, "y") for c in calls])
         out = ctypes.c_void_p()
         self._g = None
-        _check(lib().gbb_graph_create(n, images, Ns, Ks, xs, ys, M, self._ws.data_ptr(), self._ws.numel(),
+        _check(lib().gbb_graph_create(n, images, Ns, Ks, xs, ys, M, *_given(self._ws, calls[0][3].get_device()),
                                       ctypes.byref(out)))
         self._g = out
         self._calls = list(calls)
@@ -453,7 +465,7 @@ def gemm_mixed_w_64x64_path(image, N: int, K: int, x, path: int, out=None, works
     need = lib().gbb_gemm_mixed_w_64x64_path_workspace(N, K, M, path)
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
-    _with_workspace(x.device, workspace, need,
+    _with_workspace(x, workspace, need,
                     lambda ws, n: lib().gbb_gemm_mixed_w_64x64_path(*args, ws, n, path, _stream(x)))
     return y
 
@@ -494,7 +506,7 @@ def gemm_w48a8(image, N: int, K: int, n8: int, xq, xs, ga: int | None = None, ou
         _check(lib().gbb_gemm_w48a8(*args, _stream(xq)))
         return y
     need = 0 if workspace is not None else gemm_w48a8_workspace(N, K, n8, M, ga)
-    _with_workspace(xq.device, workspace, need, lambda ws, n: lib().gbb_gemm_w48a8_split(*args, ws, n, _stream(xq)))
+    _with_workspace(xq, workspace, need, lambda ws, n: lib().gbb_gemm_w48a8_split(*args, ws, n, _stream(xq)))
     return y
 
 

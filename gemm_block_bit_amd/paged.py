@@ -17,7 +17,7 @@ import ctypes
 
 import numpy as np
 
-from .binding import _check, _dev_ptr, _kept, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
+from .binding import _check, _dev_ptr, _given, _kept, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
@@ -195,9 +195,7 @@ def _with_workspace(kind: str, device: int, given, call, args, need):
     replay: one that is kept would be shared with calls outside the graph."""
     stream = _raw_stream(device)
     if given is not None:
-        if given.get_device() != device:
-            raise ValueError(f"workspace is on {given.device}, not on GPU {device}")
-        _check(call(*args, given.data_ptr(), given.numel() * given.element_size(), stream))
+        _check(call(*args, *_given(given, device), stream))
         return
     if _capturing():
         buf = _zeros(max(need(), 16), device)

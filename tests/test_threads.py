@@ -95,7 +95,7 @@ def test_product_calls_on_one_stream_do_not_overlap(monkeypatch):
     class FakeLib:
         gbb_gemm_mixed_w_path = call
         gbb_gemm_mixed_w_path_workspace = staticmethod(lambda N, K, M, path: 64)
-    x = type("X", (), {"shape": (1, 128), "dim": lambda self: 2, "device": "gpu"})()
+    x = type("X", (), {"shape": (1, 128), "dim": lambda self: 2, "device": "gpu", "get_device": lambda self: 0})()
     for name, value in (("_ws_cache", {}), ("_torch", lambda: FakeTorch), ("lib", lambda: FakeLib),
                         ("_dev_ptr", lambda *a: 0), ("_stream", lambda t: 0)):
         monkeypatch.setattr(gbb.binding, name, value)
