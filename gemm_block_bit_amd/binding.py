@@ -255,6 +255,17 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _on(device: int, fn, *args):
+    """fn(*args) with GPU `device` as the current one.  The library launches on
+    the current GPU and plans for it, and the handle of a default stream does
+    not say whose it is."""
+    torch = _torch()
+    if torch.cuda.current_device() == device:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 class _Kept:
     """A device buffer that is kept for one (device, stream), and the lock
     under which its calls are enqueued.  A call may take several launches that
@@ -294,17 +305,17 @@ def _with_workspace(x, given, nbytes: int, call) -> None:
     stream) reused across calls; the library leaves its counters zero after every
     call."""
     torch = _torch()
-    device = x.device
+    device, index = x.device, x.get_device()
     if given is not None:
-        _check(call(*_given(given, x.get_device())))
+        _check(_on(index, call, *_given(given, index)))
     elif nbytes == 0:
-        _check(call(None, 0))
+        _check(_on(index, call, None, 0))
     else:
         kept = _kept(_ws_cache, (device, torch.cuda.current_stream(device).cuda_stream))
         with kept.lock:
             if kept.buf is None or kept.buf.numel() < nbytes:
                 kept.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-            _check(call(kept.buf.data_ptr(), kept.buf.numel()))
+            _check(_on(index, call, kept.buf.data_ptr(), kept.buf.numel()))
 
 
 def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=None):
@@ -313,7 +324,7 @@ def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=N
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    need = lib().gbb_gemm_mixed_w_path_workspace(N, K, M, path)   # 0 when the call needs none
+    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_path_workspace, N, K, M, path)   # 0 when the call needs none
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
     _with_workspace(x, workspace, need,
@@ -335,9 +346,9 @@ def gemm_mixed_w_noalloc(image, N: int, K: int, x, out=None):
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    _check(lib().gbb_gemm_mixed_w_noalloc(
-        _dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
-        _dev_ptr(y, torch.float16, "y"), M, _stream(x)))
+    _check(_on(
+        x.get_device(), lib().gbb_gemm_mixed_w_noalloc, _dev_ptr(image, torch.uint8, "image"), N, K,
+        _dev_ptr(x, torch.float16, "x"), _dev_ptr(y, torch.float16, "y"), M, _stream(x)))
     return y
 
 
@@ -368,18 +379,17 @@ class Batched:
         self._K = (ctypes.c_int * n)(*[c[2] for c in calls])
         self._x = (ctypes.c_void_p * n)(*[_dev_ptr(c[3], torch.float16, "x") for c in calls])
         self._y = (ctypes.c_void_p * n)(*[_dev_ptr(c[4], torch.float16, "y") for c in calls])
-        need = lib().gbb_gemm_mixed_w_batched_workspace(n, self._N, self._K, M)
-        dev = calls[0][3].device
+        dev, self._index = calls[0][3].device, calls[0][3].get_device()
+        need = _on(self._index, lib().gbb_gemm_mixed_w_batched_workspace, n, self._N, self._K, M)
         self._ws = workspace if workspace is not None else torch.zeros(max(need, 256), dtype=torch.uint8,
                                                                        device=dev)
-        self._ws_at = _given(self._ws, calls[0][3].get_device())
+        self._ws_at = _given(self._ws, self._index)
         self._calls = list(calls)
 
     def launch(self):
         torch = _torch()
-        _check(lib().gbb_gemm_mixed_w_batched(self.n, self._images, self._N, self._K, self._x, self._y, self.M,
-                                              *self._ws_at,
-                                              torch.cuda.current_stream(self._ws.device).cuda_stream))
+        _check(_on(self._index, lib().gbb_gemm_mixed_w_batched, self.n, self._images, self._N, self._K, self._x,
+                   self._y, self.M, *self._ws_at, torch.cuda.current_stream(self._ws.device).cuda_stream))
 
 
 class Graph:
@@ -397,8 +407,8 @@ class Graph:
         for (img, N, K, x, y) in calls:
             if x.dim() != 2 or tuple(x.shape) != (M, K) or tuple(y.shape) != (M, N):
                 raise ValueError(f"x must be [{M}][{K}] and y [{M}][{N}]")
-        need = max(gemm_mixed_w_workspace(N, K, M) for (_, N, K, _, _) in calls)
-        dev = calls[0][3].device
+        dev, self._index = calls[0][3].device, calls[0][3].get_device()
+        need = max(_on(self._index, gemm_mixed_w_workspace, N, K, M) for (_, N, K, _, _) in calls)
         self._ws = workspace if workspace is not None else torch.zeros(max(need, 256), dtype=torch.uint8,
                                                                        device=dev)
         n = len(calls)
@@ -409,15 +419,16 @@ class Graph:
         ys = (ctypes.c_void_p * n)(*[_dev_ptr(c[4], torch.float16, "y") for c in calls])
         out = ctypes.c_void_p()
         self._g = None
-        _check(lib().gbb_graph_create(n, images, Ns, Ks, xs, ys, M, *_given(self._ws, calls[0][3].get_device()),
-                                      ctypes.byref(out)))
+        _check(_on(self._index, lib().gbb_graph_create, n, images, Ns, Ks, xs, ys, M, *_given(self._ws, self._index),
+                   ctypes.byref(out)))
         self._g = out
         self._calls = list(calls)
 
     def launch(self):
         """Replay on torch's current stream of the calls' device."""
         torch = _torch()
-        _check(lib().gbb_graph_launch(self._g, torch.cuda.current_stream(self._ws.device).cuda_stream))
+        _check(_on(self._index, lib().gbb_graph_launch, self._g,
+                   torch.cuda.current_stream(self._ws.device).cuda_stream))
 
     def close(self):
         if self._g is not None:
@@ -435,7 +446,7 @@ def unpack_codes(image, N: int, K: int, block_cols: int = 128):
     torch = _torch()
     q = torch.empty((N, K), dtype=torch.uint8, device=image.device)
     fn = lib().gbb_unpack_codes if block_cols == 128 else lib().gbb_unpack_codes_64x64
-    _check(fn(_dev_ptr(image, torch.uint8, "image"), N, K, q.data_ptr(), _stream(image)))
+    _check(_on(image.get_device(), fn, _dev_ptr(image, torch.uint8, "image"), N, K, q.data_ptr(), _stream(image)))
     return q
 
 
@@ -445,7 +456,8 @@ def dequant(image, N: int, K: int, block_cols: int = 128):
     w32 = torch.empty((N, K), dtype=torch.float32, device=image.device)
     w16 = torch.empty((N, K), dtype=torch.float16, device=image.device)
     fn = lib().gbb_dequant if block_cols == 128 else lib().gbb_dequant_64x64
-    _check(fn(_dev_ptr(image, torch.uint8, "image"), N, K, w32.data_ptr(), w16.data_ptr(), _stream(image)))
+    _check(_on(image.get_device(), fn, _dev_ptr(image, torch.uint8, "image"), N, K, w32.data_ptr(), w16.data_ptr(),
+               _stream(image)))
     return w32, w16
 
 
@@ -462,7 +474,7 @@ def gemm_mixed_w_64x64_path(image, N: int, K: int, x, path: int, out=None, works
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    need = lib().gbb_gemm_mixed_w_64x64_path_workspace(N, K, M, path)
+    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_64x64_path_workspace, N, K, M, path)
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
     _with_workspace(x, workspace, need,
@@ -482,8 +494,8 @@ def quant_act_i8(x, ga: int | None = None):
     ga = K if ga is None else ga
     xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
     xs = torch.empty((M,) if ga == K else (M, K // 128), dtype=torch.float16, device=x.device)
-    _check(lib().gbb_quant_act_i8(_dev_ptr(x, torch.float16, "x"), M, K, ga, xq.data_ptr(), xs.data_ptr(),
-                                  _stream(x)))
+    _check(_on(x.get_device(), lib().gbb_quant_act_i8, _dev_ptr(x, torch.float16, "x"), M, K, ga, xq.data_ptr(),
+               xs.data_ptr(), _stream(x)))
     return xq, xs
 
 
@@ -503,9 +515,9 @@ def gemm_w48a8(image, N: int, K: int, n8: int, xq, xs, ga: int | None = None, ou
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, n8, _dev_ptr(xq, torch.int8, "xq"),
             _dev_ptr(xs, torch.float16, "xs"), ga, _dev_ptr(y, torch.float16, "y"), M)
     if not split:
-        _check(lib().gbb_gemm_w48a8(*args, _stream(xq)))
+        _check(_on(xq.get_device(), lib().gbb_gemm_w48a8, *args, _stream(xq)))
         return y
-    need = 0 if workspace is not None else gemm_w48a8_workspace(N, K, n8, M, ga)
+    need = 0 if workspace is not None else _on(xq.get_device(), gemm_w48a8_workspace, N, K, n8, M, ga)
     _with_workspace(xq, workspace, need, lambda ws, n: lib().gbb_gemm_w48a8_split(*args, ws, n, _stream(xq)))
     return y
 
@@ -517,6 +529,6 @@ def w48_group_acc(image, N: int, K: int, n8: int, xq, ga: int | None = None):
     M = xq.shape[0]
     ga = K if ga is None else ga
     acc = torch.empty((M, N, K // 128), dtype=torch.int32, device=xq.device)
-    _check(lib().gbb_w48_group_acc(_dev_ptr(image, torch.uint8, "image"), N, K, n8,
-                                   _dev_ptr(xq, torch.int8, "xq"), ga, acc.data_ptr(), M, _stream(xq)))
+    _check(_on(xq.get_device(), lib().gbb_w48_group_acc, _dev_ptr(image, torch.uint8, "image"), N, K, n8,
+               _dev_ptr(xq, torch.int8, "xq"), ga, acc.data_ptr(), M, _stream(xq)))
     return acc

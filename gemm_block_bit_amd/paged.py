@@ -17,7 +17,7 @@ import ctypes
 
 import numpy as np
 
-from .binding import _check, _dev_ptr, _given, _kept, _np_ptr, _PagedCache, _RopeScaling, _torch, lib
+from .binding import _check, _dev_ptr, _given, _kept, _np_ptr, _on, _PagedCache, _RopeScaling, _torch, lib
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
@@ -67,19 +67,29 @@ def _device_of(t, name) -> int:
     return device
 
 
-_int32 = _float32 = _raw_stream = _capturing = None
+_int32 = _float32 = _raw_stream = _current_device = _capturing = None
 
 
 def _resolve() -> None:
     """What every call needs of torch, looked up once.  The stream as a
     hipStream_t is taken by the accessor that torch's own generated code uses
     (the public one builds two Python objects for every call, 2 us)."""
-    global _int32, _float32, _raw_stream, _capturing
+    global _int32, _float32, _raw_stream, _current_device, _capturing
     torch = _torch()
     _float32, _capturing = torch.float32, torch.cuda.is_current_stream_capturing
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _int32 = torch.int32
+
+
+def _enqueue(device: int, call, *args) -> None:
+    """call(*args, stream) with torch's current stream of GPU `device`, which
+    has to be the current GPU for the library to launch there."""
+    if _current_device() == device:
+        _check(call(*args, _raw_stream(device)))
+    else:
+        _check(_on(device, call, *args, _raw_stream(device)))
 
 
 # ----------------------------------------------------------------------------
@@ -128,9 +138,8 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
             raise ValueError(f"out is on {y.device}, not on {x.device}")
     tp, n_pos, rot = _table(table, device)
     ys = y.stride()
-    _check(lib().gbb_rope(x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H, D,
-                          _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout),
-                          int(transpose), _raw_stream(device)))
+    _enqueue(device, lib().gbb_rope, x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H,
+             D, _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout), int(transpose))
     return y
 
 
@@ -193,6 +202,8 @@ def _with_workspace(kind: str, device: int, given, call, args, need):
     small.  A call that
     is captured in a graph gets a buffer of the graph's own, cleared in every
     replay: one that is kept would be shared with calls outside the graph."""
+    if _current_device() != device:
+        return _on(device, _with_workspace, kind, device, given, call, args, need)
     stream = _raw_stream(device)
     if given is not None:
         _check(call(*args, *_given(given, device), stream))
@@ -237,16 +248,16 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
         q = out
         qp = _ptr(q, qkv.dtype, device, "out", (T, q_heads, D))
     tp, n_pos, rot = _table(table, device)
-    _check(lib().gbb_rope_append(
-        cache._ref, qkv.data_ptr(), stride[0] if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
-        _ptr(positions, _int32, device, "positions", (T,)), _ptr(slots, _int32, device, "slots", (T,)), tp,
-        n_pos, rot, _layout(layout), qp, _raw_stream(device)))
+    _enqueue(device, lib().gbb_rope_append, cache._ref, qkv.data_ptr(), stride[0] if T > 1 else width,
+             _dtype_code(qkv.dtype), T, q_heads, _ptr(positions, _int32, device, "positions", (T,)),
+             _ptr(slots, _int32, device, "slots", (T,)), tp, n_pos, rot, _layout(layout), qp)
     return q
 
 
 def paged_attention_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int,
                               with_weights: bool = False) -> int:
-    return lib().gbb_paged_attention_workspace(cache._ref, batch, q_heads, max_len, int(with_weights))
+    return _on(cache._index, lib().gbb_paged_attention_workspace, cache._ref, batch, q_heads, max_len,
+               int(with_weights))
 
 
 def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, scale: float | None = None, out=None,

@@ -19,6 +19,7 @@ def views():
 def test_views_with_gaps_are_refused(i, monkeypatch):
     ws = views()[i]
     monkeypatch.setattr(gbb.paged, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(gbb.paged, "_current_device", lambda: -1)
     with pytest.raises(ValueError, match="contiguous"):
         gbb.paged._with_workspace("evict", -1, ws, never, (), never)
 
@@ -36,6 +37,7 @@ def test_views_with_gaps_are_refused_by_products(i, monkeypatch):
     monkeypatch.setattr(gbb.binding, "lib", lambda: FakeLib)
     monkeypatch.setattr(gbb.binding, "_dev_ptr", lambda *a: 0)
     monkeypatch.setattr(gbb.binding, "_stream", lambda t: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     y = torch.zeros(1, 64, dtype=torch.float16)
     for call in (lambda: gbb.gemm_mixed_w(x, 64, 128, x, y, ws), lambda: gbb.gemm_mixed_w_64x64(x, 64, 128, x, y, ws),
                  lambda: gbb.gemm_w48a8(x, 64, 128, 0, x, x, out=y, workspace=ws),

@@ -61,6 +61,7 @@ def test_paged_calls_on_one_stream_do_not_overlap(monkeypatch):
     call = Library(at=-3)
     monkeypatch.setattr(gbb.paged, "_ws_cache", {})
     monkeypatch.setattr(gbb.paged, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(gbb.paged, "_current_device", lambda: 0)
     monkeypatch.setattr(gbb.paged, "_capturing", lambda: False)
     monkeypatch.setattr(gbb.paged, "_zeros", lambda n, device: Buffer(n))
     in_threads(4, lambda i: [gbb.paged._with_workspace("evict", 0, None, call, (), lambda: 16) for _ in range(5)])
@@ -76,6 +77,7 @@ def test_paged_calls_grow_one_buffer(monkeypatch):
         return 0 if n >= 2 << 20 else -5
     monkeypatch.setattr(gbb.paged, "_ws_cache", {})
     monkeypatch.setattr(gbb.paged, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(gbb.paged, "_current_device", lambda: 0)
     monkeypatch.setattr(gbb.paged, "_capturing", lambda: False)
     monkeypatch.setattr(gbb.paged, "_zeros", lambda n, device: Buffer(n))
     in_threads(4, lambda i: gbb.paged._with_workspace("attention", 0, None, call, (), lambda: 2 << 20))
@@ -90,6 +92,7 @@ def test_product_calls_on_one_stream_do_not_overlap(monkeypatch):
         zeros = staticmethod(lambda n, dtype, device: Buffer(n))
 
         class cuda:
+            current_device = staticmethod(lambda: 0)
             current_stream = staticmethod(lambda device: type("S", (), {"cuda_stream": 0}))
 
     class FakeLib:
