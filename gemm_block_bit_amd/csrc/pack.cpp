@@ -10,7 +10,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
 #include <thread>
 #include <vector>
 
@@ -22,15 +21,15 @@ namespace gbb {
 // ---------------------------------------------------------------------------
 // error text
 // ---------------------------------------------------------------------------
-static thread_local std::string g_last_error;
+static thread_local char g_last_error[512];   // no allocation: it also tells that memory ran out
 
 gbb_status fail(gbb_status st, const char* fmt, ...) {
-  char buf[512];
+  char buf[sizeof g_last_error] = "";   // the last text may be among the arguments
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  strcpy(g_last_error, buf);
   return st;
 }
 
@@ -313,7 +312,7 @@ static gbb_status pack_blocks(const uint16_t* W, int N, int K, const uint8_t* bi
 
 using namespace gbb;
 
-extern "C" const char* gbb_last_error(void) { return g_last_error.c_str(); }
+extern "C" const char* gbb_last_error(void) { return g_last_error; }
 
 extern "C" size_t gbb_packed_bytes(const uint8_t* bits, int N, int K) {
   if (check_bits(bits, N, K) != GBB_OK) return 0;

@@ -1,8 +1,8 @@
 // Host tables of rotations for the rotary positions (gbb_rope_table).
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <new>
-#include <system_error>
 #include <thread>
 #include <vector>
 
@@ -85,8 +85,9 @@ extern "C" gbb_status gbb_rope_table(int rot, int n_pos, double base, const gbb_
     int p0 = 0;
     try {
       for (; p0 + step < n_pos; p0 += step) pool.emplace_back(rows, p0, p0 + step);
-    } catch (const std::system_error&) {
-      // no further thread to be had: this one does the rest
+    } catch (const std::exception&) {
+      // no further thread, or no memory for its state, to be had: this one
+      // does the rest, and those that run are joined below
     }
     rows(p0, n_pos);
     for (auto& t : pool) t.join();
