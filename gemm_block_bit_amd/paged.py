@@ -96,9 +96,17 @@ def _enqueue(device: int, call, *args) -> None:
 # rotary positions
 # ----------------------------------------------------------------------------
 def rope_table(rot: int, n_pos: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
-               original_len: float = 0.0, low: float = 1.0, high: float = 4.0, attention: float = 1.0) -> np.ndarray:
+               original_len: float = 0.0, low: float | None = None, high: float | None = None,
+               attention: float = 1.0) -> np.ndarray:
     """float32 [n_pos][rot/2][2] of (cos, sin) on the host (see
-    gbb_rope_table); scaling is plain, linear, bands or yarn."""
+    gbb_rope_table); scaling is plain, linear, bands or yarn.  low and high
+    default to what each is published with: bands 1 and 4 wave lengths in
+    original_len, yarn 1 and 32 turns.  attention is left to the caller (yarn
+    is published with 0.1 ln factor + 1)."""
+    if low is None:
+        low = 1.0
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     table = np.empty((max(0, n_pos), max(0, rot) // 2, 2), np.float32)
