@@ -67,18 +67,20 @@ def _device_of(t, name) -> int:
     return device
 
 
-_int32 = _float32 = _raw_stream = _current_device = _capturing = None
+_int32 = _float32 = _raw_stream = _current_device = _capturing = _grad_enabled = _written = None
 
 
 def _resolve() -> None:
     """What every call needs of torch, looked up once.  The stream as a
     hipStream_t is taken by the accessor that torch's own generated code uses
     (the public one builds two Python objects for every call, 2 us)."""
-    global _int32, _float32, _raw_stream, _current_device, _capturing
+    global _int32, _float32, _raw_stream, _current_device, _capturing, _grad_enabled, _written
     torch = _torch()
     _float32, _capturing = torch.float32, torch.cuda.is_current_stream_capturing
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    # _written: a tensor's version, by which torch sees that a saved one changed
+    _grad_enabled, _written = torch.is_grad_enabled, torch.autograd.graph.increment_version
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _int32 = torch.int32
 
@@ -128,9 +130,16 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
     contiguous) with its first 2 * table.shape[1] elements rotated to int32
     positions [T].  out: where to write (x itself for in place), else a new
     contiguous tensor.  transpose: the transposed rotation, which is the
-    gradient with respect to x."""
+    gradient with respect to x; where x requires one, the result takes part in
+    torch's differentiation (the table has no gradient)."""
     if _int32 is None:
         _resolve()
+    if getattr(x, "requires_grad", False) and _grad_enabled():
+        return _differentiable().apply(x, positions, table, layout, transpose, out)
+    return _rope(x, positions, table, layout, transpose, out)
+
+
+def _rope(x, positions, table, layout, transpose, out):
     device = _device_of(x, "x")
     shape, xs = x.shape, x.stride()
     if len(shape) != 3 or xs[2] != 1:
@@ -148,7 +157,39 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
     ys = y.stride()
     _enqueue(device, lib().gbb_rope, x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H,
              D, _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout), int(transpose))
+    if out is not None:
+        _written(out)
     return y
+
+
+_Rope = None
+
+
+def _differentiable():
+    """The rotation as a torch.autograd.Function, made at its first use."""
+    global _Rope
+    if _Rope is not None:
+        return _Rope
+    torch = _torch()
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, table, layout, transpose, out):
+            ctx.layout, ctx.transpose = layout, transpose
+            ctx.save_for_backward(positions, table)
+            if out is not None:
+                ctx.mark_dirty(out)
+            return _rope(x, positions, table, layout, transpose, out)
+
+        @staticmethod
+        def backward(ctx, g):
+            positions, table = ctx.saved_tensors
+            if g.stride(2) != 1:
+                g = g.contiguous()
+            return rope(g, positions, table, ctx.layout, not ctx.transpose), None, None, None, None, None
+
+    _Rope = Rope
+    return Rope
 
 
 # ----------------------------------------------------------------------------
