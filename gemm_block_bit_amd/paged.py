@@ -85,15 +85,6 @@ def _resolve() -> None:
     _int32 = torch.int32
 
 
-def _enqueue(device: int, call, *args) -> None:
-    """call(*args, stream) with torch's current stream of GPU `device`, which
-    has to be the current GPU for the library to launch there."""
-    if _current_device() == device:
-        _check(call(*args, _raw_stream(device)))
-    else:
-        _check(_on(device, call, *args, _raw_stream(device)))
-
-
 # ----------------------------------------------------------------------------
 # rotary positions
 # ----------------------------------------------------------------------------
@@ -134,13 +125,11 @@ def rope(x, positions, table, layout: str = "half", transpose: bool = False, out
     torch's differentiation (the table has no gradient)."""
     if _int32 is None:
         _resolve()
-    if getattr(x, "requires_grad", False) and _grad_enabled():
-        return _differentiable().apply(x, positions, table, layout, transpose, out)
-    return _rope(x, positions, table, layout, transpose, out)
-
-
-def _rope(x, positions, table, layout, transpose, out):
     device = _device_of(x, "x")
+    if x.requires_grad and _grad_enabled():
+        return _differentiable().apply(x, positions, table, layout, transpose, out)
+    if _current_device() != device:
+        return _on(device, rope, x, positions, table, layout, transpose, out)
     shape, xs = x.shape, x.stride()
     if len(shape) != 3 or xs[2] != 1:
         raise ValueError("x must be [T][H][D] with contiguous heads")
@@ -155,8 +144,9 @@ def _rope(x, positions, table, layout, transpose, out):
             raise ValueError(f"out is on {y.device}, not on {x.device}")
     tp, n_pos, rot = _table(table, device)
     ys = y.stride()
-    _enqueue(device, lib().gbb_rope, x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H,
-             D, _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout), int(transpose))
+    _check(lib().gbb_rope(x.data_ptr(), xs[0], xs[1], y.data_ptr(), ys[0], ys[1], _dtype_code(x.dtype), T, H, D,
+                          _ptr(positions, _int32, device, "positions", (T,)), tp, n_pos, rot, _layout(layout),
+                          int(transpose), _raw_stream(device)))
     if out is not None:
         _written(out)
     return y
@@ -179,7 +169,7 @@ def _differentiable():
             ctx.save_for_backward(positions, table)
             if out is not None:
                 ctx.mark_dirty(out)
-            return _rope(x, positions, table, layout, transpose, out)
+            return rope(x, positions, table, layout, transpose, out)   # torch runs this without gradients
 
         @staticmethod
         def backward(ctx, g):
@@ -244,15 +234,13 @@ _E_SPACE = -5
 
 
 def _with_workspace(kind: str, device: int, given, call, args, need):
-    """call(*args, workspace, bytes, stream) with the caller's workspace, or
-    with a buffer kept per use, device and stream (zero when it is new; kept
-    apart from the buffer of the gemm calls, which has to stay zero), one call
-    at a time.  need() is only asked when a call says that the buffer is too
-    small.  A call that
-    is captured in a graph gets a buffer of the graph's own, cleared in every
-    replay: one that is kept would be shared with calls outside the graph."""
-    if _current_device() != device:
-        return _on(device, _with_workspace, kind, device, given, call, args, need)
+    """call(*args, workspace, bytes, stream), on the current GPU, with the
+    caller's workspace, or with a buffer kept per use, device and stream (zero
+    when it is new; kept apart from the buffer of the gemm calls, which has to
+    stay zero), one call at a time.  need() is only asked when a call says that
+    the buffer is too small.  A call that is captured in a graph gets a buffer
+    of the graph's own, cleared in every replay: one that is kept would be
+    shared with calls outside the graph."""
     stream = _raw_stream(device)
     if given is not None:
         _check(call(*args, *_given(given, device), stream))
@@ -282,6 +270,8 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
     (rows may be strided), writes k and v to the cache's int32 slots [T] and
     returns q [T][q_heads][head size] (see gbb_rope_append)."""
     device = cache._index
+    if _current_device() != device:
+        return _on(device, rope_append, cache, qkv, q_heads, positions, slots, table, layout, out)
     if _device_of(qkv, "qkv") != device:
         raise ValueError(f"qkv is on {qkv.device}, not on GPU {device}")
     D = cache.head_dim
@@ -297,9 +287,10 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
         q = out
         qp = _ptr(q, qkv.dtype, device, "out", (T, q_heads, D))
     tp, n_pos, rot = _table(table, device)
-    _enqueue(device, lib().gbb_rope_append, cache._ref, qkv.data_ptr(), stride[0] if T > 1 else width,
-             _dtype_code(qkv.dtype), T, q_heads, _ptr(positions, _int32, device, "positions", (T,)),
-             _ptr(slots, _int32, device, "slots", (T,)), tp, n_pos, rot, _layout(layout), qp)
+    _check(lib().gbb_rope_append(
+        cache._ref, qkv.data_ptr(), stride[0] if T > 1 else width, _dtype_code(qkv.dtype), T, q_heads,
+        _ptr(positions, _int32, device, "positions", (T,)), _ptr(slots, _int32, device, "slots", (T,)), tp,
+        n_pos, rot, _layout(layout), qp, _raw_stream(device)))
     return q
 
 
@@ -318,6 +309,8 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     weights with this step's added (cache.weights itself for in place).
     Returns [B][q_heads][head size] (see gbb_paged_attention)."""
     device, D = cache._index, cache.head_dim
+    if _current_device() != device:
+        return _on(device, paged_attention, cache, q, block_table, lengths, max_len, scale, out, lse, weights_out, workspace)
     if _device_of(q, "q") != device:
         raise ValueError(f"q is on {q.device}, not on GPU {device}")
     shape, stride = q.shape, q.stride()
@@ -359,6 +352,9 @@ def cache_evict(cache: PagedCache, block_table, lengths, max_len: int, budget: i
     if cache.weights is None or cache.positions is None:
         raise ValueError("eviction needs a cache with weights and positions")
     device = cache._index
+    if _current_device() != device:
+        return _on(device, cache_evict, cache, block_table, lengths, max_len, budget, recent, weights_out, positions_out,
+                   lengths_out, workspace)
     bt = _ptr(block_table, _int32, device, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B][pages]")
