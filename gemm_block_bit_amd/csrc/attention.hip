@@ -65,7 +65,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;   // see above: 2^14 < 65504
 constexpr int kMaxJoin = 64;     // runs that the last workgroup of a sequence joins itself
-constexpr int kMaxArrived = 4096;   // counters of such sequences, at the workspace's start
+constexpr int kMaxArrived = GBB_ATTENTION_COUNTERS / 4;   // counters of such sequences, at the workspace's start
 constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles x 4 waves x 32 slots
 
 

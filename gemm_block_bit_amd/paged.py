@@ -235,34 +235,41 @@ _E_SPACE = -5
 
 def _with_workspace(kind: str, device: int, given, call, args, need):
     """call(*args, workspace, bytes, stream), on the current GPU, with the
-    caller's workspace, or with a buffer kept per use, device and stream (zero
-    when it is new; kept apart from the buffer of the gemm calls, which has to
-    stay zero), one call at a time.  need() is only asked when a call says that
-    the buffer is too small.  A call that is captured in a graph gets a buffer
-    of the graph's own, cleared in every replay: one that is kept would be
-    shared with calls outside the graph."""
+    caller's workspace, or with a buffer kept per use, device and stream (apart
+    from the buffer of the gemm calls, which has to stay zero), one call at a
+    time.  need() is only asked when a call says that the buffer is too small.
+    A call that is captured in a graph gets a buffer of the graph's own, whose
+    counters are cleared in every replay: one that is kept would be shared with
+    calls outside the graph."""
     stream = _raw_stream(device)
     if given is not None:
         _check(call(*args, *_given(given, device), stream))
         return
     if _capturing():
-        buf = _zeros(max(need(), 16), device)
+        buf = _buffer(kind, max(need(), 16), device)
         _check(call(*args, buf.data_ptr(), buf.numel(), stream))
         return
     kept = _kept(_ws_cache, (kind, device, stream))
     with kept.lock:
         if kept.buf is None:
-            kept.buf = _zeros(1 << 20, device)
+            kept.buf = _buffer(kind, 1 << 20, device)
         st = call(*args, kept.buf.data_ptr(), kept.buf.numel(), stream)
         if st == _E_SPACE:
-            kept.buf = _zeros(need(), device)
+            kept.buf = _buffer(kind, need(), device)
             st = call(*args, kept.buf.data_ptr(), kept.buf.numel(), stream)
         _check(st)
 
 
-def _zeros(nbytes: int, device: int):
+# bytes at a workspace's start that have to be zero before its first use
+_CLEARED = {"attention": 16384, "evict": 0}
+
+
+def _buffer(kind: str, nbytes: int, device: int):
     torch = _torch()
-    return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    if _CLEARED[kind]:
+        buf[:_CLEARED[kind]].zero_()
+    return buf
 
 
 def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, layout: str = "half", out=None):
@@ -296,6 +303,8 @@ def rope_append(cache: PagedCache, qkv, q_heads: int, positions, slots, table, l
 
 def paged_attention_workspace(cache: PagedCache, batch: int, q_heads: int, max_len: int,
                               with_weights: bool = False) -> int:
+    """Bytes of paged_attention's workspace (with_weights: of a call with
+    weights_out).  A new one's first 16384 have to be zero: torch.zeros."""
     return _on(cache._index, lib().gbb_paged_attention_workspace, cache._ref, batch, q_heads, max_len,
                int(with_weights))
 
@@ -307,7 +316,9 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
     (int32 [B] and [B][pages]); scale defaults to head size ** -0.5.  lse:
     float32 [B][q_heads] to fill.  weights_out: where to write the cache's
     weights with this step's added (cache.weights itself for in place).
-    Returns [B][q_heads][head size] (see gbb_paged_attention)."""
+    workspace: paged_attention_workspace bytes that were zero when they were
+    new (torch.zeros, not empty: outputs would stay unwritten), else the
+    binding's own.  Returns [B][q_heads][head size] (see gbb_paged_attention)."""
     device, D = cache._index, cache.head_dim
     if _current_device() != device:
         return _on(device, paged_attention, cache, q, block_table, lengths, max_len, scale, out, lse, weights_out, workspace)
@@ -340,6 +351,7 @@ def paged_attention(cache: PagedCache, q, block_table, lengths, max_len: int, sc
 
 
 def cache_evict_workspace(cache: PagedCache, batch: int, max_len: int, budget: int) -> int:
+    """Bytes of cache_evict's workspace, which may hold anything."""
     return lib().gbb_cache_evict_workspace(cache._ref, batch, max_len, budget)
 
 

@@ -508,10 +508,13 @@ gbb_status gbb_rope_append(const gbb_paged_cache* cache, const void* qkv, int64_
                            int n_pos, int rot, int layout, void* q, void* stream);
 
 /* Bytes of workspace of gbb_paged_attention (0 on a bad argument or where
- * none is needed).  It must be zero before its first use; every call leaves
- * it ready for the next one of any size, but not zero: it must not be shared
- * with calls that want a zero workspace (gbb_gemm_*), with gbb_cache_evict,
- * which leaves it in any state, or with a call that may run at the same time. */
+ * none is needed).  Its first GBB_ATTENTION_COUNTERS bytes (all of it, if it
+ * is smaller) must be zero before its first use: with other contents outputs
+ * stay unwritten, without an error.  Every call leaves it ready for the next
+ * one of any size, but not zero: it must not be shared with calls that want a
+ * zero workspace (gbb_gemm_*), with gbb_cache_evict, which leaves it in any
+ * state, or with a call that may run at the same time. */
+#define GBB_ATTENTION_COUNTERS 16384
 size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_heads, int max_len, int with_weights);
 
 /* Attention of one new token per sequence over the cache:

@@ -47,7 +47,7 @@ def where(monkeypatch):
             (gbb.paged, "lib", lambda: fake), (gbb.paged, "_ws_cache", {}), (gbb.paged, "_resolve", lambda: None),
             (gbb.paged, "_raw_stream", lambda d: 0), (gbb.paged, "_capturing", capturing),
             (gbb.paged, "_current_device", current), (gbb.paged, "_device_of", lambda t, name: t.get_device()),
-            (gbb.paged, "_zeros", lambda n, d: torch.zeros(n, dtype=torch.uint8))):
+            (gbb.paged, "_buffer", lambda kind, n, d: torch.zeros(n, dtype=torch.uint8))):
         monkeypatch.setattr(owner, name, value, raising=False)
     yield seen
     assert state["current"] == 0

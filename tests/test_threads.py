@@ -63,7 +63,7 @@ def test_paged_calls_on_one_stream_do_not_overlap(monkeypatch):
     monkeypatch.setattr(gbb.paged, "_raw_stream", lambda device: 0)
     monkeypatch.setattr(gbb.paged, "_current_device", lambda: 0)
     monkeypatch.setattr(gbb.paged, "_capturing", lambda: False)
-    monkeypatch.setattr(gbb.paged, "_zeros", lambda n, device: Buffer(n))
+    monkeypatch.setattr(gbb.paged, "_buffer", lambda kind, n, device: Buffer(n))
     in_threads(4, lambda i: [gbb.paged._with_workspace("evict", 0, None, call, (), lambda: 16) for _ in range(5)])
     assert call.calls == 20 and len(call.inside) == 1 and not call.overlapped
 
@@ -79,7 +79,7 @@ def test_paged_calls_grow_one_buffer(monkeypatch):
     monkeypatch.setattr(gbb.paged, "_raw_stream", lambda device: 0)
     monkeypatch.setattr(gbb.paged, "_current_device", lambda: 0)
     monkeypatch.setattr(gbb.paged, "_capturing", lambda: False)
-    monkeypatch.setattr(gbb.paged, "_zeros", lambda n, device: Buffer(n))
+    monkeypatch.setattr(gbb.paged, "_buffer", lambda kind, n, device: Buffer(n))
     in_threads(4, lambda i: gbb.paged._with_workspace("attention", 0, None, call, (), lambda: 2 << 20))
     assert sorted(seen) == [1 << 20] + [2 << 20] * 4
 
