@@ -554,7 +554,11 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   // runs, in their order whichever it is.  Partial results are written and
   // read at device scope (past the caches of the XCDs, which do not see each
   // other's), every wave awaits its writes before the count, and no
-  // workgroup waits for another.
+  // workgroup waits for another.  The order of the partial results and the
+  // count so rests on that wait and on the reads' scope, not on the count's
+  // own order: a release and an acquire there write back and invalidate the
+  // whole XCD's L2 once a run (32 ragged 107 -> 125 us, 2 of 131072 103 -> 115,
+  // 1 of 1000 7.1 -> 7.4), for memory that nothing here keeps in it.
   __shared__ unsigned count;
   loads_left<0>();
   __syncthreads();
@@ -746,10 +750,13 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   // us whole, 97 and 100 in runs of 2048 and 1024), three for five CUs up to
   // 2048 of up to 128 elements (160 pairs of 2000: 32 us, 41 in 1024; of up to
   // 2000: 21, 18.5 in 1024), three for eight up to 1024 (96 of 1000: 12 and
-  // 13.5 in 256; of up to 1000: 11 and 12).
+  // 13.5 in 256; of up to 1000: 11 and 12; with 256 elements 28.5, 26.3 in 256,
+  // and of up to 1000 17.5 to 19 and 20.6).  Lengths are known on the GPU only, so a
+  // rule takes what is better for equal and ragged ones together.
   // Else the longest run that makes three for five CUs (24 pairs of 8000: 20 us
   // in 192 runs of 1024, 24 in 512; 8 of 60000: 48 in 240 of 2048, 53 in 1024;
-  // 8 of 32768: 31 in 256 of 1024, 33 in 128 of 2048, 48 in 64 of 4096).  It
+  // 8 of 32768: 31 in 256 of 1024, 33 in 128 of 2048, 48 in 64 of 4096; 100 of 1500:
+  // 17.2 in 200 of 1024, 21.6 in 512, but of up to 1500 13.6 to 14.1 and 12.5).  It
   // has at most 2048 slots, and those one for every CU, so that ragged lengths
   // balance (32 ragged of up to 8192: 105 us, 114 in 4096; 80 pairs of up to
   // 5000: 21 in 1024, 25 in 240 of 2048), but above 16384 there are runs enough
@@ -765,12 +772,12 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
       (5 * pairs >= 3 * cus && max_len <= 2048 && c.head_dim < 256)) {
     p.wide = pairs < cus || max_len >= 1024;
   } else {
-    const bool ragged = max_len <= 16384;   // runs are few for a sequence
-    if (ragged) chunk = 2048;
+    const bool few = max_len <= 16384;   // runs for a sequence
+    if (few) chunk = 2048;
     const int least = max_len <= 128 * 16 ? 128 : max_len <= 256 * 16 ? 256 : max_len <= 512 * 16 ? 512 : 1024;
     const auto enough = [&] {
       const int64_t runs = pairs * ((max_len + chunk - 1) / chunk);
-      return ragged && chunk == 2048 ? runs >= cus : 5 * runs >= 3 * cus;
+      return few && chunk == 2048 ? runs >= cus : 5 * runs >= 3 * cus;
     };
     while (chunk > least && !enough()) chunk /= 2;
     p.wide = chunk >= 512;
