@@ -4,8 +4,9 @@
 // For a kv head with G query heads the work is two thin products and a
 // softmax, o = softmax(scale q K^T) V with q [G][D]: 4 G D operations a slot
 // against 2 D elements read, so with G <= 16 the cache's bytes bound it and
-// the matrix cores, at 16 query rows a tile, have room to spare (5 to 12 % of
-// the cycles; vector instructions 14 to 30 %).
+// the matrix cores, at 16 query rows a tile, have room to spare (8 to 15 % of
+// the cycles; vector instructions 17 to 34 %).  A workgroup has at most 16 query
+// heads: where a kv head has more, its K and V are read once for every 16.
 //
 // A workgroup takes one run of `chunk` slots of one (sequence, kv head); its
 // waves take tiles of 32 slots in turn, one pass with the running maximum:
@@ -45,7 +46,7 @@
 // over the kv head's query heads, one thread a slot, without atomics.
 //
 // Measured: 32 sequences of up to 8192 slots (64 / 8 heads of 128, bf16,
-// 523 MB) 104 us, 5.0 TB/s; 2 of 131072 (32 / 8, e4m3, 537 MB) 99 us, 5.4
+// 523 MB) 103 us, 5.1 TB/s; 2 of 131072 (32 / 8, e4m3, 537 MB) 100 us, 5.4
 // TB/s; a plain read kernel reaches 5.2 to 5.5 TB/s here.  1 of 1000 slots (32
 // / 8, fp16) 7 us, a chain of dependent steps: launch, page, K and V, scores,
 // the joins in the workgroup and over the runs.

@@ -9,10 +9,12 @@
 // a token's row of the table (4 rot bytes) is read once per workgroup from
 // memory and is small against the token's heads.
 //
-// Measured: 8192 tokens of 64 / 8 heads of 128 (bf16) rotated and written to a
-// cache 65 us, 5.2 TB/s; the transpose of 16384 tokens of 32 heads of 128 49
-// us, 5.5 TB/s; a large copy reaches 5.0 to 5.2 TB/s here.  Calls of up to about
-// a hundred tokens take 2.4 to 3.5 us, a launch and two dependent reads.
+// Measured, a call among others: 8192 tokens of 64 / 8 heads of 128 (bf16)
+// rotated and written to a cache 65 us, 5.2 TB/s; the transpose of 16384 tokens
+// of 32 heads of 128 49 us, 5.5 TB/s, with one input and output or with eight
+// in turn (2.1 GB, no cache holds them), where a copy of that size takes 50.6
+// (5.3 TB/s).  Calls of up to about a hundred tokens take 2.4 to 3.5 us, a
+// launch and two dependent reads.
 #include <algorithm>
 
 #include "device.h"

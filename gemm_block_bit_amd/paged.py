@@ -10,6 +10,8 @@ A decoding step around the quantized products:
     y = gemm_mixed_w(..., o.view(T, -1))
 
 Every call enqueues on torch's current stream of the cache's (or x's) device.
+Calls of several threads on one stream are as good as one after the other.  rope
+takes part in torch's differentiation; the other calls' results have no gradient.
 """
 from __future__ import annotations
 
