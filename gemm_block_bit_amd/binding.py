@@ -324,9 +324,9 @@ def gemm_mixed_w_path(image, N: int, K: int, x, path: int, out=None, workspace=N
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_path_workspace, N, K, M, path)   # 0 when the call needs none
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
+    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_path_workspace, N, K, M, path)   # 0 when the call needs none
     _with_workspace(x, workspace, need,
                     lambda ws, n: lib().gbb_gemm_mixed_w_path(*args, ws, n, path, _stream(x)))
     return y
@@ -407,16 +407,16 @@ class Graph:
         for (img, N, K, x, y) in calls:
             if x.dim() != 2 or tuple(x.shape) != (M, K) or tuple(y.shape) != (M, N):
                 raise ValueError(f"x must be [{M}][{K}] and y [{M}][{N}]")
-        dev, self._index = calls[0][3].device, calls[0][3].get_device()
-        need = max(_on(self._index, gemm_mixed_w_workspace, N, K, M) for (_, N, K, _, _) in calls)
-        self._ws = workspace if workspace is not None else torch.zeros(max(need, 256), dtype=torch.uint8,
-                                                                       device=dev)
         n = len(calls)
         images = (ctypes.c_void_p * n)(*[_dev_ptr(c[0], torch.uint8, "image") for c in calls])
         Ns = (ctypes.c_int * n)(*[c[1] for c in calls])
         Ks = (ctypes.c_int * n)(*[c[2] for c in calls])
         xs = (ctypes.c_void_p * n)(*[_dev_ptr(c[3], torch.float16, "x") for c in calls])
         ys = (ctypes.c_void_p * n)(*[_dev_ptr(c[4], torch.float16, "y") for c in calls])
+        dev, self._index = calls[0][3].device, calls[0][3].get_device()
+        need = max(_on(self._index, gemm_mixed_w_workspace, N, K, M) for (_, N, K, _, _) in calls)
+        self._ws = workspace if workspace is not None else torch.zeros(max(need, 256), dtype=torch.uint8,
+                                                                       device=dev)
         out = ctypes.c_void_p()
         self._g = None
         _check(_on(self._index, lib().gbb_graph_create, n, images, Ns, Ks, xs, ys, M, *_given(self._ws, self._index),
@@ -474,9 +474,9 @@ def gemm_mixed_w_64x64_path(image, N: int, K: int, x, path: int, out=None, works
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=x.device)
-    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_64x64_path_workspace, N, K, M, path)
     args = (_dev_ptr(image, torch.uint8, "image"), N, K, _dev_ptr(x, torch.float16, "x"),
             _dev_ptr(y, torch.float16, "y"), M)
+    need = _on(x.get_device(), lib().gbb_gemm_mixed_w_64x64_path_workspace, N, K, M, path)
     _with_workspace(x, workspace, need,
                     lambda ws, n: lib().gbb_gemm_mixed_w_64x64_path(*args, ws, n, path, _stream(x)))
     return y

@@ -121,3 +121,14 @@ def test_attention_asks_for_zero_counters_only(n, max_len, weights):
         results.append([out, lse] + ([w] if weights else []))
     for r in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
+
+
+def test_tensors_of_the_cpu_are_refused_as_such():
+    """Before a GPU is asked for anything, with or without one."""
+    x, y, image = torch.zeros(1, 128, dtype=torch.float16), torch.zeros(1, 64, dtype=torch.float16), torch.zeros(64, dtype=torch.uint8)
+    for call in (lambda: gbb.gemm_mixed_w(image, 64, 128, x), lambda: gbb.gemm_mixed_w_64x64(image, 64, 128, x),
+                 lambda: gbb.gemm_mixed_w_noalloc(image, 64, 128, x), lambda: gbb.Batched([(image, 64, 128, x, y)]),
+                 lambda: gbb.Graph([(image, 64, 128, x, y)]), lambda: gbb.quant_act_i8(x), lambda: gbb.dequant(image, 64, 128),
+                 lambda: gbb.gemm_w48a8(image, 64, 128, 0, x.to(torch.int8), x)):
+        with pytest.raises(TypeError, match="torch tensor on a GPU"):
+            call()
