@@ -38,7 +38,11 @@ from .paged import (  # noqa: F401
     PagedCache,
     cache_evict,
     cache_evict_workspace,
+    cache_keep,
+    norm_rope,
     paged_attention,
+    paged_attention_tokens,
+    paged_attention_tokens_workspace,
     paged_attention_workspace,
     rope,
     rope_append,

@@ -43,6 +43,11 @@ class _PagedCache(ctypes.Structure):    # gbb_paged_cache
                 ("dtype", _i), ("num_pages", _i), ("page", _i), ("kv_heads", _i), ("head_dim", _i)]
 
 
+class _AttentionOptions(ctypes.Structure):   # gbb_attention_options
+    _fields_ = [("softcap", _f), ("slopes", _vp), ("window", _i), ("first", _vp), ("prefix", _vp), ("tree", _vp),
+                ("tree_words", _i)]
+
+
 _SIGS = {
     "gbb_last_error": (ctypes.c_char_p, []),
     "gbb_version": (_i, []),
@@ -83,6 +88,20 @@ _SIGS = {
     "gbb_rope_append": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "gbb_paged_attention_workspace": (_sz, [_vp, _i, _i, _i, _i]),
     "gbb_paged_attention": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _i, _vp, _i, _f, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "gbb_rope_axes": (_i, [_vp, _l, _l, _vp, _l, _l, _i, _i, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "gbb_norm_rope": (_i, [_vp, _l, _l, _vp, _l, _l, _i, _i, _i, _i, _vp, _i, _f, _vp, _i, _vp, _vp, _i, _i, _i, _vp]),
+    "gbb_norm_rope_grad_workspace": (_sz, [_i, _i, _i]),
+    "gbb_norm_rope_grad": (_i, [_vp, _l, _l, _vp, _l, _l, _vp, _l, _l, _i, _i, _i, _i, _vp, _i, _f, _vp, _i, _vp, _vp,
+                                _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "gbb_norm_rope_append": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _vp, _i, _f, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp,
+                                  _vp]),
+    "gbb_paged_attention_options_workspace": (_sz, [_vp, _i, _i, _i, _i, _i]),
+    "gbb_paged_attention_options": (_i, [_vp, _vp, _l, _i, _i, _i, _vp, _i, _vp, _i, _f, _vp, _vp, _vp, _vp, _vp, _sz,
+                                         _vp]),
+    "gbb_paged_attention_tokens_workspace": (_sz, [_vp, _i, _i, _i, _i, _i, _i]),
+    "gbb_paged_attention_tokens": (_i, [_vp, _vp, _l, _i, _i, _i, _i, _vp, _vp, _i, _vp, _i, _f, _vp, _vp, _vp, _vp, _sz,
+                                        _vp]),
+    "gbb_cache_keep": (_i, [_vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
     "gbb_cache_evict_workspace": (_sz, [_vp, _i, _i, _i]),
     "gbb_cache_evict": (_i, [_vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
 }

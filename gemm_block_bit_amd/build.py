@@ -29,7 +29,7 @@ CXX_FLAGS = ["-O2", "-Wall", "-Wextra", "-fno-fast-math"] + COMMON
 
 # graph.cpp is host code on the HIP runtime (stream capture), so hipcc builds it too
 HIP_SOURCES = ["decode.hip", "decode64.hip", "prefill.hip", "w48.hip", "debug.hip", "noalloc.hip", "graph.cpp",
-               "rope.hip", "attention.hip", "evict.hip"]
+               "rope.hip", "attention.hip", "evict.hip", "norm_rope.hip", "tokens.hip", "keep.hip"]
 # per-source extra flags: the decode kernel reads its MFMA results with VALU
 # code right away, so it keeps them in VGPRs rather than accumulation
 # registers; its single-token kernel takes its arguments preloaded into

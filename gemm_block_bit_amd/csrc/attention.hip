@@ -51,69 +51,20 @@
 // / 8, fp16) 7 us, a chain of dependent steps: launch, page, K and V, scores,
 // the joins in the workgroup and over the runs.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
-#include "device.h"
-#include "internal.h"
+#include "attention_common.h"
 
 namespace gbb {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kShift = 14.f;   // see above: 2^14 < 65504
 constexpr int kMaxJoin = 64;     // runs that the last workgroup of a sequence joins itself
 constexpr int kMaxArrived = GBB_ATTENTION_COUNTERS / 4;   // counters of such sequences, at the workspace's start
 constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles x 4 waves x 32 slots
 
-
-// 16-bit element types of q, P and out.
-template <int DT> struct Half;
-template <> struct Half<GBB_F16> {
-  static constexpr int PARTS = 2;   // operands that P is given in
-  typedef _Float16 T;
-  typedef half8 V8;
-  static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
-  // two e4m3 bytes (the low or the high pair of w) as two elements, exactly
-  template <bool HI> static __device__ __forceinline__ uint32_t widen(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, HI));
-  }
-};
-template <> struct Half<GBB_BF16> {
-  static constexpr int PARTS = 3;
-  typedef __bf16 T;
-  typedef bf16x8 V8;
-  static __device__ __forceinline__ f32x4 mfma(const V8& a, const V8& b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  template <bool HI> static __device__ __forceinline__ uint32_t widen(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, HI));
-  }
-};
-
-// `bytes` of memory from `base`; loads past them give zeros.
-typedef __amdgpu_buffer_rsrc_t Span;
-__device__ __forceinline__ Span span(const void* base, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);   // raw bytes
-}
-// 16 bytes a lane, at byte `at` of s, to LDS at `to` (the same in all lanes)
-// plus 16 bytes times the lane.  The compiler does not wait for such a load
-// before LDS reads: loads_left<N>() waits until at most the N vector memory
-// operations issued last are under way (they complete in order) and
-// in_order() keeps the compiler from moving memory operations across it.
-__device__ __forceinline__ void to_lds(Span s, int at, uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(s, (__attribute__((address_space(3))) void*)to, 16, at, 0, 0, 0);
-}
-template <int N>
-__device__ __forceinline__ void loads_left() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
 // N pieces of 16 bytes from LDS, at the byte offsets at[] plus OFF, awaited.
 // Written out because the compiler, where it sees the reads, awaits every
@@ -165,35 +116,31 @@ struct SplitArgs {
   bool joins;       // no second launch
   int B, Hq, Hkv, G, qtiles, num_pages, pshift, max_pages, max_len, chunk, nsplit;
   float scale;      // scale * log2(e)
+  // OPT: a cap (times log2(e); 0: none), slopes [Hq] of a bias by distance or
+  // NULL, and how many of the newest slots take part (0: all)
+  float cap;
+  const float* slopes;
+  int window;
 };
 
 __device__ __forceinline__ int length_of(const SplitArgs& a, int b) {
   return max(0, min(a.lengths[b], a.max_len));
 }
-// 2^(x - m) with 2^(-inf - -inf) = 0, for joining partial results
-__device__ __forceinline__ float rescale(float x, float m) {
-  return x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x - m);
-}
+// The first slot that takes part, and where the runs of a sequence start: a
+// tile's 16 slots lie in one page.
+__device__ __forceinline__ int low_of(const SplitArgs& a, int len) { return a.window ? max(0, len - a.window) : 0; }
+__device__ __forceinline__ int base_of(int low) { return low & ~15; }
 
 // Waves of a workgroup: 4, or 8 (WIDE) for calls with so few runs that a
 // workgroup should have a CU to itself.
 constexpr int waves(bool wide) { return wide ? 8 : 4; }
 
-// Two floats at device scope.
-__device__ __forceinline__ void put(float* p, float x, float y) {
-  const uint64_t v = uint64_t(__builtin_bit_cast(uint32_t, y)) << 32 | __builtin_bit_cast(uint32_t, x);
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 get(const float* p) {
-  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__builtin_bit_cast(float, uint32_t(v)), __builtin_bit_cast(float, uint32_t(v >> 32)));
-}
-
 // weights_out = weights + sum over the kv head's query heads of
 // 2^(score - ref) inv, for the slots j ... j + 3, j + STEP ... below len (a
-// page holds whole groups of 4).
+// page holds whole groups of 4).  Slots below low have no score: what is read
+// in its place is not used.
 template <int STEP>
-__device__ __forceinline__ void add_weights(const SplitArgs& a, int b, int hk, int len, int j, const float* ref,
+__device__ __forceinline__ void add_weights(const SplitArgs& a, int b, int hk, int low, int len, int j, const float* ref,
                                             const float* inv) {
   for (; j < len; j += STEP) {
     const int p = a.block_table[size_t(b) * a.max_pages + (j >> a.pshift)];
@@ -219,11 +166,11 @@ __device__ __forceinline__ void add_weights(const SplitArgs& a, int b, int hk, i
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (there && j + k < len) a.weights_out[at + k] = old[k] + w[k];
+      if (there && j + k < len) a.weights_out[at + k] = j + k < low ? old[k] : old[k] + w[k];
   }
 }
 
-template <int DT, int CT, int D, bool WT, bool WIDE>
+template <int DT, int CT, int D, bool WT, bool WIDE, bool OPT>
 __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ? 3 : 4) void split_kernel(SplitArgs a) {
   typedef Half<DT> H;
   constexpr int NW = waves(WIDE), THREADS = 64 * NW;
@@ -246,7 +193,10 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   const int b = uniform(id % a.B), sp = uniform(id / a.B);
   const int rows = min(16, a.G - 16 * qt);           // query heads of this tile
   const int hq0 = hk * a.G + 16 * qt;
-  const int k0 = sp * a.chunk;
+  // (with a window the runs follow from the length)
+  const int low = OPT ? uniform(low_of(a, a.window ? length_of(a, b) : 0)) : 0;
+  const int base = OPT ? base_of(low) : 0;
+  const int k0 = base + sp * a.chunk;
   // lane 2 i + s: the page of 16-slot half s of this wave's tile i, looked up
   // before the length is known (the table has max_len's entries)
   const int key = k0 + 32 * (wave + NW * (lane >> 1)) + 16 * (lane & 1);
@@ -279,6 +229,8 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
     qf[kc] = __builtin_bit_cast(V8, qw[kc]);
   }
   const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
+  const float over = OPT && a.cap > 0.f ? 1.f / a.cap : 0.f;
+  const float slope = OPT && a.slopes ? a.slopes[hq0 + min(c, rows - 1)] * kLog2e : 0.f;
 
   // 32 rows of K a wave, and in the end the waves' outputs
   constexpr int OROW = D + 4, OWN = 16 * OROW * 4 > 32 * ROW ? 16 * OROW * 4 : 32 * ROW;
@@ -329,7 +281,9 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-          const int at = (4 * g4 + r) * ROW + u * 256 + c * VB;
+          int at = (4 * g4 + r) * ROW + u * 256 + c * VB;
+          // slots before the window read as zeros: at a weight of 0 a NaN there would reach the output
+          if (OPT && k0 + 32 * (wave + NW * i) + 16 * s + 4 * g4 + r < low) at = INT_MAX;
           if constexpr (VW == 4) {
             const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, 0);
 #pragma unroll
@@ -375,6 +329,16 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
         }
       }
       s[e] *= scale;
+      if constexpr (OPT) {
+        if (a.cap > 0.f) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[e][r] = capped<false>(s[e][r], over, a.cap);
+        }
+        if (a.slopes) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[e][r] -= slope * float(len - 1 - (key0 + 16 * e + 4 * g4 + r));
+        }
+      }
     }
     if constexpr (decltype(NEXT)::value) {
       in_order();
@@ -389,6 +353,12 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           s[e][r] = key0 + 16 * e + 4 * g4 + r >= k1 || (e ? p1 : p0) < 0 ? -INFINITY : s[e][r];
+    }
+    if (OPT && key0 < low) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[e][r] = key0 + 16 * e + 4 * g4 + r < low ? -INFINITY : s[e][r];
     }
     if constexpr (WT) {
       if (c < rows) {
@@ -501,7 +471,7 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       for (int r = 0; r < 4; ++r) so(wave, c, (t / EV) * 16 * EV + EV * (4 * g4 + r) + t % EV) = o[t][r];
   }
   __syncthreads();
-  const bool whole = len <= a.chunk;
+  const bool whole = len - base <= a.chunk;
   const float vs = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
   typedef typename H::T V2 __attribute__((ext_vector_type(2)));
   // out and lse from the joined sums of a head; with weights also what is
@@ -545,7 +515,7 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
     if (WT && a.joins) {
       loads_left<0>();   // the waves' scores are written
       __syncthreads();
-      add_weights<4 * THREADS>(a, b, hk, len, 4 * threadIdx.x, ref, inv);
+      add_weights<4 * THREADS>(a, b, hk, low, len, 4 * threadIdx.x, ref, inv);
     }
     return;
   }
@@ -566,7 +536,7 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
   unsigned* arrived = a.arrived + (b * a.Hkv + hk) * a.qtiles + qt;
   if (threadIdx.x == 0) count = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  const int ns = (len + a.chunk - 1) / a.chunk;
+  const int ns = (len - base + a.chunk - 1) / a.chunk;
   if (count != unsigned(ns - 1)) return;
   if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const size_t first = size_t(b * a.Hkv + hk) * a.nsplit * a.G + 16 * qt;   // row of run 0
@@ -665,9 +635,9 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
     fetch(0);
     const float2 first = first_runs(ml, a, lane);
     in_order();
-    const int len = length_of(a, b);
-    if (len <= a.chunk) return;
-    const int ns = (len + a.chunk - 1) / a.chunk;
+    const int len = length_of(a, b), span = len - base_of(low_of(a, len));
+    if (span <= a.chunk) return;
+    const int ns = (span + a.chunk - 1) / a.chunk;
     const float2 e = join_sums(first, ml, ns, a.G, lane);
     float acc = 0.f;
     for (int i0 = 0; i0 < ns; i0 += AHEAD) {
@@ -694,7 +664,7 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
     if (j0 >= len) return;
     // per query head: what is taken off a score, and one over the sum
     __shared__ float ref[kMaxGroup], inv[kMaxGroup];
-    const int ns = (len + a.chunk - 1) / a.chunk;
+    const int low = low_of(a, len), ns = (len - base_of(low) + a.chunk - 1) / a.chunk;
     for (int q = wave; q < a.G; q += 4) {
       const float2 e = join_sums(q == wave ? first : first_runs(ml + q, a, lane), ml + q, ns, a.G, lane);
       if (lane == 0) {
@@ -703,21 +673,24 @@ __global__ __launch_bounds__(256) void join_kernel(SplitArgs a, int joining) {
       }
     }
     __syncthreads();
-    add_weights<kJoinSlots>(a, b, hk, min(len, j0 + kJoinSlots), j0 + 4 * threadIdx.x, ref, inv);
+    add_weights<kJoinSlots>(a, b, hk, low, min(len, j0 + kJoinSlots), j0 + 4 * threadIdx.x, ref, inv);
   }
 }
 
-template <int DT, int CT, int D, bool WT>
+template <int DT, int CT, int D, bool WT, bool OPT>
 void run_split(const SplitArgs& a, bool wide, hipStream_t s) {
   const unsigned grid = unsigned(a.B) * a.Hkv * a.qtiles * a.nsplit;
-  if (wide) start((split_kernel<DT, CT, D, WT, true>), dim3(grid), dim3(64 * waves(true)), s, a);
-  else start((split_kernel<DT, CT, D, WT, false>), dim3(grid), dim3(256), s, a);
+  if (wide) start((split_kernel<DT, CT, D, WT, true, OPT>), dim3(grid), dim3(64 * waves(true)), s, a);
+  else start((split_kernel<DT, CT, D, WT, false, OPT>), dim3(grid), dim3(256), s, a);
 }
 
 template <int DT, int CT, int D>
 void run(const SplitArgs& a, bool wide, bool wt, hipStream_t s) {
-  if (wt) run_split<DT, CT, D, true>(a, wide, s);
-  else run_split<DT, CT, D, false>(a, wide, s);
+  const bool opt = a.cap > 0.f || a.slopes || a.window;
+  if (wt && opt) run_split<DT, CT, D, true, true>(a, wide, s);
+  else if (wt) run_split<DT, CT, D, true, false>(a, wide, s);
+  else if (opt) run_split<DT, CT, D, false, true>(a, wide, s);
+  else run_split<DT, CT, D, false, false>(a, wide, s);
   if (a.joins) return;
   const int heads = a.nsplit == 1 ? 0 : (a.B * a.Hq + 256 / D - 1) / (256 / D);
   constexpr bool F8 = CT == GBB_E4M3;
@@ -739,8 +712,10 @@ size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights) {
+AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int most, bool with_weights, int window) {
   AttendPlan p;
+  // slots of a sequence that take part, from the one that its runs start at
+  const int max_len = window ? int(std::min<int64_t>(most, int64_t(window) + 15)) : most;
   const int G = Hq / c.kv_heads;
   p.qtiles = (G + 15) / 16;
   const int64_t pairs = int64_t(B) * c.kv_heads * p.qtiles;
@@ -786,7 +761,7 @@ AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, boo
   p.chunk = chunk;
   p.nsplit = std::max(1, (max_len + chunk - 1) / chunk);
   const size_t rows = size_t(B) * Hq * p.nsplit;
-  p.score_stride = (size_t(max_len) + 31) & ~size_t(31);
+  p.score_stride = (size_t(most) + (window ? 47 : 31)) & ~size_t(31);   // (a window's tiles may start 16 slots off)
   const bool parts = p.nsplit > 1;
   // One launch where the last workgroup of a sequence can join its runs.  With
   // weights, where there are none to join and a workgroup has all query heads
@@ -833,6 +808,9 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& x, const AttendPla
   a.chunk = p.chunk;
   a.nsplit = p.nsplit;
   a.scale = x.scale * kLog2e;
+  a.cap = x.softcap * kLog2e;
+  a.slopes = x.slopes;
+  a.window = x.window;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const bool wt = x.weights_out != nullptr;
   if (x.dtype == GBB_F16) {

@@ -129,6 +129,53 @@ struct AppendArgs {
 };
 int launch_append(const gbb_paged_cache& c, const AppendArgs& a, void* stream);
 
+// Rotations of one to four axes: pair i turns by positions[a][T], a the first
+// axis with i < end[a].
+struct Rotation {
+  const int32_t* positions;
+  const float* table;
+  int n_pos, rot, layout, axes;
+  int end[3];
+};
+struct NormRopeArgs {
+  const void* x;
+  void* y;
+  int64_t x_token, x_head, y_token, y_head;
+  const void* weight;   // NULL: ones
+  Rotation r;
+  int T, H, D, dtype;
+  float eps;
+  bool norm, transpose, wide_weight;   // wide: fp32, else of the dtype
+};
+int launch_norm_rope(const NormRopeArgs& a, void* stream);
+struct NormRopeGradArgs {
+  const void* x;
+  const void* dy;
+  void* dx;            // or NULL
+  int64_t x_token, x_head, dy_token, dy_head, dx_token, dx_head;
+  const void* weight;
+  float* partial;      // [norm_rope_grad_rows][D], or NULL: no gradient of the weight
+  Rotation r;
+  int T, H, D, dtype;
+  float eps;
+  bool wide_weight;
+};
+int norm_rope_grad_rows(int T, int H);
+int launch_norm_rope_grad(const NormRopeGradArgs& a, void* dweight, void* stream);
+struct NormAppendArgs {
+  const void* qkv;
+  void* q;
+  int64_t token_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* slots;
+  Rotation r;
+  int T, Hq, dtype;
+  float eps;
+  bool norm, wide_weight;
+};
+int launch_norm_append(const gbb_paged_cache& c, const NormAppendArgs& a, void* stream);
+
 // The split of gbb_paged_attention: every sequence's slots in runs of `chunk`
 // (nsplit of them up to max_len), one workgroup each.
 constexpr int kMaxGroup = 128;   // query heads per kv head
@@ -139,7 +186,7 @@ struct AttendPlan {
   size_t ml_off, o_off, s_off, ws_bytes;   // workspace sections
   size_t score_stride;                     // scores per query head (with weights)
 };
-AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights);
+AttendPlan attend_plan(const gbb_paged_cache& c, int B, int Hq, int max_len, bool with_weights, int window);
 struct AttendArgs {
   const void* q;
   int64_t q_token;
@@ -151,8 +198,49 @@ struct AttendArgs {
   char* ws;
   int B, Hq, max_pages, max_len, dtype;
   float scale;
+  float softcap;        // 0: none
+  const float* slopes;  // NULL: none
+  int window;           // 0: none
 };
 int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPlan& p, void* stream);
+
+// Attention of several new tokens a sequence.  A workgroup takes `rows` rows
+// of a sequence and kv head (a row is a token and a query head) and a run of
+// `chunk` slots.
+struct TokensPlan {
+  int waves, rows, tiles;   // waves of 32 rows each a workgroup; row tiles of all sequences, at most
+  int chunk, nsplit;
+  size_t ml_off, o_off, ws_bytes;
+};
+struct TokensArgs {
+  const void* q;
+  int64_t q_token;
+  const int32_t* starts;
+  const int32_t* block_table;
+  const int32_t* lengths;
+  const int32_t* first;
+  const int32_t* prefix;
+  const uint32_t* tree;
+  void* out;
+  float* lse;
+  char* ws;
+  int T, B, Hq, max_pages, max_len, dtype, tree_words, window;
+  float scale, softcap;
+  const float* slopes;
+};
+TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_len, int window, int tree_words);
+int launch_tokens(const gbb_paged_cache& c, const TokensArgs& a, const TokensPlan& p, void* stream);
+
+struct KeepArgs {
+  const int32_t* block_table;
+  const int32_t* lengths;
+  const int32_t* drafted;
+  const int32_t* kept;
+  const int32_t* counts;
+  int32_t* lengths_out;
+  int B, max_pages, max_kept;
+};
+int launch_keep(const gbb_paged_cache& c, const KeepArgs& a, void* stream);
 
 constexpr int kMaxEvictLen = 512 * 4096;   // slots of a sequence that gbb_cache_evict takes
 struct EvictPlan {

@@ -1,0 +1,704 @@
+// Attention of several new tokens per sequence over a paged cache
+// (gbb_paged_attention_tokens): prompts, chunks of them, and trees of drafted
+// tokens, with capped or biased scores and masks.
+//
+// A row is a (token, query head) of one kv head, tokens outermost, so that the
+// G query heads of a kv head and neighbouring tokens share K and V.  A
+// workgroup takes 32 rows a wave and a run of `chunk` slots, one pass with the
+// running maximum; its waves share tiles of BN slots of K and V in LDS:
+//  - S^T = K q^T: the A operand of a 32x32x16 MFMA is 32 slots x 16 elements of
+//    K, a slot a lane; the result has lane c + 32 h holding row c, slots 8 (i /
+//    4) + 4 h + i % 4 in register i.
+//  - O^T = V^T P: which slot a k index stands for is free as long as both
+//    operands agree, so P's registers are the B operand as they are, and the A
+//    operand needs, a lane, one element of V at four slots in a row, twice:
+//    what a transposing LDS read gives (16 lanes read 4 slots of 16 elements,
+//    each gets an element's 4 slots).
+//  - a row's maximum and sum lie in the two lanes that share it: one lane swap
+//    a tile for the maximum, one at the end for the sum.
+//  - tiles go from memory to registers while the tile before is worked on, and
+//    from there to LDS; pieces of 16 bytes are permuted within a row so that
+//    lanes that read together hit different banks.  Memory past a row's range
+//    reads as zeros, whatever it holds.
+//  - a tile that all rows of a wave see whole takes no masks, one that none
+//    sees is passed over.
+//
+// With n rows of tokens the work is 4 D operations a visible slot and row
+// against 2 D elements of K and V a slot: matrix bound from some 100 rows on,
+// by the bytes of the cache below that.  Beside the products every score costs
+// an exponential, a maximum, a sum and a conversion in the vector pipes, which
+// take about as long as its share of the products at D = 128.
+//
+// P is rounded to 16 bits for the matrix cores, once in workgroups of four
+// waves, where the products bound the call (a second operand for what the
+// rounding drops would take half as long again), and the sum that divides the
+// output is that of the rounded P: an output is off by at most half a step of
+// its type relative to sum p |v|, beside its own rounding.  With fewer waves the
+// cache's bytes bound the call, and P is given in two operands (22 bits in fp16,
+// 16 in bf16).
+//
+// Where there are few row tiles the slots are split over workgroups; partial
+// results (maximum, sum, unnormalised output, fp32) go to the workspace, and
+// the last workgroup of a row tile joins them in the order of the runs.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "attention_common.h"
+
+namespace gbb {
+
+namespace {
+
+constexpr int kMaxJoin = 64;     // runs of a row tile
+constexpr int kMaxArrived = GBB_ATTENTION_COUNTERS / 4;   // counters of row tiles with several runs
+// exp2 is taken this many powers above the running maximum's 0, so that fp16
+// keeps small probabilities out of its subnormals: 2^14 < 65504
+constexpr float kShift = 14.f;
+
+typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
+
+struct Args {
+  const void* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* starts;
+  const int32_t* block_table;
+  const int32_t* lengths;
+  const int32_t* first;
+  const int32_t* prefix;
+  const uint32_t* tree;
+  const float* slopes;
+  void* out;
+  float* lse;
+  unsigned* arrived;   // [row tile][Hkv] runs that are done, 0 between calls
+  float2* ml;          // [row tile][Hkv][nsplit][rows] maximum (log2 domain) and sum
+  float* o;            // [row tile][Hkv][nsplit][rows][D]
+  int64_t q_token;
+  int T, B, Hq, Hkv, G, num_pages, pshift, max_pages, max_len, chunk, nsplit, tiles, tree_words, window;
+  float scale, cap;    // times log2(e)
+  bool negative;       // the scale's sign, taken into q
+};
+
+// Slots per tile: K and V of it take 16 KiB of LDS each at D = 128 and four waves.
+constexpr int tile_slots(int D, int NW) { return D == 256 || NW < 4 ? 32 : 64; }
+
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int i = 1; i < 32; i *= 2) x = min(x, __shfl_xor(x, i));
+  return x;
+}
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int i = 1; i < 32; i *= 2) x = max(x, __shfl_xor(x, i));
+  return x;
+}
+// Both lanes' values of a row.
+__device__ __forceinline__ float2 both(float x) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];   // (a bit_cast of r[1] itself would take r[0])
+  return make_float2(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+}
+__device__ __forceinline__ float row_max(float x) {
+  const float2 r = both(x);
+  return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float row_sum(float x) {
+  const float2 r = both(x);
+  return r.x + r.y;
+}
+
+template <int DT, int CT, int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
+  typedef Half<DT> H;
+  typedef typename H::T T;
+  typedef typename H::V8 V8;
+  constexpr bool F8 = CT == GBB_E4M3;
+  constexpr int PARTS = NW == 4 ? 1 : 2;
+  constexpr int THREADS = 64 * NW, ROWS = 32 * NW, BN = tile_slots(D, NW);
+  constexpr int ROW = 2 * D;                  // bytes of a slot in LDS
+  constexpr int GROW = F8 ? D : 2 * D;        // and in memory
+  constexpr int LPR = GROW / 16;              // lanes that load a slot
+  constexpr int RPI = 64 / LPR;               // slots a wave's load takes
+  constexpr int NL = BN / (NW * RPI);         // loads a lane of a tile of K or V
+  constexpr int PIECES = ROW / 16;
+  constexpr int KC = D / 16, NT = D / 32, NE = BN / 32;
+  constexpr int KA = KC < 8 ? KC : 8, VA = NT < 4 ? NT : 4;   // distinct permuted addresses; beyond, 256 bytes on
+  static_assert(NL >= 1 && RPI <= 16, "a load stays within 16 slots");
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int c = lane & 31, h = lane >> 5;
+
+  int id = blockIdx.x;
+  const int hk = uniform(id % a.Hkv);
+  id /= a.Hkv;
+  const int w = uniform(id % a.tiles), sp = uniform(id / a.tiles);
+  // the sequence whose row tile number w of the call is, 64 sequences at a time
+  const auto start_of = [&](int b) { return max(0, min(a.starts[b], a.T)); };
+  int b = -1, tile = 0, before = 0, ntiles = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    int n = 0;
+    if (b0 + lane < a.B) n = max(0, start_of(b0 + lane + 1) - start_of(b0 + lane));
+    const int mine = (n * a.G + ROWS - 1) / ROWS;
+    int sum = mine;
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+      const int x = __shfl_up(sum, i);
+      if (lane >= i) sum += x;
+    }
+    const uint64_t past = __ballot(w < before + sum);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      b = b0 + at;
+      ntiles = __builtin_amdgcn_readlane(mine, at);
+      tile = w - (before + __builtin_amdgcn_readlane(sum, at) - ntiles);
+      break;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  if (b < 0) return;
+  b = uniform(b);
+  const int t0 = uniform(start_of(b)), n = uniform(start_of(b + 1)) - t0;
+  const int len = uniform(max(0, min(a.lengths[b], a.max_len)));
+  const int ctx = len - n;                     // may be negative
+  const int rows_all = n * a.G;
+  const int r0 = uniform(ntiles - 1 - tile) * ROWS;   // the last tokens first: they see most
+  const int row = r0 + 32 * wave + c;
+  const bool real = row < rows_all;
+  const int token = real ? row / a.G : 0, hq = hk * a.G + (real ? row - token * a.G : 0);
+  const size_t t = size_t(t0 + token);
+
+  // What a row sees: slots [lo, hi), and with a tree those of [ctx, len) whose
+  // bit is set, from `first` on and less than `window` away.  place: where
+  // distances to slots before the new ones count from.
+  int lo = 0, hi, place = ctx + token, first = 0, drafted = 0;
+  const uint32_t* words = nullptr;
+  if (a.first) first = max(0, a.first[t]);
+  if (a.tree) {
+    words = a.tree + t * a.tree_words;
+    for (int i = 0; i < a.tree_words; ++i) {
+      const int left = n - 32 * i;
+      if (left > 0) drafted += __popc(left < 32 ? words[i] & ((1u << left) - 1) : words[i]);
+    }
+    place = ctx + drafted - 1;
+    hi = ctx;
+  } else {
+    hi = place + 1;
+    if (a.prefix) hi = max(hi, a.prefix[b]);
+    if (a.window) hi = int(min(int64_t(hi), int64_t(place) + a.window));
+    hi = min(hi, len);
+  }
+  if (a.window) lo = int(max(int64_t(0), int64_t(place) - a.window + 1));
+  lo = max(lo, first);
+  if (!real) lo = INT_MAX, hi = 0;
+  const int top = a.tree && real ? ctx + min(n, 32 * a.tree_words) : hi;         // one past the last slot it may see
+  const int bottom = a.tree && real ? max(first, min(lo, max(0, ctx))) : lo;     // and the first
+  const bool some = top > bottom;
+  const int lo_wave = uniform(wave_min(some ? bottom : INT_MAX)), hi_wave = uniform(wave_max(some ? top : 0));
+  const int lo_all = uniform(wave_max(real ? lo : 0)), hi_all = uniform(wave_min(real ? hi : INT_MAX));   // all its rows see these
+  __shared__ int range[4 * NW];
+  if (lane == 0) {
+    range[4 * wave] = lo_wave;
+    range[4 * wave + 1] = hi_wave;
+    range[4 * wave + 2] = lo_all;
+    range[4 * wave + 3] = hi_all;
+  }
+  __syncthreads();
+  int k_low = range[0], k_high = range[1], same_low = range[2], same_high = range[3];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) {
+    k_low = min(k_low, range[4 * i]);
+    k_high = max(k_high, range[4 * i + 1]);
+    same_low = max(same_low, range[4 * i + 2]);
+    same_high = min(same_high, range[4 * i + 3]);
+  }
+  k_low = uniform(k_low);
+  k_high = uniform(k_high);
+  same_low = uniform(same_low);                // all rows of the workgroup see the slots from
+  same_high = uniform(same_high);              // same_low up to same_high
+  const size_t head = t * a.Hq + hq;
+  if (k_low >= k_high) {                       // no row sees a slot
+    if (sp == 0 && real) {
+      for (int d = 8 * h; d < D; d += 16) st16(static_cast<T*>(a.out) + head * D + d, u32x4{0, 0, 0, 0});
+      if (a.lse && h == 0) a.lse[head] = -INFINITY;
+    }
+    return;
+  }
+  k_low &= ~15;
+  const int k0 = k_low + sp * a.chunk;
+  if (k0 >= k_high) return;
+  const int k1 = k0 + min(k_high - k0, a.chunk);
+  const int nt = (k1 - k0 + BN - 1) / BN;
+
+  // q, the B operand: row c, elements 16 kc + 8 h ...
+  V8 qf[KC];
+#pragma unroll
+  for (int kc = 0; kc < KC; ++kc) {
+    u32x4 x = {0, 0, 0, 0};
+    if (real) x = ld16(static_cast<const uint16_t*>(a.q) + t * a.q_token + size_t(hq) * D + 16 * kc + 8 * h);
+    if (a.negative) x ^= 0x80008000u;
+    qf[kc] = __builtin_bit_cast(V8, x);
+  }
+  const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
+  const float over = a.cap > 0.f ? 1.f / a.cap : 0.f;
+  const float slope = a.slopes ? a.slopes[hq] * kLog2e : 0.f;
+  const bool shaped = a.cap > 0.f || a.slopes;
+
+  __shared__ __align__(16) uint8_t ks[BN * ROW];
+  __shared__ __align__(16) uint8_t vs[BN * ROW];
+  // Piece p (16 bytes) of slot r lies at p ^ swizzle(r): a slot a lane for K (8
+  // lanes together hit 8 pieces), 4 slots of two pieces for V.
+  constexpr int KS = PIECES < 16 ? PIECES - 1 : 15, VS = PIECES < 16 ? PIECES / 2 - 1 : 7;
+  const auto k_swizzle = [](int r) { return r & KS; };
+  const auto v_swizzle = [](int r) { return 2 * (r & VS); };
+
+  // Pages of 64 groups of 16 slots from `group0` on, a group a lane.
+  const auto pages_from = [&](int group) {
+    const int key = min((group + lane) << 4, a.max_len - 1);
+    const int p = a.block_table[size_t(b) * a.max_pages + (key >> a.pshift)];
+    return ((group + lane) << 4) < k1 && unsigned(p) < unsigned(a.num_pages) ? p : -1;
+  };
+  const int pmask = (1 << a.pshift) - 1;
+  const size_t page_bytes = (size_t(1) << a.pshift) * GROW;
+  int pages = pages_from(k0 >> 4);
+  constexpr int TPP = 1024 / BN;               // tiles that `pages` covers
+  u32x4 kr[NL], vr[NL];
+  const auto fetch = [&](u32x4 (&x)[NL], const uint8_t* base, int i) {
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      const int r = uniform((j * NW + wave) * RPI);          // first slot of the load within the tile
+      const int group = (r >> 4) + (i % TPP) * (BN / 16);
+      const int p = __builtin_amdgcn_readlane(pages, group);
+      const int key = k0 + i * BN + (r & ~15);
+      const size_t off = (size_t(max(p, 0)) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * GROW;
+      const Span rows = span(base + off, uniform(p < 0 ? 0 : max(0, min(k1 - key, 16)) * GROW));
+      x[j] = __builtin_amdgcn_raw_buffer_load_b128(rows, (r & 15) * GROW + lane * 16, 0, 0);
+    }
+  };
+  const auto keep = [&](const u32x4 (&x)[NL], uint8_t* to, auto swizzle, auto change) {
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      const int r = (j * NW + wave) * RPI + lane / LPR, p = lane % LPR;
+      if constexpr (F8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w0 = x[j][2 * e], w1 = x[j][2 * e + 1];
+          st16(to + r * ROW + ((2 * p + e) ^ swizzle(r)) * 16,
+               change(u32x4{H::template widen<false>(w0), H::template widen<true>(w0),
+                            H::template widen<false>(w1), H::template widen<true>(w1)}));
+        }
+      } else {
+        st16(to + r * ROW + (p ^ swizzle(r)) * 16, change(x[j]));
+      }
+    }
+  };
+  const auto as_is = [](const u32x4& x) { return x; };
+  // A slot that some rows see and some do not may hold infinities or NaN: with
+  // a weight of 0 they would reach the rows that do not see it.  So they are
+  // left out of the product, and what they do to the rows that see them is found
+  // by products with 1 in the place of infinities of each sign and of NaN.
+  constexpr uint32_t EXP = DT == GBB_F16 ? 0x7c00u : 0x7f80u, ONE = DT == GBB_F16 ? 0x3c00u : 0x3f80u;
+  const auto elements = [](u32x4 x, auto f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f(x[i] & 0xffffu) | f(x[i] >> 16) << 16;
+    return x;
+  };
+  const auto sign_of = [&](int negative) {     // 1 where an element is an infinity of that sign or NaN
+    return [=](const u32x4& x) {
+      return elements(x, [=](uint32_t e) {
+        return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
+      });
+    };
+  };
+
+  // this lane's addresses in LDS: K's slot c, V's slots 4 h + (lane % 16) / 4
+  int k_at[KA], v_at[VA];
+#pragma unroll
+  for (int i = 0; i < KA; ++i) k_at[i] = c * ROW + ((2 * i + h) ^ k_swizzle(c)) * 16;
+#pragma unroll
+  for (int i = 0; i < VA; ++i) {
+    const int r = 4 * h + ((lane & 15) >> 2);
+    v_at[i] = r * ROW + ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(r)) * 16 + 8 * (lane & 1);
+  }
+
+  f32x16 o[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  float m = -INFINITY, l = 0.f;
+
+  fetch(kr, a.k, 0);
+  fetch(vr, a.v, 0);
+  for (int i = 0; i < nt; ++i) {
+    const int key0 = k0 + i * BN;
+    const int pages_now = pages;               // of this tile
+    keep(kr, ks, k_swizzle, as_is);
+    __syncthreads();
+    if (i + 1 < nt) {
+      if ((i + 1) % TPP == 0) pages = pages_from((k0 + (i + 1) * BN) >> 4);
+      fetch(kr, a.k, i + 1);
+    }
+    const bool works = key0 < hi_wave && key0 + BN > lo_wave;
+    V8 part[PARTS][BN / 16];
+    if (works) {
+      f32x16 s[NE];
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(ks + k_at[kc % KA] + (kc / KA) * 256 + e * 32 * ROW);
+          s[e] = H::mfma32(__builtin_bit_cast(V8, x), qf[kc], s[e]);
+        }
+      }
+      // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
+      const int key = key0 + 4 * h;
+      const auto slot = [](int e, int r) { return 32 * e + 8 * (r / 4) + r % 4; };
+      float unit = scale;
+      bool holes = false;                      // a page that is not there
+#pragma unroll
+      for (int g = 0; g < BN / 16; ++g)
+        holes |= key0 + 16 * g < k1 && __builtin_amdgcn_readlane(pages_now, (i % TPP) * (BN / 16) + g) < 0;
+      const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
+      uint32_t bits[NE];                       // of drafted slots, as the lane's registers have them: bit 8 (r / 4) + r % 4
+      const bool branches = a.tree && key0 + BN > ctx;
+      int beyond = 0;                          // visible drafted slots behind the tile
+      if (branches) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          const int at = key0 + 32 * e - ctx;  // the drafted slot of bit 0
+          uint64_t x = 0;
+          const int i0 = at >> 5;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u, left = n - 32 * i;
+            if (real && i >= 0 && i < a.tree_words && left > 0)
+              x |= uint64_t(left < 32 ? words[i] & ((1u << left) - 1) : words[i]) << (32 * u);
+          }
+          bits[e] = uint32_t(x >> (at & 31));
+        }
+        int upto = 0;
+        if (real) {
+          const int end = key0 + BN - ctx;     // above 0
+          for (int i = 0; i < a.tree_words && 32 * i < end; ++i) {
+            const int left = min(n, end) - 32 * i;
+            if (left > 0) upto += __popc(left < 32 ? words[i] & ((1u << left) - 1) : words[i]);
+          }
+        }
+        beyond = drafted - upto;
+      }
+      if (shaped) {
+        unit = 1.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s[e] *= scale;
+        if (a.cap > kShortCap * kLog2e) {
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[e][r] = capped<false>(s[e][r], over, a.cap);
+        } else if (a.cap > 0.f) {
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[e][r] = capped<true>(s[e][r], over, a.cap);
+        }
+        if (a.slopes) {
+          const float from = float(place - key);
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              float far = fabsf(from - float(slot(e, r)));
+              if (branches && key + slot(e, r) >= ctx) {
+                const int at = slot(0, r) + 4 * h;
+                int after = __popc(at < 31 ? bits[e] >> (at + 1) : 0u) + beyond;
+#pragma unroll
+                for (int f = e + 1; f < NE; ++f) after += __popc(bits[f]);
+                far = float(after);
+              }
+              s[e][r] = __builtin_fmaf(-slope, far, s[e][r]);
+            }
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int j = key + slot(e, r);
+            bool seen = j >= lo && j < hi && j < k1;
+            if (branches && j >= ctx) {
+              const int at = slot(0, r) + 4 * h;
+              seen = j < k1 && j >= first && (bits[e] >> at & 1u);
+              if (a.window) {
+                int after = __popc(at < 31 ? bits[e] >> (at + 1) : 0u) + beyond;
+#pragma unroll
+                for (int f = e + 1; f < NE; ++f) after += __popc(bits[f]);
+                seen = seen && after < a.window;
+              }
+            }
+            if (holes && __builtin_amdgcn_readlane(pages_now, (i % TPP) * (BN / 16) + 2 * e + r / 8) < 0) seen = false;
+            s[e][r] = seen ? s[e][r] : -INFINITY;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[e][r]);
+      mx = row_max(mx) * unit;
+      if (__any(mx > m)) {
+        const float mn = fmaxf(m, mx), f = rescale(m, mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j] *= f;
+      }
+      const float ref = m == -INFINITY ? 0.f : m - kShift;
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], unit, -ref));
+          l += p;
+#pragma unroll
+          for (int x = 0; x < PARTS; ++x) {
+            const T y = T(p);
+            part[x][2 * e + r / 8][r % 8] = y;
+            p -= float(y);   // exact
+          }
+        }
+    }
+    // V's elements 32 j ... of the slots 16 s ..., as the A operand
+    const auto v_piece = [&](int j, int s) {
+      typedef __attribute__((address_space(3))) i16x4* L;
+      const uint8_t* at = vs + v_at[j % VA] + (j / VA) * 256 + s * 16 * ROW;
+      const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
+      const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + 8 * ROW));
+      return __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    if (key0 < same_low || min(key0 + BN, k1) > same_high) {
+      int odd = 0;
+      keep(vr, vs, v_swizzle, [&](const u32x4& x) {
+        return elements(x, [&](uint32_t e) {
+          const bool bad = (e & EXP) == EXP;
+          odd |= bad;
+          return bad ? 0u : e;
+        });
+      });
+      if (__syncthreads_or(odd)) {
+#pragma unroll 1
+        for (int negative = 0; negative < 2; ++negative) {
+          __syncthreads();
+          keep(vr, vs, v_swizzle, sign_of(negative));
+          __syncthreads();
+          if (works)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              f32x16 hit = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+              for (int s = 0; s < BN / 16; ++s) hit = H::mfma32(v_piece(j, s), part[0][s], hit);
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (hit[r] > 0.f) o[j][r] += negative ? -INFINITY : INFINITY;
+            }
+        }
+        __syncthreads();
+        keep(vr, vs, v_swizzle, [&](const u32x4& x) {
+          return elements(x, [&](uint32_t e) { return (e & EXP) == EXP ? 0u : e; });
+        });
+        __syncthreads();
+      }
+    } else {
+      keep(vr, vs, v_swizzle, as_is);
+      __syncthreads();
+    }
+    if (i + 1 < nt) fetch(vr, a.v, i + 1);
+    if (works) {
+#pragma unroll
+      for (int s = 0; s < BN / 16; ++s)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const V8 x = v_piece(j, s);
+#pragma unroll
+          for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][s], o[j]);
+        }
+    }
+  }
+
+  l = row_sum(l);
+  const float vscale = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+  const int ns = (k_high - k_low - 1) / a.chunk + 1;
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  if (ns == 1) {
+    if (!real) return;
+    const float f = l == 0.f ? 0.f : vscale / l;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        V4 x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = T(l == 0.f ? 0.f : o[j][r + u] * f);
+        *reinterpret_cast<V4*>(static_cast<T*>(a.out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = x;
+      }
+    if (a.lse && h == 0) a.lse[head] = l == 0.f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
+    return;
+  }
+
+  // Partial results at device scope, awaited before the count (as in
+  // attention.hip, where the reasons stand); the last workgroup joins.
+  const size_t slot0 = (size_t(w) * a.Hkv + hk) * a.nsplit;
+  const size_t mine = (slot0 + sp) * ROWS + 32 * wave + c;
+  if (real) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) put(a.o + mine * D + 32 * j + 8 * (r / 4) + 4 * h + r % 4, o[j][r], o[j][r + 1]);
+    if (h == 0) put(reinterpret_cast<float*>(a.ml + mine), m, l);
+  }
+  __shared__ unsigned count;
+  loads_left<0>();
+  __syncthreads();
+  unsigned* arrived = a.arrived + w * a.Hkv + hk;
+  if (threadIdx.x == 0) count = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (count != unsigned(ns - 1)) return;
+  if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int valid = min(ROWS, rows_all - r0);
+  const float* po = a.o + slot0 * ROWS * D;
+  const float* pm = reinterpret_cast<const float*>(a.ml + slot0 * ROWS);
+  for (int i = threadIdx.x; i < valid * (D / 2); i += THREADS) {
+    const int q = i / (D / 2), d = 2 * (i % (D / 2));
+    float mm = -INFINITY, ll = 0.f, o0 = 0.f, o1 = 0.f;
+    for (int s0 = 0; s0 < ns; s0 += 8) {
+      float2 x[8], e[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const size_t at = size_t(min(s0 + u, ns - 1)) * ROWS + q;
+        x[u] = get(po + at * D + d);
+        e[u] = get(pm + 2 * at);
+      }
+      float top = mm;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) top = fmaxf(top, e[u].x);
+      const float f = rescale(mm, top);
+      mm = top;
+      ll *= f;
+      o0 *= f;
+      o1 *= f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < ns) {
+          const float g = rescale(e[u].x, mm);
+          ll += g * e[u].y;
+          o0 += g * x[u].x;
+          o1 += g * x[u].y;
+        }
+    }
+    const int r = r0 + q, tok = r / a.G;
+    const size_t to = size_t(t0 + tok) * a.Hq + hk * a.G + (r - tok * a.G);
+    typedef T V2 __attribute__((ext_vector_type(2)));
+    const float f = ll == 0.f ? 0.f : vscale / ll;
+    *reinterpret_cast<V2*>(static_cast<T*>(a.out) + to * D + d) = V2{T(ll == 0.f ? 0.f : o0 * f), T(ll == 0.f ? 0.f : o1 * f)};
+    if (d == 0 && a.lse) a.lse[to] = ll == 0.f ? -INFINITY : (mm - kShift + __builtin_amdgcn_logf(ll)) * kLn2;
+  }
+}
+
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int DT, int CT, int D>
+void run(const Args& a, int waves, unsigned grid, hipStream_t s) {
+  if (waves == 4) start((tokens_kernel<DT, CT, D, 4>), dim3(grid), dim3(256), s, a);
+  else if (waves == 2) start((tokens_kernel<DT, CT, D, 2>), dim3(grid), dim3(128), s, a);
+  else start((tokens_kernel<DT, CT, D, 1>), dim3(grid), dim3(64), s, a);
+}
+template <int DT, int CT>
+void run_dim(const Args& a, int D, int waves, unsigned grid, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, waves, grid, s);
+  else if (D == 128) run<DT, CT, 128>(a, waves, grid, s);
+  else run<DT, CT, 256>(a, waves, grid, s);
+}
+
+}  // namespace
+
+TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_len, int window, int tree_words) {
+  TokensPlan p;
+  const int G = Hq / c.kv_heads;
+  const int64_t rows = int64_t(T) * G;         // of a kv head
+  p.waves = rows <= int64_t(32) * B ? 1 : rows <= int64_t(64) * B ? 2 : 4;
+  p.rows = 32 * p.waves;
+  p.tiles = int(std::min<int64_t>(rows / p.rows + B, INT_MAX));
+  // slots from the first to the last that a row tile may see
+  int64_t most = max_len;
+  if (window && tree_words) most = std::min<int64_t>(most, int64_t(window) + 32 * int64_t(tree_words) + 15);
+  else if (window) most = std::min<int64_t>(most, 2 * int64_t(window) + p.rows + 15);
+  else most = most + 15;
+  const int64_t cus = device_compute_units(), groups = int64_t(p.tiles) * c.kv_heads;
+  int64_t chunk = (most + 63) & ~int64_t(63);
+  if (groups < 2 * cus && groups <= kMaxArrived) {
+    const int64_t want = std::min<int64_t>(kMaxJoin, (2 * cus + groups - 1) / groups);
+    chunk = std::max<int64_t>(256, ((most + want - 1) / want + 63) & ~int64_t(63));
+  }
+  p.chunk = int(std::min<int64_t>(chunk, INT_MAX & ~63));
+  p.nsplit = int(std::max<int64_t>(1, (most + p.chunk - 1) / p.chunk));
+  const size_t parts = p.nsplit > 1 ? size_t(groups) * p.nsplit * p.rows : 0;
+  p.ml_off = parts ? GBB_ATTENTION_COUNTERS : 0;
+  p.o_off = p.ml_off + up(parts * sizeof(float2));
+  p.ws_bytes = p.o_off + up(parts * c.head_dim * sizeof(float));
+  return p;
+}
+
+int launch_tokens(const gbb_paged_cache& c, const TokensArgs& x, const TokensPlan& p, void* stream) {
+  Args a;
+  a.q = x.q;
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.starts = x.starts;
+  a.block_table = x.block_table;
+  a.lengths = x.lengths;
+  a.first = x.first;
+  a.prefix = x.prefix;
+  a.tree = x.tree;
+  a.slopes = x.slopes;
+  a.out = x.out;
+  a.lse = x.lse;
+  a.arrived = reinterpret_cast<unsigned*>(x.ws);
+  a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
+  a.o = reinterpret_cast<float*>(x.ws + p.o_off);
+  a.q_token = x.q_token;
+  a.T = x.T;
+  a.B = x.B;
+  a.Hq = x.Hq;
+  a.Hkv = c.kv_heads;
+  a.G = x.Hq / c.kv_heads;
+  a.num_pages = c.num_pages;
+  a.pshift = __builtin_ctz(unsigned(c.page));
+  a.max_pages = x.max_pages;
+  a.max_len = x.max_len;
+  a.chunk = p.chunk;
+  a.nsplit = p.nsplit;
+  a.tiles = p.tiles;
+  a.tree_words = x.tree ? x.tree_words : 0;
+  a.window = x.window;
+  // a maximum of scaled scores is the scaled maximum for a scale above 0
+  // (1e-30 gives the exponentials that 0 does, and keeps 0 * inf out)
+  a.scale = std::max(std::fabs(x.scale), 1e-30f) * kLog2e;
+  a.negative = x.scale < 0.f;
+  a.cap = x.softcap * kLog2e;
+  const unsigned grid = unsigned(p.tiles) * unsigned(c.kv_heads) * unsigned(p.nsplit);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (x.dtype == GBB_F16) {
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.waves, grid, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.waves, grid, s);
+  } else {
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.waves, grid, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.waves, grid, s);
+  }
+  return int(hipGetLastError());
+}
+
+}  // namespace gbb

@@ -583,6 +583,142 @@ gbb_status gbb_cache_evict(const gbb_paged_cache* cache, int B, const int32_t* b
                            float* weights_out, int32_t* positions_out, void* workspace, size_t ws_bytes,
                            void* stream);
 
+/* ======================================================================== */
+/* Norms of heads, positions of several axes, and attention of prompts and  */
+/* drafted tokens over the paged cache                                      */
+/* ======================================================================== */
+
+/* Rotations of one to four axes.  Where a call takes `axes` and `sections`,
+ * positions is device int32 [axes][T] and pair i of the rot/2 pairs turns by
+ * the token's position on axis a, the first with i < sections[0] + ... +
+ * sections[a]: (c, s) = table[positions[a][t]][i].  sections is a host array of
+ * `axes` counts, 0 or more, whose sum is rot/2 (NULL with one axis).  A token
+ * with a position outside [0, n_pos) on any axis is padding. */
+#define GBB_MAX_AXES 4
+
+/* gbb_rope with positions of several axes: every argument as there. */
+gbb_status gbb_rope_axes(const void* x, int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head,
+                         int dtype, int T, int H, int D, const int32_t* positions, int axes, const int* sections,
+                         const float* table, int n_pos, int rot, int layout, int transpose, void* stream);
+
+/* Norm of every head and its rotation in one pass: y = R(x r w) with r =
+ * (mean x^2 + eps)^(-1/2) over the head's D elements, w = weight and R the
+ * rotation of gbb_rope (R does not change the elements from rot on); fp32,
+ * one rounding of y.
+ *   x, y       device, as gbb_rope (in place too); padding tokens give zeros.
+ *   weight     device [D] of weight_dtype, which is GBB_F32 or `dtype`; NULL: ones.
+ *   eps        0 or more, finite.
+ * T = 0 is a no-op.  Errors: those of gbb_rope. */
+gbb_status gbb_norm_rope(const void* x, int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head,
+                         int dtype, int T, int H, int D, const void* weight, int weight_dtype, float eps,
+                         const int32_t* positions, int axes, const int* sections, const float* table, int n_pos,
+                         int rot, int layout, void* stream);
+
+/* Its gradient: with g = R^T dy and u = x r,
+ *   dx = r (g w - u mean(g w u)),  dweight = sum over tokens and heads of g u;
+ * fp32 sums in an order that only the sizes set, one rounding.  Padding
+ * tokens have dx 0 and no part in dweight.
+ *   x, dy, dx  device, of `dtype`, strides as gbb_rope's x (x, dy) and y
+ *              (dx).  dx may be NULL, or dy with equal strides; otherwise it
+ *              must not overlap x or dy.
+ *   dweight    device [D] of weight_dtype, or NULL.  T = 0 makes it 0.
+ *   workspace  device, 16-byte aligned, gbb_norm_rope_grad_workspace bytes
+ *              where dweight is given; its contents need no initialisation.
+ * Errors: those of gbb_rope, GBB_E_SPACE. */
+size_t gbb_norm_rope_grad_workspace(int T, int H, int D);
+gbb_status gbb_norm_rope_grad(const void* x, int64_t x_token, int64_t x_head, const void* dy, int64_t dy_token,
+                              int64_t dy_head, void* dx, int64_t dx_token, int64_t dx_head, int dtype, int T, int H,
+                              int D, const void* weight, int weight_dtype, float eps, const int32_t* positions,
+                              int axes, const int* sections, const float* table, int n_pos, int rot, int layout,
+                              void* dweight, void* workspace, size_t ws_bytes, void* stream);
+
+/* gbb_rope_append with norms of the q and k heads before their rotation (as
+ * gbb_norm_rope, over head_dim elements) and positions of several axes.
+ *   q_weight, k_weight  device [head_dim] of weight_dtype (GBB_F32 or
+ *              `dtype`); both NULL: no norms.
+ * The cache's positions, where it has them, are those of the first axis. */
+gbb_status gbb_norm_rope_append(const gbb_paged_cache* cache, const void* qkv, int64_t token_stride, int dtype, int T,
+                                int q_heads, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                                const int32_t* positions, int axes, const int* sections, const int32_t* slots,
+                                const float* table, int n_pos, int rot, int layout, void* q, void* stream);
+
+/* What shapes the scores s = scale * (q . k) of attention, and what is seen. */
+typedef struct {
+  float softcap;          /* above 0: s becomes softcap * tanh(s / softcap); 0: none */
+  const float* slopes;    /* device [q_heads], or NULL: then s (capped) minus slopes[head] * distance */
+  int window;             /* above 0: only slots at a distance below it are seen; 0: no such limit */
+  /* the rest for gbb_paged_attention_tokens alone: */
+  const int32_t* first;   /* device [T], or NULL: token t sees no slot before first[t] (packed documents, padding) */
+  const int32_t* prefix;  /* device [B], or NULL: the slots below prefix[b] are seen by all of b's tokens */
+  const uint32_t* tree;   /* device [T][tree_words], or NULL: bit j of token t's row: it sees new token j */
+  int tree_words;
+} gbb_attention_options;
+
+/* gbb_paged_attention with a cap, a bias by distance or a window: the token
+ * is that of slot lengths[b] - 1, and the distance of slot j is lengths[b] - 1
+ * - j.  Slots that are not seen have no weight (weights_out holds the cache's
+ * there) and may hold anything.  options NULL is gbb_paged_attention. */
+size_t gbb_paged_attention_options_workspace(const gbb_paged_cache* cache, int B, int q_heads, int max_len,
+                                             int with_weights, int window);
+gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, const void* q, int64_t q_token, int dtype, int B,
+                                       int q_heads, const int32_t* block_table, int max_pages, const int32_t* lengths,
+                                       int max_len, float scale, const gbb_attention_options* options, void* out,
+                                       float* lse, float* weights_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of several new tokens per sequence over the cache that holds
+ * them already: prompts, chunks of them, trees of drafted tokens.
+ * Sequence b has the tokens starts[b] ... starts[b + 1] - 1, n_b of them, in
+ * the last n_b of its lengths[b] slots: token starts[b] + i has slot p =
+ * lengths[b] - n_b + i.  It sees slot j < lengths[b] of a page that is there if
+ *   without a tree: j <= p, or j < prefix[b];
+ *   with a tree: j < lengths[b] - n_b, or bit j - (lengths[b] - n_b) of its
+ *     row of the tree is set (bits from n_b on do not count);
+ *   and j >= first[t], and the distance of j is below the window.
+ * The distance is |p - j| without a tree; with one it is counted along the
+ * tree: the number of new tokens that it sees (by the tree alone) behind slot j
+ * if that is a new token's, else lengths[b] - n_b - 1 - j plus the number of
+ * all new tokens that it sees.
+ * out and lse as gbb_paged_attention, for every token; a row that sees nothing
+ * gives zeros and -inf.  A slot that a token does not see may hold anything,
+ * NaN included; one that it sees with a weight that rounds to 0 counts as such.
+ *   q, out     device [T][q_heads][head_dim] of `dtype` (as
+ *              gbb_paged_attention); token t of q is at t * q_token elements.
+ *   starts     device int32 [B + 1], rising, within [0, T] (values outside
+ *              are taken as the nearer end, a falling pair as no tokens).
+ *              Tokens outside all sequences are not read, and their outputs
+ *              not written.
+ *   block_table, lengths, max_len  as gbb_paged_attention.
+ *   options    NULL, or what shapes and masks the scores; tree and prefix
+ *              exclude each other.
+ *   workspace  16-byte aligned, of gbb_paged_attention_tokens_workspace bytes
+ *              (for the same options' window and tree_words, 0 without a
+ *              tree); to be had and shared as that of gbb_paged_attention.
+ * T = 0 or B = 0 is a no-op.  Results do not depend on the order of execution.
+ * Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN, GBB_E_SPACE, GBB_E_DEVICE. */
+size_t gbb_paged_attention_tokens_workspace(const gbb_paged_cache* cache, int T, int B, int q_heads, int max_len,
+                                            int window, int tree_words);
+gbb_status gbb_paged_attention_tokens(const gbb_paged_cache* cache, const void* q, int64_t q_token, int dtype, int T,
+                                      int B, int q_heads, const int32_t* starts, const int32_t* block_table,
+                                      int max_pages, const int32_t* lengths, int max_len, float scale,
+                                      const gbb_attention_options* options, void* out, float* lse, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* Keeps some of a sequence's newest slots, in their order: of the last
+ * drafted[b] of lengths[b] slots those numbered kept[b][i], i < counts[b], move
+ * to the first counts[b] places of them, with their weights and positions where
+ * the cache has them, for every kv head.  The slots behind are left as they are.
+ *   drafted, counts  device int32 [B]; kept device int32 [B][max_kept],
+ *              rising, within [0, drafted[b]).
+ *   lengths_out device int32 [B], not overlapping any input: lengths[b] -
+ *              drafted[b] + counts[b].
+ * A sequence with numbers outside these ranges, or with a missing page among
+ * the slots that it moves between, is left as it is, its length too.  Two
+ * sequences must not share a page among these slots.
+ * B = 0 is a no-op.  Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN, GBB_E_DEVICE. */
+gbb_status gbb_cache_keep(const gbb_paged_cache* cache, int B, const int32_t* block_table, int max_pages,
+                          const int32_t* lengths, const int32_t* drafted, const int32_t* kept, int max_kept,
+                          const int32_t* counts, int32_t* lengths_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
