@@ -246,36 +246,52 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
   const float slope = a.slopes ? a.slopes[hq] * kLog2e : 0.f;
   const bool shaped = a.cap > 0.f || a.slopes;
 
-  __shared__ __align__(16) uint8_t ks[BN * ROW];
-  __shared__ __align__(16) uint8_t vs[BN * ROW];
+  // two tiles of K, then two of V
+  constexpr int TILE = BN * ROW;
+  __shared__ __align__(16) uint8_t lds[4 * TILE];
+  uint8_t* const ks = lds;
+  uint8_t* const vs = lds + 2 * TILE;
   // Piece p (16 bytes) of slot r lies at p ^ swizzle(r): a slot a lane for K (8
   // lanes together hit 8 pieces), 4 slots of two pieces for V.
   constexpr int KS = PIECES < 16 ? PIECES - 1 : 15, VS = PIECES < 16 ? PIECES / 2 - 1 : 7;
   const auto k_swizzle = [](int r) { return r & KS; };
   const auto v_swizzle = [](int r) { return 2 * (r & VS); };
 
-  // Pages of 64 groups of 16 slots from `group0` on, a group a lane.
-  const auto pages_from = [&](int group) {
-    const int key = min((group + lane) << 4, a.max_len - 1);
-    const int p = a.block_table[size_t(b) * a.max_pages + (key >> a.pshift)];
-    return ((group + lane) << 4) < k1 && unsigned(p) < unsigned(a.num_pages) ? p : -1;
-  };
+  // Where 64 groups of 16 slots lie, a group a lane: bytes from the cache's
+  // start, bytes that take part (none of a page that is not there), and a bit
+  // for every page that should be there and is not.
   const int pmask = (1 << a.pshift) - 1;
   const size_t page_bytes = (size_t(1) << a.pshift) * GROW;
-  int pages = pages_from(k0 >> 4);
-  constexpr int TPP = 1024 / BN;               // tiles that `pages` covers
+  int off_lo, off_hi, bytes;
+  uint64_t missing;
+  const auto locate = [&](int first_slot) {
+    const int key = first_slot + 16 * lane;
+    const int p = a.block_table[size_t(b) * a.max_pages + (min(key, a.max_len - 1) >> a.pshift)];
+    const bool used = key < k1, there = used && unsigned(p) < unsigned(a.num_pages);
+    const size_t off = there ? (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * GROW : 0;
+    off_lo = int(uint32_t(off));
+    off_hi = int(uint32_t(off >> 32));
+    bytes = there ? min(k1 - key, 16) * GROW : 0;
+    missing = __ballot(used && !there);
+  };
+  constexpr int TPP = 1024 / BN;               // tiles of 64 groups
   u32x4 kr[NL], vr[NL];
-  const auto fetch = [&](u32x4 (&x)[NL], const uint8_t* base, int i) {
+  const auto load = [&](const uint8_t* base, int j, int group) {
+    const int r = uniform((j * NW + wave) * RPI);            // first slot of the load within the tile
+    const int g = group + (r >> 4);
+    const size_t off = size_t(uint32_t(__builtin_amdgcn_readlane(off_hi, g))) << 32 | uint32_t(__builtin_amdgcn_readlane(off_lo, g));
+    return __builtin_amdgcn_raw_buffer_load_b128(span(base + off, __builtin_amdgcn_readlane(bytes, g)),
+                                                 (r & 15) * GROW + lane * 16, 0, 0);
+  };
+  // starts tile i on its way to registers; returns a bit for every missing group
+  const auto fetch = [&](int i) {
+    if (i % TPP == 0) locate(k0 + i * BN);
+    const int group = (i % TPP) * (BN / 16);
 #pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      const int r = uniform((j * NW + wave) * RPI);          // first slot of the load within the tile
-      const int group = (r >> 4) + (i % TPP) * (BN / 16);
-      const int p = __builtin_amdgcn_readlane(pages, group);
-      const int key = k0 + i * BN + (r & ~15);
-      const size_t off = (size_t(max(p, 0)) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * GROW;
-      const Span rows = span(base + off, uniform(p < 0 ? 0 : max(0, min(k1 - key, 16)) * GROW));
-      x[j] = __builtin_amdgcn_raw_buffer_load_b128(rows, (r & 15) * GROW + lane * 16, 0, 0);
-    }
+    for (int j = 0; j < NL; ++j) kr[j] = load(a.k, j, group);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) vr[j] = load(a.v, j, group);
+    return uniform(uint32_t(missing >> group) & ((1u << (BN / 16)) - 1));
   };
   const auto keep = [&](const u32x4 (&x)[NL], uint8_t* to, auto swizzle, auto change) {
 #pragma unroll
@@ -305,12 +321,26 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
     for (int i = 0; i < 4; ++i) x[i] = f(x[i] & 0xffffu) | f(x[i] >> 16) << 16;
     return x;
   };
-  const auto sign_of = [&](int negative) {     // 1 where an element is an infinity of that sign or NaN
-    return [=](const u32x4& x) {
-      return elements(x, [=](uint32_t e) {
-        return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
+  const auto mixed = [&](int i) { return k0 + i * BN < same_low || min(k0 + i * BN + BN, k1) > same_high; };
+  __shared__ int odd_tile[2];                  // the last tile of each buffer that has such elements
+  // tile i from the registers to LDS
+  const auto put_tile = [&](int i) {
+    uint8_t* const kt = ks + (i & 1) * TILE;
+    uint8_t* const vt = vs + (i & 1) * TILE;
+    keep(kr, kt, k_swizzle, as_is);
+    if (!mixed(i)) {
+      keep(vr, vt, v_swizzle, as_is);
+    } else {
+      bool odd = false;
+      keep(vr, vt, v_swizzle, [&](const u32x4& x) {
+        return elements(x, [&](uint32_t e) {
+          const bool bad = (e & EXP) == EXP;
+          odd |= bad;
+          return bad ? 0u : e;
+        });
       });
-    };
+      if (odd) odd_tile[i & 1] = i;
+    }
   };
 
   // this lane's addresses in LDS: K's slot c, V's slots 4 h + (lane % 16) / 4
@@ -320,46 +350,52 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
 #pragma unroll
   for (int i = 0; i < VA; ++i) {
     const int r = 4 * h + ((lane & 15) >> 2);
-    v_at[i] = r * ROW + ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(r)) * 16 + 8 * (lane & 1);
+    v_at[i] = 2 * TILE + r * ROW + ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(r)) * 16 + 8 * (lane & 1);
   }
+  // V's elements 32 j ... of the slots 16 s ..., as the A operand
+  const auto v_piece = [&](int j, int s, int buffer) {
+    typedef __attribute__((address_space(3))) i16x4* L;
+    const uint8_t* at = lds + v_at[j % VA] + buffer + (j / VA) * 256 + s * 16 * ROW;
+    const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
+    const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + 8 * ROW));
+    return __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
 
   f32x16 o[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
   float m = -INFINITY, l = 0.f;
 
-  fetch(kr, a.k, 0);
-  fetch(vr, a.v, 0);
+  if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
+  uint32_t holes = fetch(0), holes_next = 0;
+  __syncthreads();
+  put_tile(0);
+  if (nt > 1) holes_next = fetch(1);
+  __syncthreads();
   for (int i = 0; i < nt; ++i) {
-    const int key0 = k0 + i * BN;
-    const int pages_now = pages;               // of this tile
-    keep(kr, ks, k_swizzle, as_is);
-    __syncthreads();
-    if (i + 1 < nt) {
-      if ((i + 1) % TPP == 0) pages = pages_from((k0 + (i + 1) * BN) >> 4);
-      fetch(kr, a.k, i + 1);
-    }
+    const int key0 = k0 + i * BN, buffer = (i & 1) * TILE;
     const bool works = key0 < hi_wave && key0 + BN > lo_wave;
-    V8 part[PARTS][BN / 16];
+    f32x16 s[NE];
     if (works) {
-      f32x16 s[NE];
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(ks + k_at[kc % KA] + (kc / KA) * 256 + e * 32 * ROW);
+          const u32x4 x = *reinterpret_cast<const u32x4*>(lds + k_at[kc % KA] + buffer + (kc / KA) * 256 + e * 32 * ROW);
           s[e] = H::mfma32(__builtin_bit_cast(V8, x), qf[kc], s[e]);
         }
       }
+    }
+    uint32_t holes_after = 0;
+    if (i + 1 < nt) put_tile(i + 1);
+    if (i + 2 < nt) holes_after = fetch(i + 2);
+    V8 part[PARTS][BN / 16];
+    if (works) {
       // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
       const int key = key0 + 4 * h;
       const auto slot = [](int e, int r) { return 32 * e + 8 * (r / 4) + r % 4; };
       float unit = scale;
-      bool holes = false;                      // a page that is not there
-#pragma unroll
-      for (int g = 0; g < BN / 16; ++g)
-        holes |= key0 + 16 * g < k1 && __builtin_amdgcn_readlane(pages_now, (i % TPP) * (BN / 16) + g) < 0;
       const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
       uint32_t bits[NE];                       // of drafted slots, as the lane's registers have them: bit 8 (r / 4) + r % 4
       const bool branches = a.tree && key0 + BN > ctx;
@@ -438,7 +474,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
                 seen = seen && after < a.window;
               }
             }
-            if (holes && __builtin_amdgcn_readlane(pages_now, (i % TPP) * (BN / 16) + 2 * e + r / 8) < 0) seen = false;
+            if (holes >> (2 * e + r / 8) & 1u) seen = false;
             s[e][r] = seen ? s[e][r] : -INFINITY;
           }
       }
@@ -469,62 +505,53 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
             p -= float(y);   // exact
           }
         }
-    }
-    // V's elements 32 j ... of the slots 16 s ..., as the A operand
-    const auto v_piece = [&](int j, int s) {
-      typedef __attribute__((address_space(3))) i16x4* L;
-      const uint8_t* at = vs + v_at[j % VA] + (j / VA) * 256 + s * 16 * ROW;
-      const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
-      const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + 8 * ROW));
-      return __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    if (key0 < same_low || min(key0 + BN, k1) > same_high) {
-      int odd = 0;
-      keep(vr, vs, v_swizzle, [&](const u32x4& x) {
-        return elements(x, [&](uint32_t e) {
-          const bool bad = (e & EXP) == EXP;
-          odd |= bad;
-          return bad ? 0u : e;
-        });
-      });
-      if (__syncthreads_or(odd)) {
-#pragma unroll 1
-        for (int negative = 0; negative < 2; ++negative) {
-          __syncthreads();
-          keep(vr, vs, v_swizzle, sign_of(negative));
-          __syncthreads();
-          if (works)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              f32x16 hit = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-              for (int s = 0; s < BN / 16; ++s) hit = H::mfma32(v_piece(j, s), part[0][s], hit);
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (hit[r] > 0.f) o[j][r] += negative ? -INFINITY : INFINITY;
-            }
-        }
-        __syncthreads();
-        keep(vr, vs, v_swizzle, [&](const u32x4& x) {
-          return elements(x, [&](uint32_t e) { return (e & EXP) == EXP ? 0u : e; });
-        });
-        __syncthreads();
-      }
-    } else {
-      keep(vr, vs, v_swizzle, as_is);
-      __syncthreads();
-    }
-    if (i + 1 < nt) fetch(vr, a.v, i + 1);
-    if (works) {
 #pragma unroll
       for (int s = 0; s < BN / 16; ++s)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const V8 x = v_piece(j, s);
+          const V8 x = v_piece(j, s, buffer);
 #pragma unroll
           for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][s], o[j]);
         }
     }
+    if (mixed(i) && uniform(odd_tile[i & 1]) == i) {
+      // rare: V of the tile once more, from memory
+      const int key = key0 + 16 * min(lane, BN / 16 - 1);
+      const int p = a.block_table[size_t(b) * a.max_pages + (min(key, a.max_len - 1) >> a.pshift)];
+#pragma unroll 1
+      for (int negative = 0; negative < 2; ++negative) {
+        u32x4 x[NL];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          const int r = uniform((j * NW + wave) * RPI);
+          const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + (r & ~15);
+          const bool there = unsigned(page) < unsigned(a.num_pages);
+          const size_t off = (size_t(there ? page : 0) * a.Hkv + hk) * page_bytes + size_t(slot & pmask) * GROW;
+          x[j] = __builtin_amdgcn_raw_buffer_load_b128(span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0)),
+                                                       (r & 15) * GROW + lane * 16, 0, 0);
+        }
+        __syncthreads();
+        keep(x, vs + buffer, v_swizzle, [&](const u32x4& x) {
+          return elements(x, [=](uint32_t e) {   // 1 where an element is an infinity of that sign or NaN
+            return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
+          });
+        });
+        __syncthreads();
+        if (works)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            f32x16 hit = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < BN / 16; ++s) hit = H::mfma32(v_piece(j, s, buffer), part[0][s], hit);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (hit[r] > 0.f) o[j][r] += negative ? -INFINITY : INFINITY;
+          }
+      }
+    }
+    holes = holes_next;
+    holes_next = holes_after;
+    __syncthreads();
   }
 
   l = row_sum(l);
