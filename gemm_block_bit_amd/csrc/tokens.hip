@@ -41,6 +41,7 @@
 // results (maximum, sum, unnormalised output, fp32) go to the workspace, and
 // the last workgroup of a row tile joins them in the order of the runs.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -52,9 +53,12 @@ namespace {
 
 constexpr int kMaxJoin = 64;     // runs of a row tile
 constexpr int kMaxArrived = GBB_ATTENTION_COUNTERS / 4;   // counters of row tiles with several runs
-// exp2 is taken this many powers above the running maximum's 0, so that fp16
-// keeps small probabilities out of its subnormals: 2^14 < 65504
-constexpr float kShift = 14.f;
+// Probabilities are 2^(score - ref).  ref is moved to kShift below a row's
+// maximum when they would pass 2^kLimit: seldom after the first tiles, and
+// each move costs a pass over the output.  fp16 (below 65504) so keeps those
+// down to 2^-20 of the maximum out of its subnormals; a smaller one is off by
+// 2^-31 of the maximum's at most.
+constexpr float kShift = 6.f, kLimit = 15.f;
 
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
@@ -74,7 +78,7 @@ struct Args {
   void* out;
   float* lse;
   unsigned* arrived;   // [row tile][Hkv] runs that are done, 0 between calls
-  float2* ml;          // [row tile][Hkv][nsplit][rows] maximum (log2 domain) and sum
+  float2* ml;          // [row tile][Hkv][nsplit][rows] ref (below) and sum
   float* o;            // [row tile][Hkv][nsplit][rows][D]
   int64_t q_token;
   int T, B, Hq, Hkv, G, num_pages, pshift, max_pages, max_len, chunk, nsplit, tiles, tree_words, window;
@@ -112,7 +116,7 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <int DT, int CT, int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args a) {
   typedef Half<DT> H;
   typedef typename H::T T;
   typedef typename H::V8 V8;
@@ -364,7 +368,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
   f32x16 o[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-  float m = -INFINITY, l = 0.f;
+  float ref = -FLT_MAX, l = 0.f;
 
   if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
   uint32_t holes = fetch(0), holes_next = 0;
@@ -482,16 +486,15 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
 #pragma unroll
       for (int e = 0; e < NE; ++e)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[e][r]);
+        for (int r = 0; r < 16; r += 2) mx = fmaxf(fmaxf(s[e][r], s[e][r + 1]), mx);
       mx = row_max(mx) * unit;
-      if (__any(mx > m)) {
-        const float mn = fmaxf(m, mx), f = rescale(m, mn);
-        m = mn;
+      if (__any(mx > ref + kLimit)) {
+        const float to = mx > ref + kLimit ? mx - kShift : ref, f = __builtin_amdgcn_exp2f(ref - to);
+        ref = to;
         l *= f;
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] *= f;
       }
-      const float ref = m == -INFINITY ? 0.f : m - kShift;
 #pragma unroll
       for (int e = 0; e < NE; ++e)
 #pragma unroll
@@ -570,7 +573,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
         for (int u = 0; u < 4; ++u) x[u] = T(l == 0.f ? 0.f : o[j][r + u] * f);
         *reinterpret_cast<V4*>(static_cast<T*>(a.out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = x;
       }
-    if (a.lse && h == 0) a.lse[head] = l == 0.f ? -INFINITY : (m - kShift + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && h == 0) a.lse[head] = l == 0.f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * kLn2;
     return;
   }
 
@@ -583,7 +586,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) put(a.o + mine * D + 32 * j + 8 * (r / 4) + 4 * h + r % 4, o[j][r], o[j][r + 1]);
-    if (h == 0) put(reinterpret_cast<float*>(a.ml + mine), m, l);
+    if (h == 0) put(reinterpret_cast<float*>(a.ml + mine), ref, l);
   }
   __shared__ unsigned count;
   loads_left<0>();
@@ -629,7 +632,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tokens_kernel(Args a) {
     typedef T V2 __attribute__((ext_vector_type(2)));
     const float f = ll == 0.f ? 0.f : vscale / ll;
     *reinterpret_cast<V2*>(static_cast<T*>(a.out) + to * D + d) = V2{T(ll == 0.f ? 0.f : o0 * f), T(ll == 0.f ? 0.f : o1 * f)};
-    if (d == 0 && a.lse) a.lse[to] = ll == 0.f ? -INFINITY : (mm - kShift + __builtin_amdgcn_logf(ll)) * kLn2;
+    if (d == 0 && a.lse) a.lse[to] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
   }
 }
 
