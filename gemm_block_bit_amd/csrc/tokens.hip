@@ -79,7 +79,7 @@ struct Args {
   float* lse;
   unsigned* arrived;   // [row tile][Hkv] runs that are done, 0 between calls
   float2* ml;          // [row tile][Hkv][nsplit][rows] ref (below) and sum
-  float* o;            // [row tile][Hkv][nsplit][rows][D]
+  float* o;            // [row tile][Hkv][nsplit][rows * D], in the order of the lanes that hold them
   int64_t q_token;
   int T, B, Hq, Hkv, G, num_pages, pshift, max_pages, max_len, chunk, nsplit, tiles, tree_words, window;
   float scale, cap;    // times log2(e)
@@ -558,12 +558,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   }
 
   l = row_sum(l);
-  const float vscale = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
   const int ns = (k_high - k_low - 1) / a.chunk + 1;
-  typedef T V4 __attribute__((ext_vector_type(4)));
-  if (ns == 1) {
+  // out and lse of this lane's row from the output's pieces (4 elements each)
+  const float vscale = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+  const auto finish = [&](float ref, float l) {
     if (!real) return;
     const float f = l == 0.f ? 0.f : vscale / l;
+    typedef T V4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -574,19 +575,30 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
         *reinterpret_cast<V4*>(static_cast<T*>(a.out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = x;
       }
     if (a.lse && h == 0) a.lse[head] = l == 0.f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * kLn2;
+  };
+  if (ns == 1) {
+    finish(ref, l);
     return;
   }
 
-  // Partial results at device scope, awaited before the count (as in
-  // attention.hip, where the reasons stand); the last workgroup joins.
-  const size_t slot0 = (size_t(w) * a.Hkv + hk) * a.nsplit;
-  const size_t mine = (slot0 + sp) * ROWS + 32 * wave + c;
+  // Partial results, as the lanes hold them: piece by piece, 16 bytes a lane.
+  // At device scope and awaited before the count (as in attention.hip, where
+  // the reasons stand); the last workgroup joins them in the order of the runs.
+  const size_t run0 = (size_t(w) * a.Hkv + hk) * a.nsplit;
+  constexpr int DEVICE = 16;                   // the cache policy of device scope
+  const auto run_at = [&](int s) { return span(a.o + (run0 + s) * (ROWS * D), ROWS * D * 4); };
+  const auto ml_at = [&](int s) { return reinterpret_cast<float*>(a.ml + (run0 + s) * ROWS + 32 * wave + c); };
+  const int at = (wave * (4 * NT) * 64 + lane) * 16;
   if (real) {
+    const Span to = run_at(sp);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; r += 2) put(a.o + mine * D + 32 * j + 8 * (r / 4) + 4 * h + r % 4, o[j][r], o[j][r + 1]);
-    if (h == 0) put(reinterpret_cast<float*>(a.ml + mine), ref, l);
+      for (int r = 0; r < 16; r += 4) {
+        const f32x4 x = {o[j][r], o[j][r + 1], o[j][r + 2], o[j][r + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, at + (4 * j + r / 4) * 1024, 0, DEVICE);
+      }
+    if (h == 0) put(ml_at(sp), ref, l);
   }
   __shared__ unsigned count;
   loads_left<0>();
@@ -596,44 +608,43 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   __syncthreads();
   if (count != unsigned(ns - 1)) return;
   if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int valid = min(ROWS, rows_all - r0);
-  const float* po = a.o + slot0 * ROWS * D;
-  const float* pm = reinterpret_cast<const float*>(a.ml + slot0 * ROWS);
-  for (int i = threadIdx.x; i < valid * (D / 2); i += THREADS) {
-    const int q = i / (D / 2), d = 2 * (i % (D / 2));
-    float mm = -INFINITY, ll = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int s0 = 0; s0 < ns; s0 += 8) {
-      float2 x[8], e[8];
+  if (!real) return;
+  float high = -FLT_MAX;
+  for (int s0 = 0; s0 < ns; s0 += 16) {
+    float x[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const size_t at = size_t(min(s0 + u, ns - 1)) * ROWS + q;
-        x[u] = get(po + at * D + d);
-        e[u] = get(pm + 2 * at);
-      }
-      float top = mm;
+    for (int u = 0; u < 16; ++u) x[u] = get(ml_at(min(s0 + u, ns - 1))).x;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) top = fmaxf(top, e[u].x);
-      const float f = rescale(mm, top);
-      mm = top;
-      ll *= f;
-      o0 *= f;
-      o1 *= f;
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (s0 + u < ns) {
-          const float g = rescale(e[u].x, mm);
-          ll += g * e[u].y;
-          o0 += g * x[u].x;
-          o1 += g * x[u].y;
-        }
-    }
-    const int r = r0 + q, tok = r / a.G;
-    const size_t to = size_t(t0 + tok) * a.Hq + hk * a.G + (r - tok * a.G);
-    typedef T V2 __attribute__((ext_vector_type(2)));
-    const float f = ll == 0.f ? 0.f : vscale / ll;
-    *reinterpret_cast<V2*>(static_cast<T*>(a.out) + to * D + d) = V2{T(ll == 0.f ? 0.f : o0 * f), T(ll == 0.f ? 0.f : o1 * f)};
-    if (d == 0 && a.lse) a.lse[to] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+    for (int u = 0; u < 16; ++u) high = fmaxf(high, x[u]);
   }
+  l = 0.f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) o[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  constexpr int AHEAD = 2;                     // runs whose pieces are under way at once
+  for (int s0 = 0; s0 < ns; s0 += AHEAD) {
+    u32x4 x[AHEAD][4 * NT];
+    float2 e[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const Span from = run_at(min(s0 + u, ns - 1));
+      e[u] = get(ml_at(min(s0 + u, ns - 1)));
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i) x[u][i] = __builtin_amdgcn_raw_buffer_load_b128(from, at + i * 1024, 0, DEVICE);
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (s0 + u < ns) {
+        const float f = __builtin_amdgcn_exp2f(e[u].x - high);
+        l += f * e[u].y;
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) {
+          const f32x4 y = __builtin_bit_cast(f32x4, x[u][i]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[i / 4][4 * (i % 4) + r] = __builtin_fmaf(f, y[r], o[i / 4][4 * (i % 4) + r]);
+        }
+      }
+  }
+  finish(high, l);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
