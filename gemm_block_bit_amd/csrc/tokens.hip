@@ -115,7 +115,7 @@ __device__ __forceinline__ float row_sum(float x) {
   return r.x + r.y;
 }
 
-template <int DT, int CT, int D, int NW>
+template <int DT, int CT, int D, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args a) {
   typedef Half<DT> H;
   typedef typename H::T T;
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   constexpr int NL = BN / (NW * RPI);         // loads a lane of a tile of K or V
   constexpr int PIECES = ROW / 16;
   constexpr int KC = D / 16, NT = D / 32, NE = BN / 32;
-  constexpr int KA = KC < 8 ? KC : 8, VA = NT < 4 ? NT : 4;   // distinct permuted addresses; beyond, 256 bytes on
+  constexpr int KA = KC < 8 ? KC : 8, VA = NT < 4 ? NT : 4;   // pieces of 256 bytes of a slot (beyond, 256 bytes on)
   static_assert(NL >= 1 && RPI <= 16, "a load stays within 16 slots");
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane & 31, h = lane >> 5;
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   int lo = 0, hi, place = ctx + token, first = 0, drafted = 0;
   const uint32_t* words = nullptr;
   if (a.first) first = max(0, a.first[t]);
-  if (a.tree) {
+  if constexpr (TREE) {
     words = a.tree + t * a.tree_words;
     for (int i = 0; i < a.tree_words; ++i) {
       const int left = n - 32 * i;
@@ -197,8 +197,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   if (a.window) lo = int(max(int64_t(0), int64_t(place) - a.window + 1));
   lo = max(lo, first);
   if (!real) lo = INT_MAX, hi = 0;
-  const int top = a.tree && real ? ctx + min(n, 32 * a.tree_words) : hi;         // one past the last slot it may see
-  const int bottom = a.tree && real ? max(first, min(lo, max(0, ctx))) : lo;     // and the first
+  const int top = TREE && real ? ctx + min(n, 32 * a.tree_words) : hi;         // one past the last slot it may see
+  const int bottom = TREE && real ? max(first, min(lo, max(0, ctx))) : lo;     // and the first
   const bool some = top > bottom;
   const int lo_wave = uniform(wave_min(some ? bottom : INT_MAX)), hi_wave = uniform(wave_max(some ? top : 0));
   const int lo_all = uniform(wave_max(real ? lo : 0)), hi_all = uniform(wave_min(real ? hi : INT_MAX));   // all its rows see these
@@ -347,19 +347,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     }
   };
 
-  // this lane's addresses in LDS: K's slot c, V's slots 4 h + (lane % 16) / 4
-  int k_at[KA], v_at[VA];
-#pragma unroll
-  for (int i = 0; i < KA; ++i) k_at[i] = c * ROW + ((2 * i + h) ^ k_swizzle(c)) * 16;
-#pragma unroll
-  for (int i = 0; i < VA; ++i) {
-    const int r = 4 * h + ((lane & 15) >> 2);
-    v_at[i] = 2 * TILE + r * ROW + ((4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(r)) * 16 + 8 * (lane & 1);
-  }
+  // This lane's addresses in LDS: K's slot c, V's slots 4 h + (lane % 16) / 4.
+  // Other pieces of the slot differ in bits that the permutation leaves to an xor.
+  const int k_at = c * ROW + (h ^ k_swizzle(c)) * 16;
+  const int v_slot = 4 * h + ((lane & 15) >> 2);
+  const int v_at = 2 * TILE + v_slot * ROW + ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(v_slot)) * 16 + 8 * (lane & 1);
+  // K's elements 16 kc ... of the slots 32 e ..., as the A operand
+  const auto k_piece = [&](int kc, int e, int buffer) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(lds + ((k_at + buffer) ^ (kc % KA * 32)) + (kc / KA) * 256 + e * 32 * ROW);
+    return __builtin_bit_cast(V8, x);
+  };
   // V's elements 32 j ... of the slots 16 s ..., as the A operand
   const auto v_piece = [&](int j, int s, int buffer) {
     typedef __attribute__((address_space(3))) i16x4* L;
-    const uint8_t* at = lds + v_at[j % VA] + buffer + (j / VA) * 256 + s * 16 * ROW;
+    const uint8_t* at = lds + ((v_at + buffer) ^ (j % VA * 64)) + (j / VA) * 256 + s * 16 * ROW;
     const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
     const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + 8 * ROW));
     return __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -385,10 +386,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       for (int e = 0; e < NE; ++e) {
         s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(lds + k_at[kc % KA] + buffer + (kc / KA) * 256 + e * 32 * ROW);
-          s[e] = H::mfma32(__builtin_bit_cast(V8, x), qf[kc], s[e]);
-        }
+        for (int kc = 0; kc < KC; ++kc) s[e] = H::mfma32(k_piece(kc, e, buffer), qf[kc], s[e]);
       }
     }
     uint32_t holes_after = 0;
@@ -402,7 +400,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       float unit = scale;
       const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
       uint32_t bits[NE];                       // of drafted slots, as the lane's registers have them: bit 8 (r / 4) + r % 4
-      const bool branches = a.tree && key0 + BN > ctx;
+      const bool branches = TREE && key0 + BN > ctx;
       int beyond = 0;                          // visible drafted slots behind the tile
       if (branches) {
 #pragma unroll
@@ -649,11 +647,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
+template <int DT, int CT, int D, bool TREE>
+void run_waves(const Args& a, int waves, unsigned grid, hipStream_t s) {
+  if (waves == 4) start((tokens_kernel<DT, CT, D, 4, TREE>), dim3(grid), dim3(256), s, a);
+  else start((tokens_kernel<DT, CT, D, 2, TREE>), dim3(grid), dim3(128), s, a);
+}
 template <int DT, int CT, int D>
 void run(const Args& a, int waves, unsigned grid, hipStream_t s) {
-  if (waves == 4) start((tokens_kernel<DT, CT, D, 4>), dim3(grid), dim3(256), s, a);
-  else if (waves == 2) start((tokens_kernel<DT, CT, D, 2>), dim3(grid), dim3(128), s, a);
-  else start((tokens_kernel<DT, CT, D, 1>), dim3(grid), dim3(64), s, a);
+  if (a.tree) run_waves<DT, CT, D, true>(a, waves, grid, s);
+  else run_waves<DT, CT, D, false>(a, waves, grid, s);
 }
 template <int DT, int CT>
 void run_dim(const Args& a, int D, int waves, unsigned grid, hipStream_t s) {
@@ -668,7 +670,7 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   TokensPlan p;
   const int G = Hq / c.kv_heads;
   const int64_t rows = int64_t(T) * G;         // of a kv head
-  p.waves = rows <= int64_t(32) * B ? 1 : rows <= int64_t(64) * B ? 2 : 4;
+  p.waves = rows <= int64_t(64) * B ? 2 : 4;
   p.rows = 32 * p.waves;
   p.tiles = int(std::min<int64_t>(rows / p.rows + B, INT_MAX));
   // slots from the first to the last that a row tile may see
