@@ -141,11 +141,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const int w = uniform(id % a.tiles), sp = uniform(id / a.tiles);
   // the sequence whose row tile number w of the call is, 64 sequences at a time
   const auto start_of = [&](int b) { return max(0, min(a.starts[b], a.T)); };
-  int b = -1, tile = 0, before = 0, ntiles = 0;
+  int b = -1, tile = 0, before = 0, ntiles = 0, t0 = 0, n = 0, len = 0, shared = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int n = 0;
-    if (b0 + lane < a.B) n = max(0, start_of(b0 + lane + 1) - start_of(b0 + lane));
-    const int mine = (n * a.G + ROWS - 1) / ROWS;
+    // all that is known of a sequence in one step
+    const int i = min(b0 + lane, a.B - 1);
+    const int from = start_of(i), slots = a.lengths[i], prefix = a.prefix ? a.prefix[i] : 0;
+    const int tokens = b0 + lane < a.B ? max(0, start_of(i + 1) - from) : 0;
+    const int mine = (tokens * a.G + ROWS - 1) / ROWS;
     int sum = mine;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) {
@@ -158,14 +160,19 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       b = b0 + at;
       ntiles = __builtin_amdgcn_readlane(mine, at);
       tile = w - (before + __builtin_amdgcn_readlane(sum, at) - ntiles);
+      t0 = __builtin_amdgcn_readlane(from, at);
+      n = __builtin_amdgcn_readlane(tokens, at);
+      len = max(0, min(__builtin_amdgcn_readlane(slots, at), a.max_len));
+      shared = __builtin_amdgcn_readlane(prefix, at);
       break;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
   }
   if (b < 0) return;
   b = uniform(b);
-  const int t0 = uniform(start_of(b)), n = uniform(start_of(b + 1)) - t0;
-  const int len = uniform(max(0, min(a.lengths[b], a.max_len)));
+  t0 = uniform(t0);
+  n = uniform(n);
+  len = uniform(len);
   const int ctx = len - n;                     // may be negative
   const int rows_all = n * a.G;
   const int r0 = uniform(ntiles - 1 - tile) * ROWS;   // the last tokens first: they see most
@@ -173,6 +180,19 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const bool real = row < rows_all;
   const int token = real ? row / a.G : 0, hq = hk * a.G + (real ? row - token * a.G : 0);
   const size_t t = size_t(t0 + token);
+
+  // q, the B operand: row c, elements 16 kc + 8 h ...; and the first pages of the
+  // run, where it is known by now that they will be asked for (else of no use)
+  u32x4 qw[KC];
+#pragma unroll
+  for (int kc = 0; kc < KC; ++kc) {
+    qw[kc] = u32x4{0, 0, 0, 0};
+    if (real) qw[kc] = ld16(static_cast<const uint16_t*>(a.q) + t * a.q_token + size_t(hq) * D + 16 * kc + 8 * h);
+  }
+  const auto page_of = [&](int slot) { return a.block_table[size_t(b) * a.max_pages + (min(slot, a.max_len - 1) >> a.pshift)]; };
+  const bool from_zero = !a.first && !a.window;
+  const int early = page_of(min(int64_t(sp) * a.chunk, int64_t(a.max_len)) + 16 * lane);
+  in_order();
 
   // What a row sees: slots [lo, hi), and with a tree those of [ctx, len) whose
   // bit is set, from `first` on and less than `window` away.  place: where
@@ -182,15 +202,21 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   if (a.first) first = max(0, a.first[t]);
   if constexpr (TREE) {
     words = a.tree + t * a.tree_words;
-    for (int i = 0; i < a.tree_words; ++i) {
-      const int left = n - 32 * i;
-      if (left > 0) drafted += __popc(left < 32 ? words[i] & ((1u << left) - 1) : words[i]);
+    for (int i0 = 0; i0 < a.tree_words; i0 += 4) {
+      uint32_t x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = words[min(i0 + u, a.tree_words - 1)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int left = i0 + u < a.tree_words ? n - 32 * (i0 + u) : 0;
+        drafted += left <= 0 ? 0 : __popc(left < 32 ? x[u] & ((1u << left) - 1) : x[u]);
+      }
     }
     place = ctx + drafted - 1;
     hi = ctx;
   } else {
     hi = place + 1;
-    if (a.prefix) hi = max(hi, a.prefix[b]);
+    if (a.prefix) hi = max(hi, shared);
     if (a.window) hi = int(min(int64_t(hi), int64_t(place) + a.window));
     hi = min(hi, len);
   }
@@ -236,15 +262,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const int k1 = k0 + min(k_high - k0, a.chunk);
   const int nt = (k1 - k0 + BN - 1) / BN;
 
-  // q, the B operand: row c, elements 16 kc + 8 h ...
   V8 qf[KC];
 #pragma unroll
-  for (int kc = 0; kc < KC; ++kc) {
-    u32x4 x = {0, 0, 0, 0};
-    if (real) x = ld16(static_cast<const uint16_t*>(a.q) + t * a.q_token + size_t(hq) * D + 16 * kc + 8 * h);
-    if (a.negative) x ^= 0x80008000u;
-    qf[kc] = __builtin_bit_cast(V8, x);
-  }
+  for (int kc = 0; kc < KC; ++kc) qf[kc] = __builtin_bit_cast(V8, a.negative ? qw[kc] ^ 0x80008000u : qw[kc]);
   const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
   const float over = a.cap > 0.f ? 1.f / a.cap : 0.f;
   const float slope = a.slopes ? a.slopes[hq] * kLog2e : 0.f;
@@ -268,9 +288,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const size_t page_bytes = (size_t(1) << a.pshift) * GROW;
   int off_lo, off_hi, bytes;
   uint64_t missing;
-  const auto locate = [&](int first_slot) {
+  const auto locate = [&](int first_slot, int p) {
     const int key = first_slot + 16 * lane;
-    const int p = a.block_table[size_t(b) * a.max_pages + (min(key, a.max_len - 1) >> a.pshift)];
     const bool used = key < k1, there = used && unsigned(p) < unsigned(a.num_pages);
     const size_t off = there ? (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * GROW : 0;
     off_lo = int(uint32_t(off));
@@ -289,7 +308,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   };
   // starts tile i on its way to registers; returns a bit for every missing group
   const auto fetch = [&](int i) {
-    if (i % TPP == 0) locate(k0 + i * BN);
+    if (i % TPP == 0) locate(k0 + i * BN, i == 0 && from_zero ? early : page_of(k0 + i * BN + 16 * lane));
     const int group = (i % TPP) * (BN / 16);
 #pragma unroll
     for (int j = 0; j < NL; ++j) kr[j] = load(a.k, j, group);
@@ -517,8 +536,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     }
     if (mixed(i) && uniform(odd_tile[i & 1]) == i) {
       // rare: V of the tile once more, from memory
-      const int key = key0 + 16 * min(lane, BN / 16 - 1);
-      const int p = a.block_table[size_t(b) * a.max_pages + (min(key, a.max_len - 1) >> a.pshift)];
+      const int p = page_of(key0 + 16 * min(lane, BN / 16 - 1));
 #pragma unroll 1
       for (int negative = 0; negative < 2; ++negative) {
         u32x4 x[NL];
@@ -607,21 +625,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   if (count != unsigned(ns - 1)) return;
   if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (!real) return;
-  float high = -FLT_MAX;
-  for (int s0 = 0; s0 < ns; s0 += 16) {
-    float x[16];
-#pragma unroll
-    for (int u = 0; u < 16; ++u) x[u] = get(ml_at(min(s0 + u, ns - 1))).x;
-#pragma unroll
-    for (int u = 0; u < 16; ++u) high = fmaxf(high, x[u]);
-  }
-  l = 0.f;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) o[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
   constexpr int AHEAD = 2;                     // runs whose pieces are under way at once
-  for (int s0 = 0; s0 < ns; s0 += AHEAD) {
-    u32x4 x[AHEAD][4 * NT];
-    float2 e[AHEAD];
+  u32x4 x[AHEAD][4 * NT];
+  float2 e[AHEAD];
+  const auto take = [&](int s0) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const Span from = run_at(min(s0 + u, ns - 1));
@@ -629,6 +636,21 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 #pragma unroll
       for (int i = 0; i < 4 * NT; ++i) x[u][i] = __builtin_amdgcn_raw_buffer_load_b128(from, at + i * 1024, 0, DEVICE);
     }
+  };
+  float high = -FLT_MAX;
+  for (int s0 = 0; s0 < ns; s0 += 16) {
+    float y[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) y[u] = get(ml_at(min(s0 + u, ns - 1))).x;
+    if (s0 == 0) take(0);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) high = fmaxf(high, y[u]);
+  }
+  l = 0.f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) o[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s0 = 0; s0 < ns; s0 += AHEAD) {
+    if (s0) take(s0);
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
       if (s0 + u < ns) {
