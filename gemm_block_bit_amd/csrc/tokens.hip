@@ -44,6 +44,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <utility>
 
 #include "attention_common.h"
 
@@ -113,6 +114,54 @@ __device__ __forceinline__ float row_max(float x) {
 __device__ __forceinline__ float row_sum(float x) {
   const float2 r = both(x);
   return r.x + r.y;
+}
+
+// f(0), f(1), ... as compile-time constants
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  unrolled(std::make_integer_sequence<int, N>(), f);
+}
+
+// Operands from LDS, awaited.  Written out because the compiler, where it sees
+// the reads, awaits every load to LDS before them, the next tile's among them.
+// Four pieces of 16 bytes at the offset OFF from four addresses;
+template <int OFF>
+__device__ __forceinline__ void read4(u32x4 (&x)[4], const uint32_t* at) {
+  asm volatile("ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+               "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF)
+               : "memory");
+}
+// transposed, four slots from OFF on and four from OFF + STEP on, of two or four
+// pieces: 16 lanes read 4 slots of 16 elements, and each gets an element of the four.
+template <int OFF, int STEP>
+__device__ __forceinline__ void read_turned(u32x4 (&x)[2], const uint32_t* at) {
+  u32x2 y[4];
+  asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+               "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+               : "v"(at[0]), "v"(at[1]), "n"(OFF), "n"(OFF + STEP)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x[i] = __builtin_shufflevector(y[2 * i], y[2 * i + 1], 0, 1, 2, 3);
+}
+template <int OFF, int STEP>
+__device__ __forceinline__ void read_turned(u32x4 (&x)[4], const uint32_t* at) {
+  u32x2 y[8];
+  asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+               "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+               "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+               "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3]), "=&v"(y[4]), "=&v"(y[5]), "=&v"(y[6]), "=&v"(y[7])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF), "n"(OFF + STEP)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __builtin_shufflevector(y[2 * i], y[2 * i + 1], 0, 1, 2, 3);
 }
 
 template <int DT, int CT, int D, int NW, bool TREE>
@@ -272,9 +321,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 
   // two tiles of K, then two of V
   constexpr int TILE = BN * ROW;
-  __shared__ __align__(16) uint8_t lds[4 * TILE];
-  uint8_t* const ks = lds;
-  uint8_t* const vs = lds + 2 * TILE;
+  __shared__ __align__(1024) uint8_t lds[4 * TILE];
   // Piece p (16 bytes) of slot r lies at p ^ swizzle(r): a slot a lane for K (8
   // lanes together hit 8 pieces), 4 slots of two pieces for V.
   constexpr int KS = PIECES < 16 ? PIECES - 1 : 15, VS = PIECES < 16 ? PIECES / 2 - 1 : 7;
@@ -298,42 +345,57 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     missing = __ballot(used && !there);
   };
   constexpr int TPP = 1024 / BN;               // tiles of 64 groups
-  u32x4 kr[NL], vr[NL];
-  const auto load = [&](const uint8_t* base, int j, int group) {
-    const int r = uniform((j * NW + wave) * RPI);            // first slot of the load within the tile
-    const int g = group + (r >> 4);
-    const size_t off = size_t(uint32_t(__builtin_amdgcn_readlane(off_hi, g))) << 32 | uint32_t(__builtin_amdgcn_readlane(off_lo, g));
-    return __builtin_amdgcn_raw_buffer_load_b128(span(base + off, __builtin_amdgcn_readlane(bytes, g)),
-                                                 (r & 15) * GROW + lane * 16, 0, 0);
-  };
-  // starts tile i on its way to registers; returns a bit for every missing group
+  // Starts tile i on its way: 16-bit elements straight to LDS (a load writes its
+  // lanes side by side, so each is given the piece that belongs there), e4m3 ones
+  // to registers, to be widened.  Returns a bit for every missing group.
+  u32x4 kr[F8 ? NL : 1], vr[F8 ? NL : 1];
   const auto fetch = [&](int i) {
     if (i % TPP == 0) locate(k0 + i * BN, i == 0 && from_zero ? early : page_of(k0 + i * BN + 16 * lane));
     const int group = (i % TPP) * (BN / 16);
 #pragma unroll
-    for (int j = 0; j < NL; ++j) kr[j] = load(a.k, j, group);
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
-    for (int j = 0; j < NL; ++j) vr[j] = load(a.v, j, group);
+      for (int j = 0; j < NL; ++j) {
+        const int r = uniform((j * NW + wave) * RPI);          // first slot of the load within the tile
+        const int g = group + (r >> 4);
+        const size_t off =
+            size_t(uint32_t(__builtin_amdgcn_readlane(off_hi, g))) << 32 | uint32_t(__builtin_amdgcn_readlane(off_lo, g));
+        const Span from = span((v ? a.v : a.k) + off, __builtin_amdgcn_readlane(bytes, g));
+        if constexpr (F8) {
+          (v ? vr : kr)[j] = __builtin_amdgcn_raw_buffer_load_b128(from, (r & 15) * GROW + lane * 16, 0, 0);
+        } else {
+          const int row = (r & 15) + lane / LPR, p = lane % LPR;
+          to_lds(from, row * GROW + (p ^ (v ? v_swizzle(row) : k_swizzle(row))) * 16,
+                 lds + (2 * v + (i & 1)) * TILE + r * ROW);
+        }
+      }
     return uniform(uint32_t(missing >> group) & ((1u << (BN / 16)) - 1));
   };
-  const auto keep = [&](const u32x4 (&x)[NL], uint8_t* to, auto swizzle, auto change) {
+  const auto widened = [&](const u32x4 (&x)[F8 ? NL : 1], uint8_t* to, auto swizzle) {
+    if constexpr (F8) {
 #pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      const int r = (j * NW + wave) * RPI + lane / LPR, p = lane % LPR;
-      if constexpr (F8) {
+      for (int j = 0; j < NL; ++j) {
+        const int r = (j * NW + wave) * RPI + lane / LPR, p = lane % LPR;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t w0 = x[j][2 * e], w1 = x[j][2 * e + 1];
           st16(to + r * ROW + ((2 * p + e) ^ swizzle(r)) * 16,
-               change(u32x4{H::template widen<false>(w0), H::template widen<true>(w0),
-                            H::template widen<false>(w1), H::template widen<true>(w1)}));
+               u32x4{H::template widen<false>(w0), H::template widen<true>(w0),
+                     H::template widen<false>(w1), H::template widen<true>(w1)});
         }
-      } else {
-        st16(to + r * ROW + (p ^ swizzle(r)) * 16, change(x[j]));
       }
     }
   };
-  const auto as_is = [](const u32x4& x) { return x; };
+  // tile i is in LDS for all waves, and all are done with the one before
+  const auto arrive = [&](int i) {
+    if constexpr (F8) {
+      widened(kr, lds + (i & 1) * TILE, k_swizzle);
+      widened(vr, lds + (2 + (i & 1)) * TILE, v_swizzle);
+    } else {
+      loads_left<0>();
+    }
+    __syncthreads();
+  };
   // A slot that some rows see and some do not may hold infinities or NaN: with
   // a weight of 0 they would reach the rows that do not see it.  So they are
   // left out of the product, and what they do to the rows that see them is found
@@ -345,44 +407,46 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     return x;
   };
   const auto mixed = [&](int i) { return k0 + i * BN < same_low || min(k0 + i * BN + BN, k1) > same_high; };
-  __shared__ int odd_tile[2];                  // the last tile of each buffer that has such elements
-  // tile i from the registers to LDS
-  const auto put_tile = [&](int i) {
-    uint8_t* const kt = ks + (i & 1) * TILE;
-    uint8_t* const vt = vs + (i & 1) * TILE;
-    keep(kr, kt, k_swizzle, as_is);
-    if (!mixed(i)) {
-      keep(vr, vt, v_swizzle, as_is);
-    } else {
-      bool odd = false;
-      keep(vr, vt, v_swizzle, [&](const u32x4& x) {
-        return elements(x, [&](uint32_t e) {
-          const bool bad = (e & EXP) == EXP;
-          odd |= bad;
-          return bad ? 0u : e;
-        });
-      });
-      if (odd) odd_tile[i & 1] = i;
+  __shared__ int odd_tile;                     // the last tile that has such elements
+  // f of every 16 bytes of V's tile i, in place where f says so
+  const auto each_piece = [&](int i, auto f) {
+#pragma unroll 1
+    for (int at = 16 * threadIdx.x; at < TILE; at += 16 * THREADS) {
+      uint8_t* const p = lds + (2 + (i & 1)) * TILE + at;
+      u32x4 x = ld16(p);
+      if (f(x)) st16(p, x);
     }
+  };
+  const auto clean = [&](int i) {
+    each_piece(i, [&](u32x4& x) {
+      bool odd = false;
+      x = elements(x, [&](uint32_t e) {
+        const bool bad = (e & EXP) == EXP;
+        odd |= bad;
+        return bad ? 0u : e;
+      });
+      if (odd) odd_tile = i;
+      return odd;
+    });
+    __syncthreads();
   };
 
   // This lane's addresses in LDS: K's slot c, V's slots 4 h + (lane % 16) / 4.
   // Other pieces of the slot differ in bits that the permutation leaves to an xor.
-  const int k_at = c * ROW + (h ^ k_swizzle(c)) * 16;
+  const uint32_t lds_at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  const uint32_t k_at = lds_at + c * ROW + (h ^ k_swizzle(c)) * 16;
   const int v_slot = 4 * h + ((lane & 15) >> 2);
-  const int v_at = 2 * TILE + v_slot * ROW + ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(v_slot)) * 16 + 8 * (lane & 1);
-  // K's elements 16 kc ... of the slots 32 e ..., as the A operand
-  const auto k_piece = [&](int kc, int e, int buffer) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(lds + ((k_at + buffer) ^ (kc % KA * 32)) + (kc / KA) * 256 + e * 32 * ROW);
-    return __builtin_bit_cast(V8, x);
-  };
-  // V's elements 32 j ... of the slots 16 s ..., as the A operand
-  const auto v_piece = [&](int j, int s, int buffer) {
-    typedef __attribute__((address_space(3))) i16x4* L;
-    const uint8_t* at = lds + ((v_at + buffer) ^ (j % VA * 64)) + (j / VA) * 256 + s * 16 * ROW;
-    const i16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)at);
-    const i16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(at + 8 * ROW));
-    return __builtin_bit_cast(V8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+  const uint32_t v_at = lds_at + 2 * TILE + v_slot * ROW +
+                        ((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ v_swizzle(v_slot)) * 16 + 8 * (lane & 1);
+  constexpr int VG = NT < 4 ? NT : 4;          // pieces of V that are read at once
+  // product(j, operand) for V's elements 32 j ... of the slots 16 s ... of a tile
+  const auto each_v = [&](const uint32_t (&at)[VA], auto S, auto product) {
+    unrolled<NT / VG>([&](auto G) {
+      u32x4 x[VG];
+      read_turned<decltype(S)::value * 16 * ROW + decltype(G)::value * 256, 8 * ROW>(x, at);
+#pragma unroll
+      for (int u = 0; u < VG; ++u) product(decltype(G)::value * VG + u, __builtin_bit_cast(V8, x[u]));
+    });
   };
 
   f32x16 o[NT];
@@ -390,27 +454,36 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
   float ref = -FLT_MAX, l = 0.f;
 
-  if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
-  uint32_t holes = fetch(0), holes_next = 0;
-  __syncthreads();
-  put_tile(0);
-  if (nt > 1) holes_next = fetch(1);
-  __syncthreads();
+  if (threadIdx.x == 0) odd_tile = -1;
+  uint32_t holes_next = fetch(0);
+#pragma unroll 1
   for (int i = 0; i < nt; ++i) {
+    arrive(i);
+    if (mixed(i)) clean(i);
+    const uint32_t holes = holes_next;
+    if (i + 1 < nt) holes_next = fetch(i + 1);
     const int key0 = k0 + i * BN, buffer = (i & 1) * TILE;
     const bool works = key0 < hi_wave && key0 + BN > lo_wave;
+    uint32_t v_pieces[VA];
+#pragma unroll
+    for (int u = 0; u < VA; ++u) v_pieces[u] = (v_at + buffer) ^ (u * 64);
     f32x16 s[NE];
     if (works) {
+      uint32_t k_pieces[KA];
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
+      for (int u = 0; u < KA; ++u) k_pieces[u] = (k_at + buffer) ^ (u * 32);
+      unrolled<NE>([&](auto E) {
+        constexpr int e = decltype(E)::value;
         s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        unrolled<KC / 4>([&](auto G) {
+          constexpr int kc = 4 * decltype(G)::value;
+          u32x4 x[4];
+          read4<e * 32 * ROW + kc / KA * 256>(x, k_pieces + kc % KA);
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) s[e] = H::mfma32(k_piece(kc, e, buffer), qf[kc], s[e]);
-      }
+          for (int u = 0; u < 4; ++u) s[e] = H::mfma32(__builtin_bit_cast(V8, x[u]), qf[kc + u], s[e]);
+        });
+      });
     }
-    uint32_t holes_after = 0;
-    if (i + 1 < nt) put_tile(i + 1);
-    if (i + 2 < nt) holes_after = fetch(i + 2);
     V8 part[PARTS][BN / 16];
     if (works) {
       // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
@@ -512,65 +585,77 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] *= f;
       }
+      // 16 slots at a time, so that exponentials are taken while the products
+      // of those before are formed
+      unrolled<BN / 16>([&](auto S) {
+        constexpr int t = decltype(S)::value;
 #pragma unroll
-      for (int e = 0; e < NE; ++e)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], unit, -ref));
+        for (int r = 0; r < 8; ++r) {
+          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + r], unit, -ref));
           l += p;
 #pragma unroll
           for (int x = 0; x < PARTS; ++x) {
             const T y = T(p);
-            part[x][2 * e + r / 8][r % 8] = y;
+            part[x][t][r] = y;
             p -= float(y);   // exact
           }
         }
+        each_v(v_pieces, S, [&](int j, const V8& x) {
 #pragma unroll
-      for (int s = 0; s < BN / 16; ++s)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const V8 x = v_piece(j, s, buffer);
-#pragma unroll
-          for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][s], o[j]);
-        }
+          for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][t], o[j]);
+        });
+      });
     }
-    if (mixed(i) && uniform(odd_tile[i & 1]) == i) {
-      // rare: V of the tile once more, from memory
+    if (mixed(i) && uniform(odd_tile) == i) {
+      // rare: infinities of either sign, from V as memory has it
       const int p = page_of(key0 + 16 * min(lane, BN / 16 - 1));
 #pragma unroll 1
       for (int negative = 0; negative < 2; ++negative) {
-        u32x4 x[NL];
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-          const int r = uniform((j * NW + wave) * RPI);
-          const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + (r & ~15);
+        __syncthreads();
+#pragma unroll 1
+        for (int r = wave * 16; r < BN; r += 16 * NW) {        // 16 slots of a page a wave
+          const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + r;
           const bool there = unsigned(page) < unsigned(a.num_pages);
           const size_t off = (size_t(there ? page : 0) * a.Hkv + hk) * page_bytes + size_t(slot & pmask) * GROW;
-          x[j] = __builtin_amdgcn_raw_buffer_load_b128(span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0)),
-                                                       (r & 15) * GROW + lane * 16, 0, 0);
+          const Span from = span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0));
+#pragma unroll 1
+          for (int q = lane; q < 16 * (D / 8); q += 64) {      // a piece of 8 elements a lane
+            const int row = q / (D / 8), piece = q % (D / 8);
+            u32x4 x;
+            if constexpr (F8) {
+              const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(from, row * GROW + piece * 8, 0, 0);
+              x = u32x4{H::template widen<false>(y[0]), H::template widen<true>(y[0]),
+                        H::template widen<false>(y[1]), H::template widen<true>(y[1])};
+            } else {
+              x = __builtin_amdgcn_raw_buffer_load_b128(from, row * GROW + piece * 16, 0, 0);
+            }
+            x = elements(x, [=](uint32_t e) {   // 1 where an element is an infinity of that sign or NaN
+              return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
+            });
+            st16(lds + 2 * TILE + buffer + (r + row) * ROW + (piece ^ v_swizzle(r + row)) * 16, x);
+          }
         }
         __syncthreads();
-        keep(x, vs + buffer, v_swizzle, [&](const u32x4& x) {
-          return elements(x, [=](uint32_t e) {   // 1 where an element is an infinity of that sign or NaN
-            return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
-          });
-        });
-        __syncthreads();
-        if (works)
+        if (works) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            f32x16 hit = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          for (int j0 = 0; j0 < NT; j0 += VG) {
+            f32x16 hit[VG];
 #pragma unroll
-            for (int s = 0; s < BN / 16; ++s) hit = H::mfma32(v_piece(j, s, buffer), part[0][s], hit);
+            for (int j = 0; j < VG; ++j) hit[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            unrolled<BN / 16>([&](auto S) {
+              each_v(v_pieces, S, [&](int j, const V8& x) {
+                if (j >= j0 && j < j0 + VG) hit[j - j0] = H::mfma32(x, part[0][decltype(S)::value], hit[j - j0]);
+              });
+            });
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (hit[r] > 0.f) o[j][r] += negative ? -INFINITY : INFINITY;
+            for (int j = 0; j < VG; ++j)
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (hit[j][r] > 0.f) o[j0 + j][r] += negative ? -INFINITY : INFINITY;
           }
+        }
       }
     }
-    holes = holes_next;
-    holes_next = holes_after;
-    __syncthreads();
   }
 
   l = row_sum(l);
