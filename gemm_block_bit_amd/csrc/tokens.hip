@@ -777,7 +777,12 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   TokensPlan p;
   const int G = Hq / c.kv_heads;
   const int64_t rows = int64_t(T) * G;         // of a kv head
-  p.waves = rows <= int64_t(64) * B ? 2 : 4;
+  const int64_t cus = device_compute_units();
+  // Two waves a workgroup where a sequence has few rows and there are sequences
+  // enough for the cache's bytes to bound the call (32 ragged of up to 8192
+  // slots, 8 tokens of 32 / 8 heads each: 130 us, 146 with four; with few, four
+  // stage a tile in half the time: 1 of 4000, 2 tokens: 29 and 23.5).
+  p.waves = rows <= int64_t(64) * B && 2 * int64_t(B) * c.kv_heads >= cus ? 2 : 4;
   p.rows = 32 * p.waves;
   p.tiles = int(std::min<int64_t>(rows / p.rows + B, INT_MAX));
   // slots from the first to the last that a row tile may see
@@ -785,13 +790,24 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   if (window && tree_words) most = std::min<int64_t>(most, int64_t(window) + 32 * int64_t(tree_words) + 15);
   else if (window) most = std::min<int64_t>(most, 2 * int64_t(window) + p.rows + 15);
   else most = most + 15;
-  const int64_t cus = device_compute_units(), groups = int64_t(p.tiles) * c.kv_heads;
-  int64_t chunk = (most + 63) & ~int64_t(63);
-  if (groups < 2 * cus && groups <= kMaxArrived) {
-    const int64_t want = std::min<int64_t>(kMaxJoin, (2 * cus + groups - 1) / groups);
-    chunk = std::max<int64_t>(256, ((most + want - 1) / want + 63) & ~int64_t(63));
+  // Runs.  Two workgroups a CU are resident; a run costs about 15 us beside its
+  // slots (25 us of 64 tiles' 80), its join 0.6.  With fewer row tiles than that:
+  // as many runs as make four a CU, of 384 to 2048 slots (32 of 300 x 4 tokens
+  // behind up to 4000: 55 us in 1024, 73 in 2048; 8 tiles of 4000: 27 in 384, 29
+  // in 256, 32 in 768; 136 of 8192: 94 in 2048, 105 in 1024, 135 in 4096).  With more, a single sequence's tiles
+  // balance by themselves, since those that see most start first; those of several
+  // may be of any length: runs of up to 4096 (16 trees of 64 behind up to 16384:
+  // 283, whole 500; behind 8192 each 354 and 337).
+  const int64_t groups = int64_t(p.tiles) * c.kv_heads;
+  int64_t chunk = most;
+  if (groups <= kMaxArrived) {
+    if (groups < 2 * cus) chunk = std::min<int64_t>(2048, std::max<int64_t>(384, most * groups / (4 * cus)));
+    else if (B > 1) chunk = 4096;
+    chunk = std::max(chunk, (most + kMaxJoin - 1) / kMaxJoin);
+    const int64_t runs = (most + chunk - 1) / chunk;   // of one size
+    chunk = (most + runs - 1) / runs;
   }
-  p.chunk = int(std::min<int64_t>(chunk, INT_MAX & ~63));
+  p.chunk = int(std::min<int64_t>((chunk + 63) & ~int64_t(63), INT_MAX & ~63));
   p.nsplit = int(std::max<int64_t>(1, (most + p.chunk - 1) / p.chunk));
   const size_t parts = p.nsplit > 1 ? size_t(groups) * p.nsplit * p.rows : 0;
   p.ml_off = parts ? GBB_ATTENTION_COUNTERS : 0;
