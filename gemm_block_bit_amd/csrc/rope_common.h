@@ -76,6 +76,8 @@ __device__ __forceinline__ void store_cache(void* base, size_t at, const float (
     uint8_t* p = static_cast<uint8_t*>(base) + at;
     if constexpr (E == 8) {
       *reinterpret_cast<uint2*>(p) = make_uint2(e4m3_pair2(x, scale), e4m3_pair2(x + 4, scale));
+    } else if constexpr (E == 4) {
+      *reinterpret_cast<uint32_t*>(p) = e4m3_pair2(x, scale);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
