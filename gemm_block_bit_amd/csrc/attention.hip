@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * waves(WIDE), WIDE || D == 256 ? 2 : D == 128 ?
       if constexpr (OPT) {
         if (a.cap > 0.f) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s[e][r] = capped<false>(s[e][r], over, a.cap);
+          for (int r = 0; r < 4; ++r) s[e][r] = capped(s[e][r], over, a.cap);
         }
         if (a.slopes) {
 #pragma unroll

@@ -80,19 +80,15 @@ __device__ __forceinline__ float2 get(const float* p) {
 }
 
 // The capped score cap tanh(x / cap) in the log2 domain: x comes times
-// log2(e), and so does the result; out = cap log2(e).  tanh(y) = 1 - 2 / (1 +
-// e^2y) loses digits where y is small: its error is below 2^-22 of the cap.
-// Up to kShortCap that is at most 2e-5 of a score's exponential, below a
+// log2(e), and so does the result; out = cap log2(e), over = 1 / out.  tanh(y) =
+// 1 - 2 / (1 + e^2y) loses digits where y is small: its error is below 2^-22 of
+// the cap.  Up to kShortCap that is at most 2e-5 of a score's exponential, below a
 // hundredth of what rounding an output to 16 bits takes; above, arguments below
 // 0.35 take the series (its first term left out is below 2^-25 of the result).
 constexpr float kShortCap = 80.f;
-template <bool SHORT>
 __device__ __forceinline__ float capped(float x, float over, float out) {
-  const float y = x * over;   // over = 1 / out
-  const float e = __builtin_amdgcn_exp2f(y * (2.f * kLog2e));
-  const float t = __builtin_fmaf(-2.f * out, __builtin_amdgcn_rcpf(e + 1.f), out);
-  if (SHORT) return t;
-  const float y2 = y * y;
+  const float y = x * over, y2 = y * y;
+  const float t = __builtin_fmaf(-2.f * out, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y * (2.f * kLog2e)) + 1.f), out);
   const float p = y * out * (1.f + y2 * (-1.f / 3.f + y2 * (2.f / 15.f + y2 * (-17.f / 315.f + y2 * (62.f / 2835.f - y2 * (1382.f / 155925.f))))));
   return fabsf(y) < 0.35f ? p : t;
 }

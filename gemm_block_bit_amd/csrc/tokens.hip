@@ -100,6 +100,8 @@ __device__ __forceinline__ int wave_max(int x) {
   for (int i = 1; i < 32; i *= 2) x = max(x, __shfl_xor(x, i));
   return x;
 }
+// n ones from bit 0 on, all or none where n is outside a word
+__device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1; }
 // Both lanes' values of a row.
 __device__ __forceinline__ float2 both(float x) {
   const uint32_t bits = __builtin_bit_cast(uint32_t, x);
@@ -162,6 +164,15 @@ __device__ __forceinline__ void read_turned(u32x4 (&x)[4], const uint32_t* at) {
                : "memory");
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = __builtin_shufflevector(y[2 * i], y[2 * i + 1], 0, 1, 2, 3);
+}
+
+// The kernel's arguments, read again where this is called: what is not needed
+// in the loop over tiles would fill the scalar registers there.
+typedef __attribute__((address_space(4))) const Args* LateArgs;
+__device__ __forceinline__ LateArgs late_args() {
+  uintptr_t p = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(p));
+  return reinterpret_cast<LateArgs>(p);
 }
 
 template <int DT, int CT, int D, int NW, bool TREE>
@@ -228,17 +239,19 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const int row = r0 + 32 * wave + c;
   const bool real = row < rows_all;
   const int token = real ? row / a.G : 0, hq = hk * a.G + (real ? row - token * a.G : 0);
-  const size_t t = size_t(t0 + token);
-
+  const int t = t0 + token;
   // q, the B operand: row c, elements 16 kc + 8 h ...; and the first pages of the
   // run, where it is known by now that they will be asked for (else of no use)
   u32x4 qw[KC];
 #pragma unroll
   for (int kc = 0; kc < KC; ++kc) {
     qw[kc] = u32x4{0, 0, 0, 0};
-    if (real) qw[kc] = ld16(static_cast<const uint16_t*>(a.q) + t * a.q_token + size_t(hq) * D + 16 * kc + 8 * h);
+    if (real) qw[kc] = ld16(static_cast<const uint16_t*>(a.q) + int64_t(t) * a.q_token + size_t(hq) * D + 16 * kc + 8 * h);
   }
-  const auto page_of = [&](int slot) { return a.block_table[size_t(b) * a.max_pages + (min(slot, a.max_len - 1) >> a.pshift)]; };
+  const auto page_of = [&](int slot) {
+    const LateArgs x = late_args();
+    return x->block_table[size_t(b) * x->max_pages + (min(slot, x->max_len - 1) >> x->pshift)];
+  };
   const bool from_zero = !a.first && !a.window;
   const int early = page_of(min(int64_t(sp) * a.chunk, int64_t(a.max_len)) + 16 * lane);
   in_order();
@@ -247,19 +260,19 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   // bit is set, from `first` on and less than `window` away.  place: where
   // distances to slots before the new ones count from.
   int lo = 0, hi, place = ctx + token, first = 0, drafted = 0;
-  const uint32_t* words = nullptr;
+  // word i of the row's tree, without bits that do not count
+  const auto tree_word = [&](int i) {
+    if (i < 0 || i >= a.tree_words) return 0u;
+    return a.tree[size_t(t) * a.tree_words + i] & uint32_t(below(n - 32 * i));
+  };
   if (a.first) first = max(0, a.first[t]);
   if constexpr (TREE) {
-    words = a.tree + t * a.tree_words;
     for (int i0 = 0; i0 < a.tree_words; i0 += 4) {
       uint32_t x[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = words[min(i0 + u, a.tree_words - 1)];
+      for (int u = 0; u < 4; ++u) x[u] = tree_word(i0 + u);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int left = i0 + u < a.tree_words ? n - 32 * (i0 + u) : 0;
-        drafted += left <= 0 ? 0 : __popc(left < 32 ? x[u] & ((1u << left) - 1) : x[u]);
-      }
+      for (int u = 0; u < 4; ++u) drafted += __popc(x[u]);
     }
     place = ctx + drafted - 1;
     hi = ctx;
@@ -297,9 +310,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   k_high = uniform(k_high);
   same_low = uniform(same_low);                // all rows of the workgroup see the slots from
   same_high = uniform(same_high);              // same_low up to same_high
-  const size_t head = t * a.Hq + hq;
   if (k_low >= k_high) {                       // no row sees a slot
     if (sp == 0 && real) {
+      const size_t head = size_t(t) * a.Hq + hq;
       for (int d = 8 * h; d < D; d += 16) st16(static_cast<T*>(a.out) + head * D + d, u32x4{0, 0, 0, 0});
       if (a.lse && h == 0) a.lse[head] = -INFINITY;
     }
@@ -308,6 +321,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   k_low &= ~15;
   const int k0 = k_low + sp * a.chunk;
   if (k0 >= k_high) return;
+  // what is needed after the tiles
+  __shared__ int saved[4];
+  if (threadIdx.x == 0) {
+    saved[0] = t0;
+    saved[1] = r0;
+    saved[2] = rows_all;
+    saved[3] = (k_high - k_low - 1) / a.chunk + 1;
+  }
   const int k1 = k0 + min(k_high - k0, a.chunk);
   const int nt = (k1 - k0 + BN - 1) / BN;
 
@@ -317,7 +338,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const float scale = F8 && a.k_scale ? a.scale * a.k_scale[hk] : a.scale;
   const float over = a.cap > 0.f ? 1.f / a.cap : 0.f;
   const float slope = a.slopes ? a.slopes[hq] * kLog2e : 0.f;
-  const bool shaped = a.cap > 0.f || a.slopes;
+  enum { PLAIN, SHORT_CAP, BIAS, OTHER };
+  const int shape = a.cap > 0.f ? a.slopes || a.cap > kShortCap * kLog2e ? OTHER : SHORT_CAP : a.slopes ? BIAS : PLAIN;
+  // slots up to this are behind every row of the wave (of a tree: before all new ones)
+  const int place_low = uniform(min(wave_min(real ? place : INT_MAX), TREE ? ctx - 1 : INT_MAX));
 
   // two tiles of K, then two of V
   constexpr int TILE = BN * ROW;
@@ -331,14 +355,17 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   // Where 64 groups of 16 slots lie, a group a lane: bytes from the cache's
   // start, bytes that take part (none of a page that is not there), and a bit
   // for every page that should be there and is not.
-  const int pmask = (1 << a.pshift) - 1;
-  const size_t page_bytes = (size_t(1) << a.pshift) * GROW;
+  // (bytes from the cache's start of a slot of page p)
+  const auto place_of_slot = [&](int p, int slot) {
+    const LateArgs x = late_args();
+    return ((size_t(p) * x->Hkv + hk) << x->pshift) * GROW + size_t(slot & ((1 << x->pshift) - 1)) * GROW;
+  };
   int off_lo, off_hi, bytes;
   uint64_t missing;
   const auto locate = [&](int first_slot, int p) {
     const int key = first_slot + 16 * lane;
-    const bool used = key < k1, there = used && unsigned(p) < unsigned(a.num_pages);
-    const size_t off = there ? (size_t(p) * a.Hkv + hk) * page_bytes + size_t(key & pmask) * GROW : 0;
+    const bool used = key < k1, there = used && unsigned(p) < unsigned(late_args()->num_pages);
+    const size_t off = there ? place_of_slot(p, key) : 0;
     off_lo = int(uint32_t(off));
     off_hi = int(uint32_t(off >> 32));
     bytes = there ? min(k1 - key, 16) * GROW : 0;
@@ -352,22 +379,22 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const auto fetch = [&](int i) {
     if (i % TPP == 0) locate(k0 + i * BN, i == 0 && from_zero ? early : page_of(k0 + i * BN + 16 * lane));
     const int group = (i % TPP) * (BN / 16);
+    // load j of the wave takes slots from STEP j + first on: within 16 of them that
+    // the compiler can tell where `first` adds nothing across them
+    constexpr int STEP = NW * RPI;
+    static_assert(STEP % 16 == 0 || 16 % STEP == 0, "a load's 16 slots follow from j and the wave apart");
+    const int first = wave * RPI, row = first % 16 + lane / LPR, p = lane % LPR;
 #pragma unroll
     for (int v = 0; v < 2; ++v)
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const int r = uniform((j * NW + wave) * RPI);          // first slot of the load within the tile
-        const int g = group + (r >> 4);
-        const size_t off =
-            size_t(uint32_t(__builtin_amdgcn_readlane(off_hi, g))) << 32 | uint32_t(__builtin_amdgcn_readlane(off_lo, g));
+        const int g = group + j * STEP / 16 + (STEP > 16 ? first / 16 : 0), r = j * STEP % 16 + row;
+        const uint64_t off = __builtin_bit_cast(uint64_t, u32x2{uint32_t(__builtin_amdgcn_readlane(off_lo, g)),
+                                                                uint32_t(__builtin_amdgcn_readlane(off_hi, g))});
         const Span from = span((v ? a.v : a.k) + off, __builtin_amdgcn_readlane(bytes, g));
-        if constexpr (F8) {
-          (v ? vr : kr)[j] = __builtin_amdgcn_raw_buffer_load_b128(from, (r & 15) * GROW + lane * 16, 0, 0);
-        } else {
-          const int row = (r & 15) + lane / LPR, p = lane % LPR;
-          to_lds(from, row * GROW + (p ^ (v ? v_swizzle(row) : k_swizzle(row))) * 16,
-                 lds + (2 * v + (i & 1)) * TILE + r * ROW);
-        }
+        if constexpr (F8) (v ? vr : kr)[j] = __builtin_amdgcn_raw_buffer_load_b128(from, r * GROW + p * 16, 0, 0);
+        else to_lds(from, r * GROW + (p ^ (v ? v_swizzle(r) : k_swizzle(r))) * 16,
+                    lds + (2 * v + (i & 1)) * TILE + first * ROW + j * STEP * ROW);
       }
     return uniform(uint32_t(missing >> group) & ((1u << (BN / 16)) - 1));
   };
@@ -386,15 +413,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       }
     }
   };
-  // tile i is in LDS for all waves, and all are done with the one before
-  const auto arrive = [&](int i) {
-    if constexpr (F8) {
-      widened(kr, lds + (i & 1) * TILE, k_swizzle);
-      widened(vr, lds + (2 + (i & 1)) * TILE, v_swizzle);
-    } else {
-      loads_left<0>();
-    }
-    __syncthreads();
+  // tile i from the registers to LDS (e4m3)
+  const auto widen_tile = [&](int i) {
+    widened(kr, lds + (i & 1) * TILE, k_swizzle);
+    widened(vr, lds + (2 + (i & 1)) * TILE, v_swizzle);
   };
   // A slot that some rows see and some do not may hold infinities or NaN: with
   // a weight of 0 they would reach the rows that do not see it.  So they are
@@ -458,7 +480,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   uint32_t holes_next = fetch(0);
 #pragma unroll 1
   for (int i = 0; i < nt; ++i) {
-    arrive(i);
+    // tile i is in LDS for all waves, and all are done with the one before
+    if (F8) widen_tile(i);
+    else loads_left<0>();
+    __syncthreads();
     if (mixed(i)) clean(i);
     const uint32_t holes = holes_next;
     if (i + 1 < nt) holes_next = fetch(i + 1);
@@ -489,49 +514,62 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
       const int key = key0 + 4 * h;
       const auto slot = [](int e, int r) { return 32 * e + 8 * (r / 4) + r % 4; };
-      float unit = scale;
+      // scores are s times unit plus offset
+      float unit = scale, offset = 0.f;
       const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
-      uint32_t bits[NE];                       // of drafted slots, as the lane's registers have them: bit 8 (r / 4) + r % 4
+      // With a tree: bit j of the slot key0 + j that is a new token which the row's
+      // tree has, and how many of those lie behind the tile.
       const bool branches = TREE && key0 + BN > ctx;
-      int beyond = 0;                          // visible drafted slots behind the tile
-      if (branches) {
+      uint64_t bits = 0;
+      int beyond = 0;
+      if (branches && real) {
+        const int from = key0 - ctx, i0 = from >> 5, end = from + BN;   // end above 0
+        uint32_t x[3];
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          const int at = key0 + 32 * e - ctx;  // the drafted slot of bit 0
-          uint64_t x = 0;
-          const int i0 = at >> 5;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int i = i0 + u, left = n - 32 * i;
-            if (real && i >= 0 && i < a.tree_words && left > 0)
-              x |= uint64_t(left < 32 ? words[i] & ((1u << left) - 1) : words[i]) << (32 * u);
-          }
-          bits[e] = uint32_t(x >> (at & 31));
-        }
-        int upto = 0;
-        if (real) {
-          const int end = key0 + BN - ctx;     // above 0
-          for (int i = 0; i < a.tree_words && 32 * i < end; ++i) {
-            const int left = min(n, end) - 32 * i;
-            if (left > 0) upto += __popc(left < 32 ? words[i] & ((1u << left) - 1) : words[i]);
-          }
-        }
-        beyond = drafted - upto;
+        for (int u = 0; u < 3; ++u) x[u] = tree_word(i0 + u);
+        const uint64_t low = uint64_t(x[1]) << 32 | x[0], high = uint64_t(x[2]) << 32 | x[1];
+        const int shift = from & 31;
+        bits = (low >> shift & 0xffffffffu) | (high >> shift) << 32;
+        if (BN == 32) bits &= 0xffffffffu;
+        beyond = drafted;
+        for (int i = 0; 32 * i < end; ++i) beyond -= __popc(tree_word(i) & uint32_t(below(end - 32 * i)));
       }
-      if (shaped) {
+      // (The usual shapes each in one branch of their own: where branches follow
+      // each other the scores are copied in those that are not taken, 64 and more
+      // registers a tile.)
+      const auto cap_short = [&](float x) {    // tanh(x / cap) / 2 - 1 / 2 = -1 / (1 + e^(2 x / cap))
+        return __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x * (scale * over * (2.f * kLog2e))));
+      };
+      if (shape == SHORT_CAP) {
+        unit = 2.f * a.cap;
+        offset = a.cap;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[e][r] = cap_short(s[e][r]);
+      } else if (shape == BIAS && key0 + BN <= place_low + 1) {   // no slot lies ahead of a row
+        const float base = -slope * float(place - key);
         unit = 1.f;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) s[e] *= scale;
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            s[e][r] = __builtin_fmaf(s[e][r], scale, __builtin_fmaf(slope, float(slot(e, r)), base));
+      } else if (shape != PLAIN) {
+        unit = 1.f;
         if (a.cap > kShortCap * kLog2e) {
 #pragma unroll
           for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[e][r] = capped<false>(s[e][r], over, a.cap);
+            for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r] * scale, over, a.cap);
         } else if (a.cap > 0.f) {
 #pragma unroll
           for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[e][r] = capped<true>(s[e][r], over, a.cap);
+            for (int r = 0; r < 16; ++r) s[e][r] = __builtin_fmaf(2.f * a.cap, cap_short(s[e][r]), a.cap);
+        } else {
+#pragma unroll
+          for (int e = 0; e < NE; ++e) s[e] *= scale;
         }
         if (a.slopes) {
           const float from = float(place - key);
@@ -540,44 +578,39 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               float far = fabsf(from - float(slot(e, r)));
-              if (branches && key + slot(e, r) >= ctx) {
-                const int at = slot(0, r) + 4 * h;
-                int after = __popc(at < 31 ? bits[e] >> (at + 1) : 0u) + beyond;
-#pragma unroll
-                for (int f = e + 1; f < NE; ++f) after += __popc(bits[f]);
-                far = float(after);
-              }
+              if (branches && key + slot(e, r) >= ctx)
+                far = float(beyond + __popcll(bits >> (4 * h) >> slot(e, r) >> 1));
               s[e][r] = __builtin_fmaf(-slope, far, s[e][r]);
             }
         }
       }
       if (!whole) {
+        // bit j: the row sees the slot key0 + j
+        uint64_t seen = below(min(hi, k1) - key0) & ~below(lo - key0);
+        if (branches) {
+          uint64_t x = bits;
+          if (a.window)   // the nearest ones: those with fewer behind them
+            for (int more = beyond + __popcll(x) - a.window; more > 0 && x; --more) x &= x - 1;
+          seen |= x & below(k1 - key0) & ~below(first - key0);
+        }
+        if (holes) {
+#pragma unroll
+          for (int g = 0; g < BN / 16; ++g)
+            if (holes >> g & 1u) seen &= ~(uint64_t(0xffff) << (16 * g));
+        }
+        seen >>= 4 * h;
+        const uint32_t part[2] = {uint32_t(seen), uint32_t(seen >> 32)};
 #pragma unroll
         for (int e = 0; e < NE; ++e)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = key + slot(e, r);
-            bool seen = j >= lo && j < hi && j < k1;
-            if (branches && j >= ctx) {
-              const int at = slot(0, r) + 4 * h;
-              seen = j < k1 && j >= first && (bits[e] >> at & 1u);
-              if (a.window) {
-                int after = __popc(at < 31 ? bits[e] >> (at + 1) : 0u) + beyond;
-#pragma unroll
-                for (int f = e + 1; f < NE; ++f) after += __popc(bits[f]);
-                seen = seen && after < a.window;
-              }
-            }
-            if (holes >> (2 * e + r / 8) & 1u) seen = false;
-            s[e][r] = seen ? s[e][r] : -INFINITY;
-          }
+          for (int r = 0; r < 16; ++r) s[e][r] = part[e] >> slot(0, r) & 1u ? s[e][r] : -INFINITY;
       }
       float mx = -INFINITY;
 #pragma unroll
       for (int e = 0; e < NE; ++e)
 #pragma unroll
         for (int r = 0; r < 16; r += 2) mx = fmaxf(fmaxf(s[e][r], s[e][r + 1]), mx);
-      mx = row_max(mx) * unit;
+      mx = __builtin_fmaf(row_max(mx), unit, offset);
       if (__any(mx > ref + kLimit)) {
         const float to = mx > ref + kLimit ? mx - kShift : ref, f = __builtin_amdgcn_exp2f(ref - to);
         ref = to;
@@ -585,13 +618,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] *= f;
       }
+      const float under = offset - ref;
       // 16 slots at a time, so that exponentials are taken while the products
       // of those before are formed
       unrolled<BN / 16>([&](auto S) {
         constexpr int t = decltype(S)::value;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + r], unit, -ref));
+          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + r], unit, under));
           l += p;
 #pragma unroll
           for (int x = 0; x < PARTS; ++x) {
@@ -615,8 +649,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
 #pragma unroll 1
         for (int r = wave * 16; r < BN; r += 16 * NW) {        // 16 slots of a page a wave
           const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + r;
-          const bool there = unsigned(page) < unsigned(a.num_pages);
-          const size_t off = (size_t(there ? page : 0) * a.Hkv + hk) * page_bytes + size_t(slot & pmask) * GROW;
+          const bool there = unsigned(page) < unsigned(late_args()->num_pages);
+          const size_t off = place_of_slot(there ? page : 0, slot);
           const Span from = span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0));
 #pragma unroll 1
           for (int q = lane; q < 16 * (D / 8); q += 64) {      // a piece of 8 elements a lane
@@ -659,23 +693,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   }
 
   l = row_sum(l);
-  const int ns = (k_high - k_low - 1) / a.chunk + 1;
+  const LateArgs x = late_args();
+  const int ns = uniform(saved[3]);
+  const int last_row = uniform(saved[1]) + 32 * wave + c;
+  const bool writes = last_row < uniform(saved[2]);
   // out and lse of this lane's row from the output's pieces (4 elements each)
-  const float vscale = F8 && a.v_scale ? a.v_scale[hk] : 1.f;
+  const float vscale = F8 && x->v_scale ? x->v_scale[hk] : 1.f;
   const auto finish = [&](float ref, float l) {
-    if (!real) return;
+    if (!writes) return;
+    const int G = x->G, token = last_row / G;
+    const size_t head = size_t(uniform(saved[0]) + token) * x->Hq + hk * G + (last_row - token * G);
     const float f = l == 0.f ? 0.f : vscale / l;
     typedef T V4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        V4 x;
+        V4 y;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = T(l == 0.f ? 0.f : o[j][r + u] * f);
-        *reinterpret_cast<V4*>(static_cast<T*>(a.out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = x;
+        for (int u = 0; u < 4; ++u) y[u] = T(l == 0.f ? 0.f : o[j][r + u] * f);
+        *reinterpret_cast<V4*>(static_cast<T*>(x->out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = y;
       }
-    if (a.lse && h == 0) a.lse[head] = l == 0.f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * kLn2;
+    if (x->lse && h == 0) x->lse[head] = l == 0.f ? -INFINITY : (ref + __builtin_amdgcn_logf(l)) * kLn2;
   };
   if (ns == 1) {
     finish(ref, l);
@@ -685,33 +724,34 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   // Partial results, as the lanes hold them: piece by piece, 16 bytes a lane.
   // At device scope and awaited before the count (as in attention.hip, where
   // the reasons stand); the last workgroup joins them in the order of the runs.
-  const size_t run0 = (size_t(w) * a.Hkv + hk) * a.nsplit;
+  const int tile_of_call = uniform(int(blockIdx.x) / x->Hkv % x->tiles), run = uniform(int(blockIdx.x) / x->Hkv / x->tiles);
+  const size_t run0 = (size_t(tile_of_call) * x->Hkv + hk) * x->nsplit;
   constexpr int DEVICE = 16;                   // the cache policy of device scope
-  const auto run_at = [&](int s) { return span(a.o + (run0 + s) * (ROWS * D), ROWS * D * 4); };
-  const auto ml_at = [&](int s) { return reinterpret_cast<float*>(a.ml + (run0 + s) * ROWS + 32 * wave + c); };
+  const auto run_at = [&](int s) { return span(x->o + (run0 + s) * (ROWS * D), ROWS * D * 4); };
+  const auto ml_at = [&](int s) { return reinterpret_cast<float*>(x->ml + (run0 + s) * ROWS + 32 * wave + c); };
   const int at = (wave * (4 * NT) * 64 + lane) * 16;
-  if (real) {
-    const Span to = run_at(sp);
+  if (writes) {
+    const Span to = run_at(run);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        const f32x4 x = {o[j][r], o[j][r + 1], o[j][r + 2], o[j][r + 3]};
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, at + (4 * j + r / 4) * 1024, 0, DEVICE);
+        const f32x4 y = {o[j][r], o[j][r + 1], o[j][r + 2], o[j][r + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), to, at + (4 * j + r / 4) * 1024, 0, DEVICE);
       }
-    if (h == 0) put(ml_at(sp), ref, l);
+    if (h == 0) put(ml_at(run), ref, l);
   }
   __shared__ unsigned count;
   loads_left<0>();
   __syncthreads();
-  unsigned* arrived = a.arrived + w * a.Hkv + hk;
+  unsigned* arrived = x->arrived + tile_of_call * x->Hkv + hk;
   if (threadIdx.x == 0) count = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (count != unsigned(ns - 1)) return;
   if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!real) return;
+  if (!writes) return;
   constexpr int AHEAD = 2;                     // runs whose pieces are under way at once
-  u32x4 x[AHEAD][4 * NT];
+  u32x4 pieces[AHEAD][4 * NT];
   float2 e[AHEAD];
   const auto take = [&](int s0) {
 #pragma unroll
@@ -719,7 +759,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       const Span from = run_at(min(s0 + u, ns - 1));
       e[u] = get(ml_at(min(s0 + u, ns - 1)));
 #pragma unroll
-      for (int i = 0; i < 4 * NT; ++i) x[u][i] = __builtin_amdgcn_raw_buffer_load_b128(from, at + i * 1024, 0, DEVICE);
+      for (int i = 0; i < 4 * NT; ++i) pieces[u][i] = __builtin_amdgcn_raw_buffer_load_b128(from, at + i * 1024, 0, DEVICE);
     }
   };
   float high = -FLT_MAX;
@@ -743,7 +783,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
         l += f * e[u].y;
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i) {
-          const f32x4 y = __builtin_bit_cast(f32x4, x[u][i]);
+          const f32x4 y = __builtin_bit_cast(f32x4, pieces[u][i]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[i / 4][4 * (i % 4) + r] = __builtin_fmaf(f, y[r], o[i / 4][4 * (i % 4) + r]);
         }
