@@ -45,11 +45,17 @@
 // weights the scores are stored too (fp32), and exp(s - max) / sum is added
 // over the kv head's query heads, one thread a slot, without atomics.
 //
+// Scores may be capped, biased by distance or cut to a window (OPT, kernels of
+// their own, so that plain calls keep theirs): a cap is an exponential and a
+// reciprocal a score more, a bias one multiply-add, and a window moves the first
+// slot of the runs, so that what lies before it is not read.
+//
 // Measured: 32 sequences of up to 8192 slots (64 / 8 heads of 128, bf16,
 // 523 MB) 103 us, 5.1 TB/s; 2 of 131072 (32 / 8, e4m3, 537 MB) 100 us, 5.4
 // TB/s; a plain read kernel reaches 5.2 to 5.5 TB/s here.  1 of 1000 slots (32
 // / 8, fp16) 7 us, a chain of dependent steps: launch, page, K and V, scores,
-// the joins in the workgroup and over the runs.
+// the joins in the workgroup and over the runs; with a bias 9.1 a call, eager.
+// 32 of up to 16384 with a cap and a window of 4096 (64 / 8, bf16, 464 MB) 92 us.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -64,7 +70,6 @@ constexpr float kShift = 14.f;   // see above: 2^14 < 65504
 constexpr int kMaxJoin = 64;     // runs that the last workgroup of a sequence joins itself
 constexpr int kMaxArrived = GBB_ATTENTION_COUNTERS / 4;   // counters of such sequences, at the workspace's start
 constexpr int kMaxChunk = 4096;  // two page entries of a tile a lane: 32 tiles x 4 waves x 32 slots
-
 
 // N pieces of 16 bytes from LDS, at the byte offsets at[] plus OFF, awaited.
 // Written out because the compiler, where it sees the reads, awaits every

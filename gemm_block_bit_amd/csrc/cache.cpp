@@ -358,9 +358,10 @@ extern "C" size_t gbb_paged_attention_options_workspace(const gbb_paged_cache* c
 
 namespace {
 
-gbb_status check_options(const gbb_attention_options& o, bool tokens) {
+gbb_status check_options(const gbb_attention_options& o, float scale, bool tokens) {
   if (!(o.softcap >= 0.f) || !std::isfinite(o.softcap)) return fail(GBB_E_ARG, "softcap must be 0 or more and finite");
-  if (o.softcap > 0.f && o.softcap < 1e-30f) return fail(GBB_E_ARG, "softcap must be 0 or at least 1e-30");
+  if (o.softcap > 0.f && (o.softcap < 1e-30f || o.softcap > 1e30f || std::fabs(scale) > 1e30 * double(o.softcap)))
+    return fail(GBB_E_ARG, "softcap must be 0, or within 1e-30 of the scale and 1e30");
   if (o.window < 0) return fail(GBB_E_ARG, "window must not be negative (%d)", o.window);
   if (!tokens && (o.first || o.prefix || o.tree)) return fail(GBB_E_ARG, "first, prefix and tree are for several tokens");
   if (o.tree && o.prefix) return fail(GBB_E_ARG, "tree and prefix exclude each other");
@@ -389,7 +390,7 @@ extern "C" gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, 
   static const gbb_attention_options none = {};
   const gbb_attention_options& o = options ? *options : none;
   AttendPlan p;
-  gbb_status st = check_options(o, false);
+  gbb_status st = check_options(o, scale, false);
   if (st != GBB_OK) return st;
   const int window = o.window >= max_len ? 0 : o.window;   // no limit
   if ((st = check_attend_shape(cache, B, q_heads, max_len, weights_out != nullptr, window, p)) != GBB_OK) return st;
@@ -417,6 +418,10 @@ extern "C" gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, 
 
 namespace {
 
+// A window that no distance reaches is none.  A token of more than its sequence
+// has slots lies up to T before the first, so slots of its prefix up to T further.
+int tokens_window(int window, int max_len, int T) { return window >= int64_t(max_len) + T ? 0 : window; }
+
 // Shapes alone, for the workspace query (launch sizes included).
 gbb_status check_tokens_shape(const gbb_paged_cache* c, int T, int B, int q_heads, int max_len, int window, int tree_words,
                               TokensPlan& p) {
@@ -441,8 +446,8 @@ gbb_status check_tokens_shape(const gbb_paged_cache* c, int T, int B, int q_head
 extern "C" size_t gbb_paged_attention_tokens_workspace(const gbb_paged_cache* cache, int T, int B, int q_heads,
                                                        int max_len, int window, int tree_words) {
   TokensPlan p;
-  if (check_tokens_shape(cache, T, B, q_heads, max_len, window >= max_len ? 0 : window, tree_words, p) != GBB_OK || T == 0 ||
-      B == 0)
+  if (check_tokens_shape(cache, T, B, q_heads, max_len, tokens_window(window, max_len, T), tree_words, p) != GBB_OK ||
+      T == 0 || B == 0)
     return 0;
   return p.ws_bytes;
 }
@@ -456,13 +461,13 @@ extern "C" gbb_status gbb_paged_attention_tokens(const gbb_paged_cache* cache, c
   static const gbb_attention_options none = {};
   const gbb_attention_options& o = options ? *options : none;
   TokensPlan p;
-  gbb_status st = check_options(o, true);
+  gbb_status st = check_options(o, scale, true);
   if (st != GBB_OK) return st;
-  const int window = o.window >= max_len ? 0 : o.window, words = o.tree ? o.tree_words : 0;
+  const int window = tokens_window(o.window, max_len, T), words = o.tree ? o.tree_words : 0;
   if ((st = check_tokens_shape(cache, T, B, q_heads, max_len, window, words, p)) != GBB_OK) return st;
   if ((st = check_dtype(cache, dtype)) != GBB_OK) return st;
   if ((st = check_sequences(cache, B, block_table, max_pages, lengths, max_len)) != GBB_OK) return st;
-  if (!std::isfinite(scale)) return fail(GBB_E_ARG, "scale must be finite");
+  if (!(std::fabs(scale) <= 1e30f)) return fail(GBB_E_ARG, "scale must be within -1e30 and 1e30");
   if (T == 0 || B == 0) return GBB_OK;
   if (!q || !out || !starts) return fail(GBB_E_ARG, "q, out and starts must not be NULL");
   const int64_t row = int64_t(q_heads) * cache->head_dim;

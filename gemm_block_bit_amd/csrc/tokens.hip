@@ -16,30 +16,39 @@
 //    each gets an element's 4 slots).
 //  - a row's maximum and sum lie in the two lanes that share it: one lane swap
 //    a tile for the maximum, one at the end for the sum.
-//  - tiles go from memory to registers while the tile before is worked on, and
-//    from there to LDS; pieces of 16 bytes are permuted within a row so that
-//    lanes that read together hit different banks.  Memory past a row's range
-//    reads as zeros, whatever it holds.
-//  - a tile that all rows of a wave see whole takes no masks, one that none
-//    sees is passed over.
+//  - 16-bit tiles go from memory straight to LDS, e4m3 ones to registers and
+//    from there, widened, to LDS; either while the tile before is worked on, in
+//    two buffers, so that a tile takes one barrier.  Pieces of 16 bytes are
+//    permuted within a row so that lanes that read together hit different
+//    banks.  Memory past a row's range, and pages that are not there, read as
+//    zeros, whatever they hold.
+//  - what a row sees of a tile is a 64-bit mask.  A tile that all rows of a wave
+//    see whole takes none, one that none sees is passed over.
 //
-// With n rows of tokens the work is 4 D operations a visible slot and row
-// against 2 D elements of K and V a slot: matrix bound from some 100 rows on,
-// by the bytes of the cache below that.  Beside the products every score costs
-// an exponential, a maximum, a sum and a conversion in the vector pipes, which
-// take about as long as its share of the products at D = 128.
+// With n rows the work is 4 D operations a visible slot and row against 2 D
+// elements of K and V a slot: matrix bound from some 100 rows on, by the bytes
+// of the cache below that.  Beside the products every score costs an
+// exponential, a maximum, a sum and a conversion in the vector pipes, which
+// take about as long as its share of the products at D = 128, and a cap another
+// exponential and a reciprocal; the tiles' reads from LDS (each wave reads all
+// of K and V) come third.  Measured, 32 query over 8 kv heads of 128, bf16, a
+// prompt of 8192 tokens (550e9 operations, 456 us at the rate of a large
+// product): 575 to 600 us, with a bias 636 to 660, with a cap 688 to 713; heads
+// of 64 343, of 256 900; e4m3 617.  Through registers and LDS writes the plain
+// one took 621, with waits before every load to LDS 780.
 //
 // P is rounded to 16 bits for the matrix cores, once in workgroups of four
 // waves, where the products bound the call (a second operand for what the
-// rounding drops would take half as long again), and the sum that divides the
-// output is that of the rounded P: an output is off by at most half a step of
-// its type relative to sum p |v|, beside its own rounding.  With fewer waves the
-// cache's bytes bound the call, and P is given in two operands (22 bits in fp16,
-// 16 in bf16).
+// rounding drops would take half as long again): an output is off by at most
+// half a step of its type relative to sum p |v|, beside its own rounding.  The
+// sum that divides the output, and makes lse, is of P before that, in fp32.
+// With two waves the cache's bytes bound the call, and P is given in two
+// operands (22 bits in fp16, 16 in bf16).
 //
 // Where there are few row tiles the slots are split over workgroups; partial
 // results (maximum, sum, unnormalised output, fp32) go to the workspace, and
-// the last workgroup of a row tile joins them in the order of the runs.
+// the last workgroup of a row tile joins them in the order of the runs, so the
+// result is the same bits each time.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -830,20 +839,23 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   if (window && tree_words) most = std::min<int64_t>(most, int64_t(window) + 32 * int64_t(tree_words) + 15);
   else if (window) most = std::min<int64_t>(most, 2 * int64_t(window) + p.rows + 15);
   else most = most + 15;
-  // Runs.  Two workgroups a CU are resident; a run costs about 15 us beside its
-  // slots (25 us of 64 tiles' 80), its join 0.6.  With fewer row tiles than that:
-  // as many runs as make four a CU, of 384 to 2048 slots (32 of 300 x 4 tokens
-  // behind up to 4000: 55 us in 1024, 73 in 2048; 8 tiles of 4000: 27 in 384, 29
-  // in 256, 32 in 768; 136 of 8192: 94 in 2048, 105 in 1024, 135 in 4096).  With more, a single sequence's tiles
-  // balance by themselves, since those that see most start first; those of several
-  // may be of any length: runs of up to 4096 (16 trees of 64 behind up to 16384:
-  // 283, whole 500; behind 8192 each 354 and 337).
+  // Runs.  Two workgroups a CU are resident; a run costs some 10 us beside its
+  // slots (1.3 us a tile of 64), and 0.6 in the join.  With fewer row tiles than
+  // that: as many runs as make four a CU, of 384 to 2048 slots (32 tiles of 300 x 4
+  // tokens behind up to 4000: 55 us in 1024, 73 in 2048; 8 tiles of 4000: 27 in 384,
+  // 29 in 256, 32 in 768; 136 of 8192: 94 in 2048, 105 in 1024, 135 in 4096).  With
+  // more, a single sequence's tiles balance by themselves, since those that see
+  // most start first; those of several may be of any length: runs of up to 4096
+  // (16 trees of 64 behind up to 16384: 283 us, whole 500; behind 8192 each 354
+  // and 337).
   const int64_t groups = int64_t(p.tiles) * c.kv_heads;
   int64_t chunk = most;
   if (groups <= kMaxArrived) {
     if (groups < 2 * cus) chunk = std::min<int64_t>(2048, std::max<int64_t>(384, most * groups / (4 * cus)));
     else if (B > 1) chunk = 4096;
-    chunk = std::max(chunk, (most + kMaxJoin - 1) / kMaxJoin);
+    // at most 64 runs a tile and 16 workgroups a CU (the workspace has 64 KiB
+    // for each at 128 elements)
+    chunk = std::max({chunk, (most + kMaxJoin - 1) / kMaxJoin, most * groups / (16 * cus)});
     const int64_t runs = (most + chunk - 1) / chunk;   // of one size
     chunk = (most + runs - 1) / runs;
   }

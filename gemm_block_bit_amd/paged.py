@@ -22,6 +22,7 @@ no gradient.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import numpy as np
 
@@ -30,6 +31,7 @@ from .binding import (_AttentionOptions, _check, _dev_ptr, _given, _kept, _np_pt
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
+_INT_MAX = 2 ** 31 - 1
 _dtype_codes: dict = {}
 
 
@@ -135,7 +137,7 @@ def _axes(positions, sections, device, tokens):
         return _ptr(positions, _int32, device, "positions", (tokens,)), 1, None
     array = _section_arrays.get(sections) if type(sections) is tuple else None
     if array is None:
-        sections = tuple(int(n) for n in sections)
+        sections = tuple(operator.index(n) for n in sections)
         if not 1 <= len(sections) <= 4:
             raise ValueError(f"sections must have 1 to 4 axes ({len(sections)})")
         array = _section_arrays.setdefault(sections, (ctypes.c_int * len(sections))(*sections))
@@ -453,14 +455,14 @@ def paged_attention_workspace(cache: PagedCache, batch: int, q_heads: int, max_l
     """Bytes of paged_attention's workspace (with_weights: of a call with
     weights_out).  A new one's first 16384 have to be zero: torch.zeros."""
     return _on(cache._index, lib().gbb_paged_attention_options_workspace, cache._ref, batch, q_heads, max_len,
-               int(with_weights), window)
+               int(with_weights), min(window, _INT_MAX))
 
 
 def _options(device, q_heads, softcap, slopes, window, first=None, prefix=None, tree=None, tokens=0, batch=0):
     """A gbb_attention_options, or None where nothing is asked for."""
     if not softcap and slopes is None and not window and first is None and prefix is None and tree is None:
         return None
-    words = 0
+    words, window = 0, min(window, _INT_MAX)
     if tree is not None:
         p, shape = _ptr(tree, _int32, device, "tree"), tree.shape
         if len(shape) != 2 or shape[0] != tokens:
@@ -527,7 +529,7 @@ def paged_attention_tokens_workspace(cache: PagedCache, tokens: int, batch: int,
     """Bytes of paged_attention_tokens' workspace (tree_words: tree.shape[1]).
     A new one's first 16384 have to be zero: torch.zeros."""
     return _on(cache._index, lib().gbb_paged_attention_tokens_workspace, cache._ref, tokens, batch, q_heads, max_len,
-               window, tree_words)
+               min(window, _INT_MAX), tree_words)
 
 
 def paged_attention_tokens(cache: PagedCache, q, starts, block_table, lengths, max_len: int,

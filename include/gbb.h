@@ -644,7 +644,8 @@ gbb_status gbb_norm_rope_append(const gbb_paged_cache* cache, const void* qkv, i
 
 /* What shapes the scores s = scale * (q . k) of attention, and what is seen. */
 typedef struct {
-  float softcap;          /* above 0: s becomes softcap * tanh(s / softcap); 0: none */
+  float softcap;          /* above 0: s becomes softcap * tanh(s / softcap); 0: none.  Of 1e-30 to 1e30, and of
+                             1e-30 |scale| or more */
   const float* slopes;    /* device [q_heads], or NULL: then s (capped) minus slopes[head] * distance */
   int window;             /* above 0: only slots at a distance below it are seen; 0: no such limit */
   /* the rest for gbb_paged_attention_tokens alone: */
@@ -688,6 +689,7 @@ gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, const void*
  *              Tokens outside all sequences are not read, and their outputs
  *              not written.
  *   block_table, lengths, max_len  as gbb_paged_attention.
+ *   scale      of -1e30 to 1e30.
  *   options    NULL, or what shapes and masks the scores; tree and prefix
  *              exclude each other.
  *   workspace  16-byte aligned, of gbb_paged_attention_tokens_workspace bytes

@@ -317,6 +317,23 @@ def test_starts_and_lengths_that_make_no_sense_stay_in_bounds():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 24, 25, 30, 64, 65, 2 ** 31 - 1])
+def test_more_tokens_than_slots(window):
+    """Those before the first slot see what their sequence shares (a window
+    counts from where they would lie), or what the tree gives them."""
+    n, length = 40, 25
+    o = dict(window=window) if window else {}
+    s = Setup([length - n, 0], [n, 3], 4, 2, 64, seed=12, prefix=np.array([20, 0]), slopes=2.0 ** -np.arange(1, 5), **o)
+    lse = torch.zeros(s.T, 4, device=dev())
+    s.check(s.run(lse=lse), lse)
+    bits = np.zeros((n + 3, n), bool)
+    bits[:n] = random_tree(np.random.default_rng(13), n)
+    bits[n:, :3] = True
+    s = Setup([length - n, 0], [n, 3], 4, 2, 64, seed=14, tree=(bits, 2), slopes=2.0 ** -np.arange(1, 5), **o)
+    s.check(s.run(lse=lse), lse)
+
+
+@pytest.mark.gpu
 def test_pages_that_are_not_there():
     s = Setup([150, 60, 0], [60, 9, 40], 4, 2, 128, page=16, seed=11)
     s.bt[0, 0], s.bt[0, 5], s.bt[0, 12] = -1, s.k.shape[0], -2 ** 31
@@ -586,7 +603,8 @@ def test_argument_refusals():
     for bad in (dict(c=dict(v=None)), dict(c=dict(dtype=2)), dict(dt=1), dict(T=-1), dict(B=-1), dict(ml=0), dict(mp=0),
                 dict(sc=float("inf")), dict(q=None), dict(out=None), dict(st=None), dict(bt=None), dict(ln=None),
                 dict(out=8 << 20), dict(o=dict(softcap=-1.0)), dict(o=dict(softcap=float("nan"))), dict(o=dict(softcap=1e-35)),
-                dict(o=dict(window=-1)), dict(o=dict(tree=1 << 20, tree_words=1, prefix=1 << 20))):
+                dict(o=dict(window=-1)), dict(o=dict(tree=1 << 20, tree_words=1, prefix=1 << 20)),
+                dict(o=dict(softcap=1e35)), dict(sc=1e25, o=dict(softcap=1e-10)), dict(sc=-1e35)):
         assert tokens(**bad) == -1, bad
     for bad in (dict(c=dict(page=8)), dict(c=dict(head_dim=32)), dict(hq=5), dict(hq=2 * 129), dict(ml=65), dict(qt=128),
                 dict(T=1 << 23), dict(B=1 << 23), dict(o=dict(tree=1 << 20, tree_words=0)),
@@ -599,7 +617,8 @@ def test_argument_refusals():
     assert tokens(ws=None, **long) == -1
     assert tokens(wb=16, **long) == -5
     assert tokens(ws=(1 << 24) + 8, **long) == -4
-    for o in (dict(first=1 << 20), dict(prefix=1 << 20), dict(tree=1 << 20, tree_words=1), dict(window=-1), dict(softcap=-2.0)):
+    for o in (dict(first=1 << 20), dict(prefix=1 << 20), dict(tree=1 << 20, tree_words=1), dict(window=-1), dict(softcap=-2.0), dict(softcap=1e35),
+              dict(softcap=float("inf"))):
         assert one(o) == -1, o
     assert one(dict(slopes=2)) == -4
     cc = C(**base)
@@ -621,3 +640,4 @@ def test_binding_refusals():
     with pytest.raises((TypeError, ValueError)):
         gbb.paged._options(0, 4, 0.0, torch.zeros(4), 0)
     assert gbb.paged._options(0, 4, 0.0, None, 0) is None
+    assert gbb.paged._options(0, 4, 0.0, None, 2 ** 32 + 5)._obj.window == 2 ** 31 - 1   # not 5
