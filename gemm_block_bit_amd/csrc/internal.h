@@ -210,7 +210,8 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPla
 struct TokensPlan {
   int waves, rows, tiles;   // waves of 32 rows each a workgroup; row tiles of all sequences, at most
   int chunk, nsplit;
-  size_t ml_off, o_off, ws_bytes;
+  bool second;              // the runs are joined by a second launch
+  size_t notes_off, ml_off, o_off, ws_bytes;
 };
 struct TokensArgs {
   const void* q;

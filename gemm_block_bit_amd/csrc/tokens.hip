@@ -47,8 +47,9 @@
 //
 // Where there are few row tiles the slots are split over workgroups; partial
 // results (maximum, sum, unnormalised output, fp32) go to the workspace, and
-// the last workgroup of a row tile joins them in the order of the runs, so the
-// result is the same bits each time.
+// the last workgroup of a row tile, or where there are more runs a second
+// launch, joins them in the order of the runs, so the result is the same bits
+// each time.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -72,6 +73,9 @@ constexpr float kShift = 6.f, kLimit = 15.f;
 
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
+// What the second launch has to know of a row tile and kv head.
+struct Note { int t0, r0, rows, runs; };       // its sequence's first token and rows, its own first row
+
 struct Args {
   const void* q;
   const uint8_t* k;
@@ -90,6 +94,7 @@ struct Args {
   unsigned* arrived;   // [row tile][Hkv] runs that are done, 0 between calls
   float2* ml;          // [row tile][Hkv][nsplit][rows] ref (below) and sum
   float* o;            // [row tile][Hkv][nsplit][rows * D], in the order of the lanes that hold them
+  Note* notes;         // [row tile][Hkv] where a second launch joins the runs, else NULL
   int64_t q_token;
   int T, B, Hq, Hkv, G, num_pages, pshift, max_pages, max_len, chunk, nsplit, tiles, tree_words, window;
   float scale, cap;    // times log2(e)
@@ -237,7 +242,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     }
     before += __builtin_amdgcn_readlane(sum, 63);
   }
-  if (b < 0) return;
+  // for the second launch: how many runs there are to join
+  const auto tell = [&](int t0, int r0, int rows, int runs) {
+    Note* const notes = late_args()->notes;
+    if (notes && sp == 0 && threadIdx.x == 0) notes[w * a.Hkv + hk] = Note{t0, r0, rows, runs};
+  };
+  if (b < 0) {
+    tell(0, 0, 0, 0);
+    return;
+  }
   b = uniform(b);
   t0 = uniform(t0);
   n = uniform(n);
@@ -325,6 +338,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       for (int d = 8 * h; d < D; d += 16) st16(static_cast<T*>(a.out) + head * D + d, u32x4{0, 0, 0, 0});
       if (a.lse && h == 0) a.lse[head] = -INFINITY;
     }
+    tell(0, 0, 0, 0);
     return;
   }
   k_low &= ~15;
@@ -338,6 +352,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     saved[2] = rows_all;
     saved[3] = (k_high - k_low - 1) / a.chunk + 1;
   }
+  tell(t0, r0, rows_all, (k_high - k_low - 1) / a.chunk + 1);
   const int k1 = k0 + min(k_high - k0, a.chunk);
   const int nt = (k1 - k0 + BN - 1) / BN;
 
@@ -750,6 +765,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
       }
     if (h == 0) put(ml_at(run), ref, l);
   }
+  if (x->notes) return;
   __shared__ unsigned count;
   loads_left<0>();
   __syncthreads();
@@ -801,6 +817,67 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   finish(high, l);
 }
 
+// The join in a launch of its own: a workgroup takes 32 rows of a row tile and kv
+// head, a wave 32 of their elements.  The same sums in the same order.
+constexpr int kBatch = 8;        // runs under way at once
+template <int DT, int D>
+__global__ __launch_bounds__(2 * D) void join_kernel(Args a, int rows) {
+  typedef typename Half<DT>::T T;
+  const int lane = threadIdx.x & 63, j = uniform(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
+  const int slices = rows / 32, part = blockIdx.x % slices, group = blockIdx.x / slices, hk = group % a.Hkv;
+  const Note note = a.notes[group];
+  const int ns = uniform(note.runs);
+  if (ns < 2) return;                          // its workgroup has written the output
+  const int row = note.r0 + 32 * part + c;
+  if (row >= note.rows) return;
+  const float2* const ml = a.ml + size_t(group) * a.nsplit * rows + 32 * part + c;
+  const float* const o = a.o + size_t(group) * a.nsplit * rows * D + (part * (4 * (D / 32)) + 4 * j) * 256 + 4 * lane;
+  f32x4 pieces[kBatch][4];
+  float2 e[kBatch];
+  const auto take = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = min(s0 + u, ns - 1);
+      e[u] = ml[size_t(s) * rows];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pieces[u][i] = *reinterpret_cast<const f32x4*>(o + size_t(s) * rows * D + 256 * i);
+    }
+  };
+  float high = -FLT_MAX;
+  for (int s0 = 0; s0 < ns; s0 += 16) {
+    float y[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) y[u] = ml[size_t(min(s0 + u, ns - 1)) * rows].x;
+    if (s0 == 0) take(0);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) high = fmaxf(high, y[u]);
+  }
+  float l = 0.f, sum[16] = {};
+  for (int s0 = 0; s0 < ns; s0 += kBatch) {
+    if (s0) take(s0);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (s0 + u < ns) {
+        const float f = __builtin_amdgcn_exp2f(e[u].x - high);
+        l += f * e[u].y;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] = __builtin_fmaf(f, pieces[u][i / 4][i % 4], sum[i]);
+      }
+  }
+  const int token = row / a.G;
+  const size_t head = size_t(note.t0 + token) * a.Hq + hk * a.G + (row - token * a.G);
+  const float f = l == 0.f ? 0.f : (a.v_scale ? a.v_scale[hk] : 1.f) / l;
+  typedef T V4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int r = 0; r < 16; r += 4) {
+    V4 y;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] = T(l == 0.f ? 0.f : sum[r + u] * f);
+    *reinterpret_cast<V4*>(static_cast<T*>(a.out) + head * D + 32 * j + 8 * (r / 4) + 4 * h) = y;
+  }
+  if (a.lse && h == 0 && j == 0) a.lse[head] = l == 0.f ? -INFINITY : (high + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int DT, int CT, int D, bool TREE>
@@ -818,6 +895,13 @@ void run_dim(const Args& a, int D, int waves, unsigned grid, hipStream_t s) {
   if (D == 64) run<DT, CT, 64>(a, waves, grid, s);
   else if (D == 128) run<DT, CT, 128>(a, waves, grid, s);
   else run<DT, CT, 256>(a, waves, grid, s);
+}
+template <int DT>
+void run_join(const Args& a, int D, int rows, hipStream_t s) {
+  const dim3 grid(unsigned(a.tiles) * unsigned(a.Hkv) * unsigned(rows / 32));
+  if (D == 64) start((join_kernel<DT, 64>), grid, dim3(128), s, a, rows);
+  else if (D == 128) start((join_kernel<DT, 128>), grid, dim3(256), s, a, rows);
+  else start((join_kernel<DT, 256>), grid, dim3(512), s, a, rows);
 }
 
 }  // namespace
@@ -840,19 +924,28 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   else if (window) most = std::min<int64_t>(most, 2 * int64_t(window) + p.rows + 15);
   else most = most + 15;
   // Runs.  Two workgroups a CU are resident; a run costs some 10 us beside its
-  // slots (1.3 us a tile of 64), and 0.6 in the join.  With fewer row tiles than
-  // that: as many runs as make four a CU, of 384 to 2048 slots (32 tiles of 300 x 4
-  // tokens behind up to 4000: 55 us in 1024, 73 in 2048; 8 tiles of 4000: 27 in 384,
-  // 29 in 256, 32 in 768; 136 of 8192: 94 in 2048, 105 in 1024, 135 in 4096).  With
-  // more, a single sequence's tiles balance by themselves, since those that see
-  // most start first; those of several may be of any length: runs of up to 4096
-  // (16 trees of 64 behind up to 16384: 283 us, whole 500; behind 8192 each 354
-  // and 337).
+  // slots (1.3 us a tile of 64), and 0.6 in the join by the last workgroup.  With
+  // fewer row tiles than that: as many runs as make four a CU, of 256 to 2048
+  // slots, which a second launch joins, on more CUs but some 4 us later (a tree of
+  // 25 behind 4000: 23 us in runs of 256 against 28 in runs of 384 that the last
+  // workgroup joins; 64 tokens behind 65536: 124 and 143, 300 x 4 behind up to 4000:
+  // 60 and 66; in runs of 128 the tree takes 30, of 512 25).  Where that makes fewer
+  // than four runs, of at least 384, and no second launch (12 heads of 512 tokens:
+  // 14.6 us, 15.3 with one).  With more tiles, a single sequence's balance by
+  // themselves, since those that see most start first; those of several may be of
+  // any length: runs of up to 4096 (16 trees of 64 behind up to 16384: 283 us, whole
+  // 500; behind 8192 each 354 and 337).
   const int64_t groups = int64_t(p.tiles) * c.kv_heads;
   int64_t chunk = most;
+  bool second = false;
   if (groups <= kMaxArrived) {
-    if (groups < 2 * cus) chunk = std::min<int64_t>(2048, std::max<int64_t>(384, most * groups / (4 * cus)));
-    else if (B > 1) chunk = 4096;
+    if (groups < 2 * cus) {
+      chunk = std::min<int64_t>(2048, std::max<int64_t>(256, most * groups / (4 * cus)));
+      second = most > 3 * chunk;
+      if (!second) chunk = std::max<int64_t>(384, chunk);
+    } else if (B > 1) {
+      chunk = 4096;
+    }
     // at most 64 runs a tile and 16 workgroups a CU (the workspace has 64 KiB
     // for each at 128 elements)
     chunk = std::max({chunk, (most + kMaxJoin - 1) / kMaxJoin, most * groups / (16 * cus)});
@@ -862,7 +955,9 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   p.chunk = int(std::min<int64_t>((chunk + 63) & ~int64_t(63), INT_MAX & ~63));
   p.nsplit = int(std::max<int64_t>(1, (most + p.chunk - 1) / p.chunk));
   const size_t parts = p.nsplit > 1 ? size_t(groups) * p.nsplit * p.rows : 0;
-  p.ml_off = parts ? GBB_ATTENTION_COUNTERS : 0;
+  p.second = second && p.nsplit > 1;
+  p.notes_off = parts ? GBB_ATTENTION_COUNTERS : 0;
+  p.ml_off = p.notes_off + (p.second ? up(groups * sizeof(Note)) : 0);
   p.o_off = p.ml_off + up(parts * sizeof(float2));
   p.ws_bytes = p.o_off + up(parts * c.head_dim * sizeof(float));
   return p;
@@ -887,6 +982,7 @@ int launch_tokens(const gbb_paged_cache& c, const TokensArgs& x, const TokensPla
   a.arrived = reinterpret_cast<unsigned*>(x.ws);
   a.ml = reinterpret_cast<float2*>(x.ws + p.ml_off);
   a.o = reinterpret_cast<float*>(x.ws + p.o_off);
+  a.notes = p.second ? reinterpret_cast<Note*>(x.ws + p.notes_off) : nullptr;
   a.q_token = x.q_token;
   a.T = x.T;
   a.B = x.B;
@@ -915,6 +1011,11 @@ int launch_tokens(const gbb_paged_cache& c, const TokensArgs& x, const TokensPla
   } else {
     if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.waves, grid, s);
     else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.waves, grid, s);
+  }
+  if (p.second) {
+    if (c.dtype != GBB_E4M3) a.v_scale = nullptr;
+    if (x.dtype == GBB_F16) run_join<GBB_F16>(a, c.head_dim, p.rows, s);
+    else run_join<GBB_BF16>(a, c.head_dim, p.rows, s);
   }
   return int(hipGetLastError());
 }

@@ -54,6 +54,25 @@ def test_a_gradient_in_place_of_the_output_s(D, rot, layout, dt):
     assert torch.equal(grad(dy), dw) and torch.equal(dy, dx)
 
 
+@pytest.mark.parametrize("B,n", [(8, 12300), (3, 12300), (1, 600), (2, 150)])
+def test_runs_joined_in_the_launch_and_by_a_second(B, n):
+    """Many row tiles and few, in several runs: sequences of one length and of
+    others, on the same pages."""
+    hkv, D, page = 64, 64, 64
+    s = Setup([n - 1], [1], hkv, hkv, D, page=page, seed=n + B)
+    d = s.qd.device
+    lengths = [n, n, n // 3, 70, n, 1, n - 100, 4200][:B]
+    g = np.random.default_rng(B)
+    q = torch.from_numpy((2 * g.standard_normal((B, hkv, D))).astype(np.float16))
+    s.q, s.T, s.lengths, s.new, s.starts, s.bt = q, B, lengths, [1] * B, np.arange(B + 1, dtype=np.int32), s.bt.repeat(B, 0)
+    s.to_device()
+    lse = torch.zeros(B, hkv, device=d)
+    out = s.run(lse=lse)
+    s.check(out, lse)
+    for _ in range(3):                            # the same bits each time
+        assert torch.equal(s.run(), out)
+
+
 def test_a_step_of_drafts_in_a_graph():
     """Norms and append, attention of a tree, the cut to the kept tokens and
     attention of the next token captured together; every replay, with eager work
