@@ -817,21 +817,22 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   finish(high, l);
 }
 
-// The join in a launch of its own: a workgroup takes 32 rows of a row tile and kv
-// head, a wave 32 of their elements.  The same sums in the same order.
+// The join in a launch of its own: a workgroup of one wave takes 32 elements of 32
+// rows of a row tile and kv head.  The same sums in the same order.
 constexpr int kBatch = 8;        // runs under way at once
 template <int DT, int D>
-__global__ __launch_bounds__(2 * D) void join_kernel(Args a, int rows) {
+__global__ __launch_bounds__(64) void join_kernel(Args a, int rows) {
   typedef typename Half<DT>::T T;
-  const int lane = threadIdx.x & 63, j = uniform(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
-  const int slices = rows / 32, part = blockIdx.x % slices, group = blockIdx.x / slices, hk = group % a.Hkv;
+  constexpr int NT = D / 32;
+  const int lane = threadIdx.x, j = blockIdx.x % NT, c = lane & 31, h = lane >> 5;
+  const int slices = rows / 32, part = blockIdx.x / NT % slices, group = blockIdx.x / NT / slices, hk = group % a.Hkv;
   const Note note = a.notes[group];
   const int ns = uniform(note.runs);
   if (ns < 2) return;                          // its workgroup has written the output
   const int row = note.r0 + 32 * part + c;
   if (row >= note.rows) return;
   const float2* const ml = a.ml + size_t(group) * a.nsplit * rows + 32 * part + c;
-  const float* const o = a.o + size_t(group) * a.nsplit * rows * D + (part * (4 * (D / 32)) + 4 * j) * 256 + 4 * lane;
+  const float* const o = a.o + size_t(group) * a.nsplit * rows * D + (part * (4 * NT) + 4 * j) * 256 + 4 * lane;
   f32x4 pieces[kBatch][4];
   float2 e[kBatch];
   const auto take = [&](int s0) {
@@ -898,10 +899,10 @@ void run_dim(const Args& a, int D, int waves, unsigned grid, hipStream_t s) {
 }
 template <int DT>
 void run_join(const Args& a, int D, int rows, hipStream_t s) {
-  const dim3 grid(unsigned(a.tiles) * unsigned(a.Hkv) * unsigned(rows / 32));
-  if (D == 64) start((join_kernel<DT, 64>), grid, dim3(128), s, a, rows);
-  else if (D == 128) start((join_kernel<DT, 128>), grid, dim3(256), s, a, rows);
-  else start((join_kernel<DT, 256>), grid, dim3(512), s, a, rows);
+  const dim3 grid(unsigned(a.tiles) * unsigned(a.Hkv) * unsigned(rows / 32) * unsigned(D / 32));
+  if (D == 64) start((join_kernel<DT, 64>), grid, dim3(64), s, a, rows);
+  else if (D == 128) start((join_kernel<DT, 128>), grid, dim3(64), s, a, rows);
+  else start((join_kernel<DT, 256>), grid, dim3(64), s, a, rows);
 }
 
 }  // namespace
@@ -925,13 +926,14 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   else most = most + 15;
   // Runs.  Two workgroups a CU are resident; a run costs some 10 us beside its
   // slots (1.3 us a tile of 64), and 0.6 in the join by the last workgroup.  With
-  // fewer row tiles than that: as many runs as make four a CU, of 256 to 2048
-  // slots, which a second launch joins, on more CUs but some 4 us later (a tree of
-  // 25 behind 4000: 23 us in runs of 256 against 28 in runs of 384 that the last
-  // workgroup joins; 64 tokens behind 65536: 124 and 143, 300 x 4 behind up to 4000:
-  // 60 and 66; in runs of 128 the tree takes 30, of 512 25).  Where that makes fewer
-  // than four runs, of at least 384, and no second launch (12 heads of 512 tokens:
-  // 14.6 us, 15.3 with one).  With more tiles, a single sequence's balance by
+  // fewer row tiles than that: as many runs as make four a CU, or three where there
+  // are several sequences (some of p.tiles are empty then, and some tiles short), of
+  // 256 to 2048 slots, which a second launch joins, on more CUs but some 4 us later: a
+  // tree of 25 behind 4000 takes 22.5 us in runs of 256, 24 in 192, 28 in runs of 384
+  // that the last workgroup joins; 64 tokens behind 65536 take 121, 136 with three a
+  // CU, 143 joined by the last; 300 x 4 behind up to 4000 52, 59 with four a CU, 66.
+  // Where that makes one or two runs, of at least 384, and no second launch (256
+  // tokens 14, 17 with one).  With more tiles, a single sequence's balance by
   // themselves, since those that see most start first; those of several may be of
   // any length: runs of up to 4096 (16 trees of 64 behind up to 16384: 283 us, whole
   // 500; behind 8192 each 354 and 337).
@@ -940,8 +942,8 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   bool second = false;
   if (groups <= kMaxArrived) {
     if (groups < 2 * cus) {
-      chunk = std::min<int64_t>(2048, std::max<int64_t>(256, most * groups / (4 * cus)));
-      second = most > 3 * chunk;
+      chunk = std::min<int64_t>(2048, std::max<int64_t>(256, most * groups / ((B > 1 ? 3 : 4) * cus)));
+      second = most > 2 * chunk;
       if (!second) chunk = std::max<int64_t>(384, chunk);
     } else if (B > 1) {
       chunk = 4096;
