@@ -295,6 +295,17 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
   const int l = threadIdx.x % s.lanes, r = threadIdx.x / s.lanes;
   const int D = c.head_dim, Hkv = c.kv_heads, H = a.Hq + 2 * Hkv;
   Walk at(s, H, r);
+  // q's and k's weights, in LDS: loads from memory on the way would wait for the
+  // next head's, which were asked for before
+  __shared__ __align__(16) float weights[2][256];
+  if (a.norm && a.q_weight) {
+    for (int d = threadIdx.x; d < 2 * D; d += 256) {
+      const void* const from = d < D ? a.q_weight : a.k_weight;
+      const int i = d < D ? d : d - D;
+      weights[d >= D][i] = a.wide_weight ? static_cast<const float*>(from)[i] : float(static_cast<const T*>(from)[i]);
+    }
+    __syncthreads();
+  }
   if (r / s.hp >= s.tp || at.t >= a.T || at.h >= H) return;
   const U first(s.n, a.r.rot, l);
   const auto x_of = [&](const Walk& w) { return static_cast<const T*>(a.qkv) + w.t * a.token_stride + size_t(w.h) * D; };
@@ -305,12 +316,17 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
   const auto token_of = [&](int t) { return Token{place_of<AXES>(a.r, a.T, t), a.slots[t]}; };
   float p[E], q[E], w[E], v[E];
   Angles<E, HALF> g;
+  // the scale of a head's elements in the cache
+  const auto element_of = [&](int h) {
+    const float* const scales = CT != GBB_E4M3 || h < a.Hq ? nullptr : h < a.Hq + Hkv ? c.k_scale : c.v_scale;
+    return scales ? scales[(h - a.Hq) % Hkv] : 1.f;
+  };
   // unit u of head `at` from p and q, the head's inverse root mean square given
-  const auto finish = [&](const U& unit, int u, const Token& token, float scale) {
+  const auto finish = [&](const U& unit, int u, const Token& token, float scale, float element) {
     const bool query = at.h < a.Hq, value = at.h >= a.Hq + Hkv;
     const bool there = token.place.there && unsigned(token.slot) < unsigned(c.num_pages) * unsigned(c.page);
     if (a.norm && !value) {
-      unit.weights(query ? a.q_weight : a.k_weight, a.wide_weight, a.dtype, w, v);
+      unit.load(weights[!query], w, v);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         p[i] = p[i] * scale * w[i];
@@ -326,8 +342,6 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
       const int hk = value ? at.h - a.Hq - Hkv : at.h - a.Hq;
       const int shift = 31 - __builtin_clz(unsigned(c.page));   // a power of two
       const size_t row = ((size_t(token.slot >> shift) * Hkv + hk) << shift) + (token.slot & (c.page - 1));
-      const float* scales = value ? c.v_scale : c.k_scale;
-      const float element = CT == GBB_E4M3 && scales ? scales[hk] : 1.f;
       void* base = value ? c.v : c.k;
       if (unit.there) store_cache<CT, E>(base, row * D + unit.d0, p, element);
       if (unit.two) store_cache<CT, E>(base, row * D + unit.d1, q, element);
@@ -341,6 +355,7 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
   if constexpr (ONE) {
     Packed<T, E> x = {}, x_next = {};
     x.load(first, x_of(at));
+    float element = element_of(at.h), element_next = 1.f;
     if (first.pair) load_angles<AXES>(g, a.r, token.place, l, 1.f);
     Token token_next = token_of(min(at.t + at.tokens, a.T - 1));
     while (at.t < a.T) {
@@ -350,6 +365,7 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
       const Token here = token;
       if (next.t < a.T) {
         x_next.load(first, x_of(next));
+        element_next = element_of(next.h);
         if (moves) {
           token = token_next;
           if (first.pair) load_angles<AXES>(g_next, a.r, token.place, l, 1.f);
@@ -359,8 +375,9 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
       x.wide(p, q);
       float scale = 1.f;
       if (a.norm && at.h < a.Hq + Hkv) scale = inverse_root(over_head(dot(p, q, p, q), s.lanes), D, a.eps);
-      finish(first, l, here, scale);
+      finish(first, l, here, scale, element);
       x = x_next;
+      element = element_next;
       g = g_next;
       at = next;
     }
@@ -379,7 +396,7 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
         const U unit(s.n, a.r.rot, u);
         if (unit.pair) load_angles<AXES>(g, a.r, token.place, u, 1.f);
         unit.load(x_of(at), p, q);
-        finish(unit, u, token, scale);
+        finish(unit, u, token, scale, element_of(at.h));
       }
     }
   }
