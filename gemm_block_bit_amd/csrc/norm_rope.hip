@@ -27,7 +27,7 @@
 // elements in turn (16384 x 32 heads of 128, bf16, with gradients 258 -> 147 us).
 //
 // Measured: forward 54 us (4.9 TB/s; a copy of its size 50.6), gradient 87 (4.6
-// TB/s), 4097 tokens of 64 / 8 heads of 128 into an e4m3 cache 34 (4.8 TB/s).
+// TB/s), 4097 tokens of 64 / 8 heads of 128 into an e4m3 cache 35 (4.7 TB/s).
 // Calls of up to about a hundred tokens take a launch and two dependent reads.
 #include <algorithm>
 
@@ -596,9 +596,9 @@ dim3 grid_of(const Spread& s, int T, int H, int resident) {
 }
 // Workgroups of 256 threads a CU, by the registers that a unit takes: 16384 x 32
 // heads of 128 in halves 54 us in 4 a CU, 56 in 8, interleaved 56 in 8, 57 in 4;
-// 4097 tokens into an e4m3 cache 34 in 6, 37 in 8, 39 in 4.
+// 4097 tokens into an e4m3 cache 35 in 6, 40 in 8, 41 in 4, in halves 42 in 4, 45 in 6.
 int resident(bool half, int E) { return half && E == 8 ? 4 : 8; }
-constexpr int kAppending = 6;
+int appending(bool half, int E) { return half && E == 8 ? 4 : 6; }
 // The gradient's, each of which sums over its heads: in halves 87 us in 3 a CU, 92 in
 // 8; interleaved 86 in 5, 98 in 3; heads of 96 with 24 rotated 100 in 5, 132 in 3.
 constexpr int kMostSummed = 5;
@@ -712,7 +712,7 @@ int launch_norm_append(const gbb_paged_cache& c, const NormAppendArgs& a, void* 
   if (E < 8) E = half ? 1 : 2;
   bool one;
   const Spread s = spread(a.Hq + 2 * c.kv_heads, c.head_dim, a.r.rot, a.r.layout, E, one);
-  const dim3 grid = grid_of(s, a.T, a.Hq + 2 * c.kv_heads, kAppending);
+  const dim3 grid = grid_of(s, a.T, a.Hq + 2 * c.kv_heads, appending(half, E));
   if (a.dtype == GBB_F16) {
     if (c.dtype == GBB_E4M3) run_norm_append<GBB_F16, GBB_E4M3>(c, a, E, half, one, s, grid, st);
     else run_norm_append<GBB_F16, GBB_F16>(c, a, E, half, one, s, grid, st);
