@@ -361,14 +361,15 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
     while (at.t < a.T) {
       Walk next = at;
       const bool moves = next.step();
-      Angles<E, HALF> g_next = g;
+      Angles<E, HALF> g_next;                // not in halves, where a unit's angles take twice
+      if (!HALF) g_next = g;                 // the registers (36 us, with them 42 in 4 workgroups a CU)
       const Token here = token;
       if (next.t < a.T) {
         x_next.load(first, x_of(next));
         element_next = element_of(next.h);
         if (moves) {
           token = token_next;
-          if (first.pair) load_angles<AXES>(g_next, a.r, token.place, l, 1.f);
+          if (!HALF && first.pair) load_angles<AXES>(g_next, a.r, token.place, l, 1.f);
           token_next = token_of(min(next.t + next.tokens, a.T - 1));
         }
       }
@@ -378,7 +379,8 @@ __global__ __launch_bounds__(256) void norm_append_kernel(NormAppendArgs a, gbb_
       finish(first, l, here, scale, element);
       x = x_next;
       element = element_next;
-      g = g_next;
+      if (!HALF) g = g_next;
+      else if (moves && next.t < a.T && first.pair) load_angles<AXES>(g, a.r, token.place, l, 1.f);
       at = next;
     }
   } else {
@@ -596,9 +598,9 @@ dim3 grid_of(const Spread& s, int T, int H, int resident) {
 }
 // Workgroups of 256 threads a CU, by the registers that a unit takes: 16384 x 32
 // heads of 128 in halves 54 us in 4 a CU, 56 in 8, interleaved 56 in 8, 57 in 4;
-// 4097 tokens into an e4m3 cache 35 in 6, 40 in 8, 41 in 4, in halves 42 in 4, 45 in 6.
+// 4097 tokens into an e4m3 cache 35 in 6, 40 in 8, 41 in 4, in halves 36 in 5, 40 in 4, 39 in 6.
 int resident(bool half, int E) { return half && E == 8 ? 4 : 8; }
-int appending(bool half, int E) { return half && E == 8 ? 4 : 6; }
+int appending(bool half, int E) { return half && E == 8 ? 5 : 6; }
 // The gradient's, each of which sums over its heads: in halves 87 us in 3 a CU, 92 in
 // 8; interleaved 86 in 5, 98 in 3; heads of 96 with 24 rotated 100 in 5, 132 in 3.
 constexpr int kMostSummed = 5;
