@@ -342,8 +342,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     return;
   }
   k_low &= ~15;
+  // (nsplit runs reach over max_len slots from 0 on: from k_low on they may end past 2^31)
+  if (int64_t(sp) * a.chunk >= k_high - k_low) return;
   const int k0 = k_low + sp * a.chunk;
-  if (k0 >= k_high) return;
   // what is needed after the tiles
   __shared__ int saved[4];
   if (threadIdx.x == 0) {
