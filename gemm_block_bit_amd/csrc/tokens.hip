@@ -312,26 +312,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   const bool some = top > bottom;
   const int lo_wave = uniform(wave_min(some ? bottom : INT_MAX)), hi_wave = uniform(wave_max(some ? top : 0));
   const int lo_all = uniform(wave_max(real ? lo : 0)), hi_all = uniform(wave_min(real ? hi : INT_MAX));   // all its rows see these
-  __shared__ int range[4 * NW];
+  __shared__ int range[2 * NW];
   if (lane == 0) {
-    range[4 * wave] = lo_wave;
-    range[4 * wave + 1] = hi_wave;
-    range[4 * wave + 2] = lo_all;
-    range[4 * wave + 3] = hi_all;
+    range[2 * wave] = lo_wave;
+    range[2 * wave + 1] = hi_wave;
   }
   __syncthreads();
-  int k_low = range[0], k_high = range[1], same_low = range[2], same_high = range[3];
+  int k_low = range[0], k_high = range[1];
 #pragma unroll
   for (int i = 1; i < NW; ++i) {
-    k_low = min(k_low, range[4 * i]);
-    k_high = max(k_high, range[4 * i + 1]);
-    same_low = max(same_low, range[4 * i + 2]);
-    same_high = min(same_high, range[4 * i + 3]);
+    k_low = min(k_low, range[2 * i]);
+    k_high = max(k_high, range[2 * i + 1]);
   }
   k_low = uniform(k_low);
   k_high = uniform(k_high);
-  same_low = uniform(same_low);                // all rows of the workgroup see the slots from
-  same_high = uniform(same_high);              // same_low up to same_high
   if (k_low >= k_high) {                       // no row sees a slot
     if (sp == 0 && real) {
       const size_t head = size_t(t) * a.Hq + hq;
@@ -443,18 +437,21 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
     widened(kr, lds + (i & 1) * TILE, k_swizzle);
     widened(vr, lds + (2 + (i & 1)) * TILE, v_swizzle);
   };
-  // A slot that some rows see and some do not may hold infinities or NaN: with
-  // a weight of 0 they would reach the rows that do not see it.  So they are
-  // left out of the product, and what they do to the rows that see them is found
-  // by products with 1 in the place of infinities of each sign and of NaN.
+  // V may hold infinities or NaN.  In the products they become NaN at a weight of
+  // 0 (of rows that do not see the slot, or whose weight rounds to 0), and at one
+  // given in two operands, of which the second is 0 or negative.  So a workgroup
+  // whose output is not finite after its tiles, which is rare, goes over them
+  // again with care: such elements are left out of the product, and what they do to
+  // the rows that see them is found by products with 1 in the place of infinities of
+  // each sign and of NaN.
   constexpr uint32_t EXP = DT == GBB_F16 ? 0x7c00u : 0x7f80u, ONE = DT == GBB_F16 ? 0x3c00u : 0x3f80u;
   const auto elements = [](u32x4 x, auto f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = f(x[i] & 0xffffu) | f(x[i] >> 16) << 16;
     return x;
   };
-  const auto mixed = [&](int i) { return k0 + i * BN < same_low || min(k0 + i * BN + BN, k1) > same_high; };
   __shared__ int odd_tile;                     // the last tile that has such elements
+  __shared__ bool again;                       // the tiles are gone over again
   // f of every 16 bytes of V's tile i, in place where f says so
   const auto each_piece = [&](int i, auto f) {
 #pragma unroll 1
@@ -497,224 +494,246 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
   };
 
   f32x16 o[NT];
+  float ref, l;
+  bool careful = false;
+  if (threadIdx.x == 0) again = false;
+#pragma unroll 1
+  for (;;) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-  float ref = -FLT_MAX, l = 0.f;
+    for (int i = 0; i < NT; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    ref = -FLT_MAX;
+    l = 0.f;
 
-  if (threadIdx.x == 0) odd_tile = -1;
-  uint32_t holes_next = fetch(0);
+    if (threadIdx.x == 0) odd_tile = -1;
+    uint32_t holes_next = fetch(0);
 #pragma unroll 1
-  for (int i = 0; i < nt; ++i) {
-    // tile i is in LDS for all waves, and all are done with the one before
-    if (F8) widen_tile(i);
-    else loads_left<0>();
-    __syncthreads();
-    if (mixed(i)) clean(i);
-    const uint32_t holes = holes_next;
-    if (i + 1 < nt) holes_next = fetch(i + 1);
-    const int key0 = k0 + i * BN, buffer = (i & 1) * TILE;
-    const bool works = key0 < hi_wave && key0 + BN > lo_wave;
-    uint32_t v_pieces[VA];
+    for (int i = 0; i < nt; ++i) {
+      // tile i is in LDS for all waves, and all are done with the one before
+      if (F8) widen_tile(i);
+      else loads_left<0>();
+      __syncthreads();
+      if (careful) clean(i);
+      const uint32_t holes = holes_next;
+      if (i + 1 < nt) holes_next = fetch(i + 1);
+      const int key0 = k0 + i * BN, buffer = (i & 1) * TILE;
+      const bool works = key0 < hi_wave && key0 + BN > lo_wave;
+      uint32_t v_pieces[VA];
 #pragma unroll
-    for (int u = 0; u < VA; ++u) v_pieces[u] = (v_at + buffer) ^ (u * 64);
-    f32x16 s[NE];
-    if (works) {
-      uint32_t k_pieces[KA];
+      for (int u = 0; u < VA; ++u) v_pieces[u] = (v_at + buffer) ^ (u * 64);
+      f32x16 s[NE];
+      if (works) {
+        uint32_t k_pieces[KA];
 #pragma unroll
-      for (int u = 0; u < KA; ++u) k_pieces[u] = (k_at + buffer) ^ (u * 32);
-      unrolled<NE>([&](auto E) {
-        constexpr int e = decltype(E)::value;
-        s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-        unrolled<KC / 4>([&](auto G) {
-          constexpr int kc = 4 * decltype(G)::value;
-          u32x4 x[4];
-          read4<e * 32 * ROW + kc / KA * 256>(x, k_pieces + kc % KA);
+        for (int u = 0; u < KA; ++u) k_pieces[u] = (k_at + buffer) ^ (u * 32);
+        unrolled<NE>([&](auto E) {
+          constexpr int e = decltype(E)::value;
+          s[e] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          unrolled<KC / 4>([&](auto G) {
+            constexpr int kc = 4 * decltype(G)::value;
+            u32x4 x[4];
+            read4<e * 32 * ROW + kc / KA * 256>(x, k_pieces + kc % KA);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) s[e] = H::mfma32(__builtin_bit_cast(V8, x[u]), qf[kc + u], s[e]);
+            for (int u = 0; u < 4; ++u) s[e] = H::mfma32(__builtin_bit_cast(V8, x[u]), qf[kc + u], s[e]);
+          });
         });
-      });
-    }
-    V8 part[PARTS][BN / 16];
-    if (works) {
-      // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
-      const int key = key0 + 4 * h;
-      const auto slot = [](int e, int r) { return 32 * e + 8 * (r / 4) + r % 4; };
-      // scores are s times unit plus offset
-      float unit = scale, offset = 0.f;
-      const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
-      // With a tree: bit j of the slot key0 + j that is a new token which the row's
-      // tree has, and how many of those lie behind the tile.
-      const bool branches = TREE && key0 + BN > ctx;
-      uint64_t bits = 0;
-      int beyond = 0;
-      if (branches && real) {
-        const int from = key0 - ctx, i0 = from >> 5, end = from + BN;   // end above 0
-        uint32_t x[3];
-#pragma unroll
-        for (int u = 0; u < 3; ++u) x[u] = tree_word(i0 + u);
-        const uint64_t low = uint64_t(x[1]) << 32 | x[0], high = uint64_t(x[2]) << 32 | x[1];
-        const int shift = from & 31;
-        bits = (low >> shift & 0xffffffffu) | (high >> shift) << 32;
-        if (BN == 32) bits &= 0xffffffffu;
-        beyond = drafted;
-        for (int i = 0; 32 * i < end; ++i) beyond -= __popc(tree_word(i) & uint32_t(below(end - 32 * i)));
       }
-      // (The usual shapes each in one branch of their own: where branches follow
-      // each other the scores are copied in those that are not taken, 64 and more
-      // registers a tile.)
-      const auto cap_short = [&](float x) {    // tanh(x / cap) / 2 - 1 / 2 = -1 / (1 + e^(2 x / cap))
-        return __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x * (scale * over * (2.f * kLog2e))));
-      };
-      if (shape == SHORT_CAP) {
-        unit = 2.f * a.cap;
-        offset = a.cap;
+      V8 part[PARTS][BN / 16];
+      if (works) {
+        // slot of register r of s[e]: key + 32 e + 8 (r / 4) + r % 4
+        const int key = key0 + 4 * h;
+        const auto slot = [](int e, int r) { return 32 * e + 8 * (r / 4) + r % 4; };
+        // scores are s times unit plus offset
+        float unit = scale, offset = 0.f;
+        const bool whole = key0 >= lo_all && key0 + BN <= min(hi_all, k1) && !holes;
+        // With a tree: bit j of the slot key0 + j that is a new token which the row's
+        // tree has, and how many of those lie behind the tile.
+        const bool branches = TREE && key0 + BN > ctx;
+        uint64_t bits = 0;
+        int beyond = 0;
+        if (branches && real) {
+          const int from = key0 - ctx, i0 = from >> 5, end = from + BN;   // end above 0
+          uint32_t x[3];
 #pragma unroll
-        for (int e = 0; e < NE; ++e)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[e][r] = cap_short(s[e][r]);
-      } else if (shape == BIAS && key0 + BN <= place_low + 1) {   // no slot lies ahead of a row
-        const float base = -slope * float(place - key);
-        unit = 1.f;
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            s[e][r] = __builtin_fmaf(s[e][r], scale, __builtin_fmaf(slope, float(slot(e, r)), base));
-      } else if (shape != PLAIN) {
-        unit = 1.f;
-        if (a.cap > kShortCap * kLog2e) {
+          for (int u = 0; u < 3; ++u) x[u] = tree_word(i0 + u);
+          const uint64_t low = uint64_t(x[1]) << 32 | x[0], high = uint64_t(x[2]) << 32 | x[1];
+          const int shift = from & 31;
+          bits = (low >> shift & 0xffffffffu) | (high >> shift) << 32;
+          if (BN == 32) bits &= 0xffffffffu;
+          beyond = drafted;
+          for (int i = 0; 32 * i < end; ++i) beyond -= __popc(tree_word(i) & uint32_t(below(end - 32 * i)));
+        }
+        // (The usual shapes each in one branch of their own: where branches follow
+        // each other the scores are copied in those that are not taken, 64 and more
+        // registers a tile.)
+        const auto cap_short = [&](float x) {    // tanh(x / cap) / 2 - 1 / 2 = -1 / (1 + e^(2 x / cap))
+          return __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x * (scale * over * (2.f * kLog2e))));
+        };
+        if (shape == SHORT_CAP) {
+          unit = 2.f * a.cap;
+          offset = a.cap;
 #pragma unroll
           for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r] * scale, over, a.cap);
-        } else if (a.cap > 0.f) {
+            for (int r = 0; r < 16; ++r) s[e][r] = cap_short(s[e][r]);
+        } else if (shape == BIAS && key0 + BN <= place_low + 1) {   // no slot lies ahead of a row
+          const float base = -slope * float(place - key);
+          unit = 1.f;
 #pragma unroll
           for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[e][r] = __builtin_fmaf(2.f * a.cap, cap_short(s[e][r]), a.cap);
-        } else {
+            for (int r = 0; r < 16; ++r)
+              s[e][r] = __builtin_fmaf(s[e][r], scale, __builtin_fmaf(slope, float(slot(e, r)), base));
+        } else if (shape != PLAIN) {
+          unit = 1.f;
+          if (a.cap > kShortCap * kLog2e) {
 #pragma unroll
-          for (int e = 0; e < NE; ++e) s[e] *= scale;
-        }
-        if (a.slopes) {
-          const float from = float(place - key);
+            for (int e = 0; e < NE; ++e)
 #pragma unroll
-          for (int e = 0; e < NE; ++e)
+              for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r] * scale, over, a.cap);
+          } else if (a.cap > 0.f) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              float far = fabsf(from - float(slot(e, r)));
-              if (branches && key + slot(e, r) >= ctx)
-                far = float(beyond + __popcll(bits >> (4 * h) >> slot(e, r) >> 1));
-              s[e][r] = __builtin_fmaf(-slope, far, s[e][r]);
-            }
-        }
-      }
-      if (!whole) {
-        // bit j: the row sees the slot key0 + j
-        uint64_t seen = below(min(hi, k1) - key0) & ~below(lo - key0);
-        if (branches) {
-          uint64_t x = bits;
-          if (a.window)   // the nearest ones: those with fewer behind them
-            for (int more = beyond + __popcll(x) - a.window; more > 0 && x; --more) x &= x - 1;
-          seen |= x & below(k1 - key0) & ~below(first - key0);
-        }
-        if (holes) {
+            for (int e = 0; e < NE; ++e)
 #pragma unroll
-          for (int g = 0; g < BN / 16; ++g)
-            if (holes >> g & 1u) seen &= ~(uint64_t(0xffff) << (16 * g));
-        }
-        seen >>= 4 * h;
-        const uint32_t part[2] = {uint32_t(seen), uint32_t(seen >> 32)};
+              for (int r = 0; r < 16; ++r) s[e][r] = __builtin_fmaf(2.f * a.cap, cap_short(s[e][r]), a.cap);
+          } else {
 #pragma unroll
-        for (int e = 0; e < NE; ++e)
+            for (int e = 0; e < NE; ++e) s[e] *= scale;
+          }
+          if (a.slopes) {
+            const float from = float(place - key);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[e][r] = part[e] >> slot(0, r) & 1u ? s[e][r] : -INFINITY;
-      }
-      float mx = -INFINITY;
+            for (int e = 0; e < NE; ++e)
 #pragma unroll
-      for (int e = 0; e < NE; ++e)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) mx = fmaxf(fmaxf(s[e][r], s[e][r + 1]), mx);
-      mx = __builtin_fmaf(row_max(mx), unit, offset);
-      if (__any(mx > ref + kLimit)) {
-        const float to = mx > ref + kLimit ? mx - kShift : ref, f = __builtin_amdgcn_exp2f(ref - to);
-        ref = to;
-        l *= f;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) o[j] *= f;
-      }
-      const float under = offset - ref;
-      // 16 slots at a time, so that exponentials are taken while the products
-      // of those before are formed
-      unrolled<BN / 16>([&](auto S) {
-        constexpr int t = decltype(S)::value;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + r], unit, under));
-          l += p;
-#pragma unroll
-          for (int x = 0; x < PARTS; ++x) {
-            const T y = T(p);
-            part[x][t][r] = y;
-            p -= float(y);   // exact
+              for (int r = 0; r < 16; ++r) {
+                float far = fabsf(from - float(slot(e, r)));
+                if (branches && key + slot(e, r) >= ctx)
+                  far = float(beyond + __popcll(bits >> (4 * h) >> slot(e, r) >> 1));
+                s[e][r] = __builtin_fmaf(-slope, far, s[e][r]);
+              }
           }
         }
-        each_v(v_pieces, S, [&](int j, const V8& x) {
+        if (!whole) {
+          // bit j: the row sees the slot key0 + j
+          uint64_t seen = below(min(hi, k1) - key0) & ~below(lo - key0);
+          if (branches) {
+            uint64_t x = bits;
+            if (a.window)   // the nearest ones: those with fewer behind them
+              for (int more = beyond + __popcll(x) - a.window; more > 0 && x; --more) x &= x - 1;
+            seen |= x & below(k1 - key0) & ~below(first - key0);
+          }
+          if (holes) {
 #pragma unroll
-          for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][t], o[j]);
-        });
-      });
-    }
-    if (mixed(i) && uniform(odd_tile) == i) {
-      // rare: infinities of either sign, from V as memory has it
-      const int p = page_of(key0 + 16 * min(lane, BN / 16 - 1));
-#pragma unroll 1
-      for (int negative = 0; negative < 2; ++negative) {
-        __syncthreads();
-#pragma unroll 1
-        for (int r = wave * 16; r < BN; r += 16 * NW) {        // 16 slots of a page a wave
-          const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + r;
-          const bool there = unsigned(page) < unsigned(late_args()->num_pages);
-          const size_t off = place_of_slot(there ? page : 0, slot);
-          const Span from = span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0));
-#pragma unroll 1
-          for (int q = lane; q < 16 * (D / 8); q += 64) {      // a piece of 8 elements a lane
-            const int row = q / (D / 8), piece = q % (D / 8);
-            u32x4 x;
-            if constexpr (F8) {
-              const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(from, row * GROW + piece * 8, 0, 0);
-              x = u32x4{H::template widen<false>(y[0]), H::template widen<true>(y[0]),
-                        H::template widen<false>(y[1]), H::template widen<true>(y[1])};
-            } else {
-              x = __builtin_amdgcn_raw_buffer_load_b128(from, row * GROW + piece * 16, 0, 0);
-            }
-            x = elements(x, [=](uint32_t e) {   // 1 where an element is an infinity of that sign or NaN
-              return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
-            });
-            st16(lds + 2 * TILE + buffer + (r + row) * ROW + (piece ^ v_swizzle(r + row)) * 16, x);
+            for (int g = 0; g < BN / 16; ++g)
+              if (holes >> g & 1u) seen &= ~(uint64_t(0xffff) << (16 * g));
+          }
+          seen >>= 4 * h;
+          const uint32_t part[2] = {uint32_t(seen), uint32_t(seen >> 32)};
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[e][r] = part[e] >> slot(0, r) & 1u ? s[e][r] : -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) mx = fmaxf(fmaxf(s[e][r], s[e][r + 1]), mx);
+        mx = __builtin_fmaf(row_max(mx), unit, offset);
+        if (__any(mx > ref + kLimit)) {
+          const float to = mx > ref + kLimit ? mx - kShift : ref, f = __builtin_amdgcn_exp2f(ref - to);
+          ref = to;
+          l *= f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (careful && f == 0.f)           // what an infinity added so far has no weight any more
+              o[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            o[j] *= f;
           }
         }
-        __syncthreads();
-        if (works) {
+        const float under = offset - ref;
+        // 16 slots at a time, so that exponentials are taken while the products
+        // of those before are formed
+        unrolled<BN / 16>([&](auto S) {
+          constexpr int t = decltype(S)::value;
 #pragma unroll
-          for (int j0 = 0; j0 < NT; j0 += VG) {
-            f32x16 hit[VG];
+          for (int r = 0; r < 8; ++r) {
+            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + r], unit, under));
+            l += p;
 #pragma unroll
-            for (int j = 0; j < VG; ++j) hit[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-            unrolled<BN / 16>([&](auto S) {
-              each_v(v_pieces, S, [&](int j, const V8& x) {
-                if (j >= j0 && j < j0 + VG) hit[j - j0] = H::mfma32(x, part[0][decltype(S)::value], hit[j - j0]);
+            for (int x = 0; x < PARTS; ++x) {
+              const T y = T(p);
+              part[x][t][r] = y;
+              p -= float(y);   // exact
+            }
+          }
+          each_v(v_pieces, S, [&](int j, const V8& x) {
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) o[j] = H::mfma32(x, part[u][t], o[j]);
+          });
+        });
+      }
+      if (careful && uniform(odd_tile) == i) {
+        // rare: infinities of either sign, from V as memory has it
+        const int p = page_of(key0 + 16 * min(lane, BN / 16 - 1));
+#pragma unroll 1
+        for (int negative = 0; negative < 2; ++negative) {
+          __syncthreads();
+#pragma unroll 1
+          for (int r = wave * 16; r < BN; r += 16 * NW) {        // 16 slots of a page a wave
+            const int page = __builtin_amdgcn_readlane(p, r >> 4), slot = key0 + r;
+            const bool there = unsigned(page) < unsigned(late_args()->num_pages);
+            const size_t off = place_of_slot(there ? page : 0, slot);
+            const Span from = span(a.v + off, uniform(there ? max(0, min(k1 - slot, 16)) * GROW : 0));
+#pragma unroll 1
+            for (int q = lane; q < 16 * (D / 8); q += 64) {      // a piece of 8 elements a lane
+              const int row = q / (D / 8), piece = q % (D / 8);
+              u32x4 x;
+              if constexpr (F8) {
+                const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(from, row * GROW + piece * 8, 0, 0);
+                x = u32x4{H::template widen<false>(y[0]), H::template widen<true>(y[0]),
+                          H::template widen<false>(y[1]), H::template widen<true>(y[1])};
+              } else {
+                x = __builtin_amdgcn_raw_buffer_load_b128(from, row * GROW + piece * 16, 0, 0);
+              }
+              x = elements(x, [=](uint32_t e) {   // 1 where an element is an infinity of that sign or NaN
+                return (e & EXP) == EXP && ((e & 0x7fffu) != EXP || int(e >> 15) == negative) ? ONE : 0u;
               });
-            });
+              st16(lds + 2 * TILE + buffer + (r + row) * ROW + (piece ^ v_swizzle(r + row)) * 16, x);
+            }
+          }
+          __syncthreads();
+          if (works) {
 #pragma unroll
-            for (int j = 0; j < VG; ++j)
+            for (int j0 = 0; j0 < NT; j0 += VG) {
+              f32x16 hit[VG];
 #pragma unroll
-              for (int r = 0; r < 16; ++r)
-                if (hit[j][r] > 0.f) o[j0 + j][r] += negative ? -INFINITY : INFINITY;
+              for (int j = 0; j < VG; ++j) hit[j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+              unrolled<BN / 16>([&](auto S) {
+                each_v(v_pieces, S, [&](int j, const V8& x) {
+                  if (j >= j0 && j < j0 + VG) hit[j - j0] = H::mfma32(x, part[0][decltype(S)::value], hit[j - j0]);
+                });
+              });
+#pragma unroll
+              for (int j = 0; j < VG; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                  if (hit[j][r] > 0.f) o[j0 + j][r] += negative ? -INFINITY : INFINITY;
+            }
           }
         }
       }
     }
+
+    if (careful) break;
+    f32x4 odd = {0, 0, 0, 0};                    // 0, or NaN where an output is not finite
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) odd[r % 4] = __builtin_fmaf(o[j][r], 0.f, odd[r % 4]);
+    if (__any(odd[0] + odd[1] + odd[2] + odd[3] != 0.f)) again = true;
+    __syncthreads();                             // all are done with the tiles
+    careful = uniform(again);
+    if (!careful) break;
   }
 
   l = row_sum(l);
@@ -811,7 +830,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args 
         for (int i = 0; i < 4 * NT; ++i) {
           const f32x4 y = __builtin_bit_cast(f32x4, pieces[u][i]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[i / 4][4 * (i % 4) + r] = __builtin_fmaf(f, y[r], o[i / 4][4 * (i % 4) + r]);
+          for (int r = 0; r < 4; ++r)          // (an infinity at a weight of 0 is none)
+            o[i / 4][4 * (i % 4) + r] = __builtin_fmaf(f, f == 0.f ? 0.f : y[r], o[i / 4][4 * (i % 4) + r]);
         }
       }
   }
@@ -863,7 +883,8 @@ __global__ __launch_bounds__(64) void join_kernel(Args a, int rows) {
         const float f = __builtin_amdgcn_exp2f(e[u].x - high);
         l += f * e[u].y;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = __builtin_fmaf(f, pieces[u][i / 4][i % 4], sum[i]);
+        for (int i = 0; i < 16; ++i)           // (an infinity at a weight of 0 is none)
+          sum[i] = __builtin_fmaf(f, f == 0.f ? 0.f : pieces[u][i / 4][i % 4], sum[i]);
       }
   }
   const int token = row / a.G;
