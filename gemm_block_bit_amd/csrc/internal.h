@@ -209,6 +209,7 @@ int launch_attend(const gbb_paged_cache& c, const AttendArgs& a, const AttendPla
 // `chunk` slots.
 struct TokensPlan {
   int waves, rows, tiles;   // waves of 32 rows each a workgroup; row tiles of all sequences, at most
+  int parts;                // 16-bit operands that probabilities are given in
   int chunk, nsplit;
   bool second;              // the runs are joined by a second launch
   size_t notes_off, ml_off, o_off, ws_bytes;

@@ -37,13 +37,13 @@
 // of 64 343, of 256 900; e4m3 617.  Through registers and LDS writes the plain
 // one took 621, with waits before every load to LDS 780.
 //
-// P is rounded to 16 bits for the matrix cores, once in workgroups of four
-// waves, where the products bound the call (a second operand for what the
-// rounding drops would take half as long again): an output is off by at most
+// P is rounded to 16 bits for the matrix cores, once where a sequence has more
+// than 128 rows, so that the products bound the call (a second operand for what the
+// rounding drops takes a third as long again): an output is off by at most
 // half a step of its type relative to sum p |v|, beside its own rounding.  The
 // sum that divides the output, and makes lse, is of P before that, in fp32.
-// With two waves the cache's bytes bound the call, and P is given in two
-// operands (22 bits in fp16, 16 in bf16).
+// With fewer rows the cache's bytes and the steps that wait for each other bound the
+// call, and P is given in two operands (22 bits in fp16, 16 in bf16).
 //
 // Where there are few row tiles the slots are split over workgroups; partial
 // results (maximum, sum, unnormalised output, fp32) go to the workspace, and
@@ -189,13 +189,12 @@ __device__ __forceinline__ LateArgs late_args() {
   return reinterpret_cast<LateArgs>(p);
 }
 
-template <int DT, int CT, int D, int NW, bool TREE>
+template <int DT, int CT, int D, int NW, int PARTS, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void tokens_kernel(Args a) {
   typedef Half<DT> H;
   typedef typename H::T T;
   typedef typename H::V8 V8;
   constexpr bool F8 = CT == GBB_E4M3;
-  constexpr int PARTS = NW == 4 ? 1 : 2;
   constexpr int THREADS = 64 * NW, ROWS = 32 * NW, BN = tile_slots(D, NW);
   constexpr int ROW = 2 * D;                  // bytes of a slot in LDS
   constexpr int GROW = F8 ? D : 2 * D;        // and in memory
@@ -904,20 +903,21 @@ __global__ __launch_bounds__(64) void join_kernel(Args a, int rows) {
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int DT, int CT, int D, bool TREE>
-void run_waves(const Args& a, int waves, unsigned grid, hipStream_t s) {
-  if (waves == 4) start((tokens_kernel<DT, CT, D, 4, TREE>), dim3(grid), dim3(256), s, a);
-  else start((tokens_kernel<DT, CT, D, 2, TREE>), dim3(grid), dim3(128), s, a);
+void run_waves(const Args& a, const TokensPlan& p, unsigned grid, hipStream_t s) {
+  if (p.waves == 2) start((tokens_kernel<DT, CT, D, 2, 2, TREE>), dim3(grid), dim3(128), s, a);
+  else if (p.parts == 2) start((tokens_kernel<DT, CT, D, 4, 2, TREE>), dim3(grid), dim3(256), s, a);
+  else start((tokens_kernel<DT, CT, D, 4, 1, TREE>), dim3(grid), dim3(256), s, a);
 }
 template <int DT, int CT, int D>
-void run(const Args& a, int waves, unsigned grid, hipStream_t s) {
-  if (a.tree) run_waves<DT, CT, D, true>(a, waves, grid, s);
-  else run_waves<DT, CT, D, false>(a, waves, grid, s);
+void run(const Args& a, const TokensPlan& p, unsigned grid, hipStream_t s) {
+  if (a.tree) run_waves<DT, CT, D, true>(a, p, grid, s);
+  else run_waves<DT, CT, D, false>(a, p, grid, s);
 }
 template <int DT, int CT>
-void run_dim(const Args& a, int D, int waves, unsigned grid, hipStream_t s) {
-  if (D == 64) run<DT, CT, 64>(a, waves, grid, s);
-  else if (D == 128) run<DT, CT, 128>(a, waves, grid, s);
-  else run<DT, CT, 256>(a, waves, grid, s);
+void run_dim(const Args& a, int D, const TokensPlan& p, unsigned grid, hipStream_t s) {
+  if (D == 64) run<DT, CT, 64>(a, p, grid, s);
+  else if (D == 128) run<DT, CT, 128>(a, p, grid, s);
+  else run<DT, CT, 256>(a, p, grid, s);
 }
 template <int DT>
 void run_join(const Args& a, int D, int rows, hipStream_t s) {
@@ -939,6 +939,13 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   // slots, 8 tokens of 32 / 8 heads each: 130 us, 146 with four; with few, four
   // stage a tile in half the time: 1 of 4000, 2 tokens: 29 and 23.5).
   p.waves = rows <= int64_t(64) * B && 2 * int64_t(B) * c.kv_heads >= cus ? 2 : 4;
+  // Operands of P: one where the products bound the call.  A slot's K and V are 4 D
+  // bytes in 16 bits, and a row takes 4 D operations, 6 D with two operands: up to 128
+  // rows, a row tile, are 192 operations a byte, where this card's rates balance at 236.
+  // (With two a tree of 25 behind 4000, 32 / 8 heads, takes 24.4 us, 23.1 with one, and 2
+  // tokens behind 4000 20 and 18.3: there verifying a draft has the bits of decoding
+  // it.  A prompt of 8192 takes 768 with two and 584 with one, 16 trees of 64 347 and 276.)
+  p.parts = rows <= int64_t(128) * B ? 2 : 1;
   p.rows = 32 * p.waves;
   p.tiles = int(std::min<int64_t>(rows / p.rows + B, INT_MAX));
   // slots from the first to the last that a row tile may see
@@ -1030,11 +1037,11 @@ int launch_tokens(const gbb_paged_cache& c, const TokensArgs& x, const TokensPla
   const unsigned grid = unsigned(p.tiles) * unsigned(c.kv_heads) * unsigned(p.nsplit);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (x.dtype == GBB_F16) {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p.waves, grid, s);
-    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p.waves, grid, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_F16, GBB_E4M3>(a, c.head_dim, p, grid, s);
+    else run_dim<GBB_F16, GBB_F16>(a, c.head_dim, p, grid, s);
   } else {
-    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p.waves, grid, s);
-    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p.waves, grid, s);
+    if (c.dtype == GBB_E4M3) run_dim<GBB_BF16, GBB_E4M3>(a, c.head_dim, p, grid, s);
+    else run_dim<GBB_BF16, GBB_BF16>(a, c.head_dim, p, grid, s);
   }
   if (p.second) {
     if (c.dtype != GBB_E4M3) a.v_scale = nullptr;

@@ -695,6 +695,10 @@ gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, const void*
  *   workspace  16-byte aligned, of gbb_paged_attention_tokens_workspace bytes
  *              (for the same options' window and tree_words, 0 without a
  *              tree); to be had and shared as that of gbb_paged_attention.
+ * Sums, maxima and lse are fp32.  Probabilities are rounded to `dtype` once
+ * where T * q_heads / kv_heads is above 128 B (an output is then off by up to
+ * half a step of `dtype` relative to sum p |v|, beside its own rounding), and
+ * carry twice its bits in other calls.
  * T = 0 or B = 0 is a no-op.  Results do not depend on the order of execution.
  * Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN, GBB_E_SPACE, GBB_E_DEVICE. */
 size_t gbb_paged_attention_tokens_workspace(const gbb_paged_cache* cache, int T, int B, int q_heads, int max_len,
