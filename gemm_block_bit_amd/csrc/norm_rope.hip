@@ -18,9 +18,10 @@
 // cache the second time.
 //
 // dw needs a sum over all heads: a workgroup keeps its own over the tokens it
-// takes (in registers; fp32, at most some hundred terms each), writes it to
-// the workspace, and a second launch adds the workgroups' in their order, so
-// it is the same bits each time.
+// takes (in registers; fp32, one chain a lane and element: 22 terms for 16384 x 32
+// heads of 128, some 20 000 for the most tokens that a call takes, 2^22 x 64 heads of
+// 256), writes it to the workspace, and a second launch adds the workgroups' in their
+// order, so it is the same bits each time.
 //
 // A workgroup takes several tokens, and loads a head's elements and angles while
 // the one before is worked on: one token each waits for its place, angles and
@@ -711,7 +712,7 @@ int launch_norm_append(const gbb_paged_cache& c, const NormAppendArgs& a, void* 
   const bool half = a.r.layout == GBB_ROPE_HALF;
   int E = unit_elements(2, a.r.rot, c.head_dim, half, address(a.qkv), address(a.q_weight) | address(a.k_weight),
                         a.wide_weight ? 4 : 2);
-  if (E < 8) E = half ? 1 : 2;
+  if (E < 8) E = half ? 1 : 2;   // (heads whose parts are no multiple of 8 are few: no kernels of their own between)
   bool one;
   const Spread s = spread(a.Hq + 2 * c.kv_heads, c.head_dim, a.r.rot, a.r.layout, E, one);
   const dim3 grid = grid_of(s, a.T, a.Hq + 2 * c.kv_heads, appending(half, E));

@@ -33,9 +33,10 @@
 // exponential and a reciprocal; the tiles' reads from LDS (each wave reads all
 // of K and V) come third.  Measured, 32 query over 8 kv heads of 128, bf16, a
 // prompt of 8192 tokens (550e9 operations, 456 us at the rate of a large
-// product): 575 to 600 us, with a bias 636 to 660, with a cap 688 to 713; heads
-// of 64 343, of 256 900; e4m3 617.  Through registers and LDS writes the plain
-// one took 621, with waits before every load to LDS 780.
+// product): 584 to 612 us, with a bias 670 to 710, with a cap 717 to 754; as many
+// heads of 64 (275e9) 346 to 364, 16 over 4 of 256 (550e9) 867 to 873, 32 over 8 of
+// 256 1720; e4m3 592 to 629.  Through registers and LDS writes the plain one took
+// 621, with waits before every load to LDS 780.
 //
 // P is rounded to 16 bits for the matrix cores, once where a sequence has more
 // than 128 rows, so that the products bound the call (a second operand for what the
@@ -960,12 +961,13 @@ TokensPlan tokens_plan(const gbb_paged_cache& c, int T, int B, int Hq, int max_l
   // 256 to 2048 slots, which a second launch joins, on more CUs but some 4 us later: a
   // tree of 25 behind 4000 takes 22.5 us in runs of 256, 24 in 192, 28 in runs of 384
   // that the last workgroup joins; 64 tokens behind 65536 take 121, 136 with three a
-  // CU, 143 joined by the last; 300 x 4 behind up to 4000 52, 59 with four a CU, 66.
+  // CU, 143 joined by the last; 4 sequences of 300 tokens behind up to 4000 each 52, 59
+  // with four a CU, 66 joined by the last (all with one operand of P).
   // Where that makes one or two runs, of at least 384, and no second launch (256
   // tokens 14, 17 with one).  With more tiles, a single sequence's balance by
   // themselves, since those that see most start first; those of several may be of
-  // any length: runs of up to 4096 (16 trees of 64 behind up to 16384: 283 us, whole
-  // 500; behind 8192 each 354 and 337).
+  // any length: runs of up to 4096 (32 trees of 64, 32 / 8 heads, bf16, behind up to
+  // 16384: 332 us, whole 443; behind 8192 each 399 and 371).
   const int64_t groups = int64_t(p.tiles) * c.kv_heads;
   int64_t chunk = most;
   bool second = false;

@@ -523,7 +523,8 @@ size_t gbb_paged_attention_workspace(const gbb_paged_cache* cache, int B, int q_
  * out = sum_j p_j v_j, p_j = exp(s_j) / sum_j exp(s_j); fp32 sums, one
  * rounding of out.  A sequence of length 0 gives zeros (so does a head
  * whose scores are all -inf).  Memory past the length is never used, so it
- * may hold anything, NaN included.
+ * may hold anything, NaN included.  An infinity of v among the slots may come
+ * out as NaN (weights go into the product in two or three parts).
  *   q, out     device [B][q_heads][head_dim] of `dtype` (GBB_F16 or
  *              GBB_BF16; the cache's dtype or a GBB_E4M3 cache); sequence b
  *              of q is at b * q_token elements.
@@ -698,7 +699,8 @@ gbb_status gbb_paged_attention_options(const gbb_paged_cache* cache, const void*
  * Sums, maxima and lse are fp32.  Probabilities are rounded to `dtype` once
  * where T * q_heads / kv_heads is above 128 B (an output is then off by up to
  * half a step of `dtype` relative to sum p |v|, beside its own rounding), and
- * carry twice its bits in other calls.
+ * carry twice its bits in other calls.  A capped score, and so lse, is off by up
+ * to 2^-21 of a softcap of up to 80, whatever the score's size.
  * T = 0 or B = 0 is a no-op.  Results do not depend on the order of execution.
  * Errors: GBB_E_ARG, GBB_E_SHAPE, GBB_E_ALIGN, GBB_E_SPACE, GBB_E_DEVICE. */
 size_t gbb_paged_attention_tokens_workspace(const gbb_paged_cache* cache, int T, int B, int q_heads, int max_len,
